@@ -234,9 +234,15 @@ def _round_to_codes(x, scale):
     return (x.double() / scale.double()).round_().clamp_(-127, 127).to(torch.int8)
 
 
+def _a_127th(peak):
+    """peak / 127 rounded to 32 bits. (Divided by a plain number, a 32-bit tensor
+    is multiplied by the number's rounded reciprocal.)"""
+    return (peak.double() / 127).float()
+
+
 def _plain_quantize(s):
     x = s["x"].float()
-    scale = x.abs().amax(1) / 127
+    scale = _a_127th(x.abs().amax(1))
     scale = torch.where(scale > 0, scale, 1.0)
     return _round_to_codes(x, scale[:, None]), scale
 
@@ -284,7 +290,7 @@ def _plain_store_one(s, x, codes, scales, by_token):
     held.index_reduce_(0, s["table"].gather(1, (before // BT).clamp(max=s["width"] - 1)[:, None])
                        .view(-1).clamp(min=0).long(), before % BT, "amax")
     held = torch.where(touched, held, 0)
-    new = torch.maximum(peak / 127, torch.where(held[:, None] > 0, scales, 0.0))
+    new = torch.maximum(_a_127th(peak), torch.where(held[:, None] > 0, scales, 0.0))
     new = torch.where(new > 0, new, 1.0)
     new = torch.where(touched[:, None], new, scales)
     out = codes.clone() if by_token else codes.transpose(2, 3).contiguous()
@@ -391,8 +397,8 @@ def exact(case, seed):
     if kind == "quantize":
         codes, scales = [], []
         for rows in s["x"].split(1024):
-            top = rows.abs().max(dim=1).values.float()
-            scale = torch.where(top > 0, top / 127.0, torch.ones_like(top))  # held in 32 bits
+            top = (rows.abs().max(dim=1).values.double() / 127.0).float()  # held in 32 bits
+            scale = torch.where(top > 0, top, torch.ones_like(top))
             ratio = rows.double() / scale.double().unsqueeze(1)
             codes.append(torch.round(ratio).clamp(-127, 127).to(torch.int8))
             scales.append(scale.double())
@@ -430,7 +436,7 @@ def exact(case, seed):
                 while len(x):
                     b, at = table[i][p // BT], p % BT
                     part, x = x[:BT - at], x[BT - at:]
-                    top = part.abs().amax(dim=(0, 2)).float() / 127.0    # [KH], held in 32 bits
+                    top = (part.abs().amax(dim=(0, 2)) / 127.0).float()  # [KH], held in 32 bits
                     if at:
                         top = torch.maximum(top, scales[b])
                     top = torch.where(top > 0, top, torch.ones_like(top))
