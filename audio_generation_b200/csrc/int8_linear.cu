@@ -1,0 +1,668 @@
+// The text model's linear layer on 8-bit integers: rows quantized to int8 codes
+// with one scale each, and the product of codes
+//   out[m, n] = a_scale[m] w_scale[n] sum_k a[m, k] w[n, k]
+// with the sum in 32-bit integers on tcgen05 (kind::i8). The integer sum is
+// exact whatever its order, so K may be split freely.
+#include <cuda_fp16.h>
+
+#include "host_util.cuh"
+#include "internal.cuh"
+#include "sm100.cuh"
+
+namespace h3 {
+namespace {
+
+// ------------------------------------------------------------- quantization
+// HBM-bound: 2 (or 4) bytes in and 1 out per element. A group of G threads
+// keeps its row in registers between the two passes over it (maximum, codes),
+// so a row is read once; rows too long for that (K > 65536 in 16 bits) are
+// read twice.
+//
+// The code is the nearest integer to the exact quotient x / scale. A product
+// with the rounded reciprocal is within 2^-22 of the quotient relative to it,
+// below 4e-5 in absolute terms for |quotient| <= 127.001; only elements
+// within 1e-4 of a tie take the division, in 64 bits, where the quotient of
+// two 32-bit floats cannot round onto a tie that it is not on (it is either on
+// the tie or 2^-25 of it away).
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN wins
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+
+struct RowScale {
+  float scale, inv;
+  bool slow;  // the reciprocal is not a normal float: divide everywhere
+};
+
+__device__ __forceinline__ RowScale row_scale_of(float amax) {
+  RowScale s;
+  s.scale = amax / 127.f;
+  if (s.scale == 0.f) s.scale = 1.f;  // zeros, or a maximum below the smallest scale
+  s.inv = 1.f / s.scale;
+  s.slow = s.scale < 1e-30f;
+  return s;
+}
+
+__device__ __noinline__ int code_by_division(float x, float scale) {
+  const double q = rint((double)x / (double)scale);
+  return (int)fmin(fmax(q, -127.0), 127.0);
+}
+
+// Low byte of the result is the code.
+__device__ __forceinline__ uint32_t code_of(float x, const RowScale& s) {
+  const float r = fmaf(x, s.inv, kMagic);
+  const float d = fmaf(x, s.inv, kMagic - r);  // quotient - rounded quotient
+  if (s.slow || fabsf(d) > 0.4999f) return (uint32_t)code_by_division(x, s.scale);
+  return __float_as_uint(r);
+}
+
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// 16 bytes of a row as floats: 8 elements of 2 bytes, or 4 of 4.
+template <h3_type T>
+struct Vec {
+  static constexpr int N = T == H3_F32 ? 4 : 8;
+};
+template <h3_type T>
+__device__ __forceinline__ void unpack(const uint4& u, float* v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (T == H3_BF16) {
+      v[2 * i] = bf16lo(w[i]);
+      v[2 * i + 1] = bf16hi(w[i]);
+    } else if constexpr (T == H3_F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    } else {
+      v[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+
+template <h3_type T>
+__device__ __forceinline__ float amax_of(const uint4& u, float m) {
+  float v[Vec<T>::N];
+  unpack<T>(u, v);
+#pragma unroll
+  for (int k = 0; k < Vec<T>::N; ++k) m = max_nan(m, fabsf(v[k]));
+  return m;
+}
+
+template <h3_type T>
+__device__ __forceinline__ void store_codes(const uint4& u, const RowScale& s, void* dst) {
+  float v[Vec<T>::N];
+  unpack<T>(u, v);
+  const uint32_t a = pack4(code_of(v[0], s), code_of(v[1], s), code_of(v[2], s), code_of(v[3], s));
+  if constexpr (T == H3_F32) {
+    *reinterpret_cast<uint32_t*>(dst) = a;
+  } else {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(
+        a, pack4(code_of(v[4], s), code_of(v[5], s), code_of(v[6], s), code_of(v[7], s)));
+  }
+}
+
+template <int G>
+__device__ __forceinline__ float group_max(float m) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if constexpr (G > 32) {
+    __shared__ float part[G / 32];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = part[threadIdx.x & (G / 32 - 1)];
+#pragma unroll
+    for (int o = G / 64; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  return m;
+}
+
+// G threads per row (a warp with eight rows per block, or the block), NV 16-byte
+// vectors of the row per thread in registers; NV = 0: any length, read twice.
+template <h3_type T, int G, int NV>
+__global__ void __launch_bounds__(G == 32 ? 256 : G)
+    k_quantize_rows_int8(int rows, int K, const uint4* __restrict__ x, int64_t stride_vec,
+                         uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  constexpr int VE = Vec<T>::N;
+  const int row = G == 32 ? blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  if (G == 32 && row >= rows) return;
+  const int t = threadIdx.x & (G - 1);
+  const int nvec = K / VE;
+  const uint4* xr = x + row * stride_vec;
+  uint8_t* cr = codes + (size_t)row * K;
+  uint4 u[NV > 0 ? NV : 1];
+  float m = 0.f;
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (t + i * G < nvec) u[i] = __ldcs(xr + t + i * G);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (t + i * G < nvec) m = amax_of<T>(u[i], m);
+  } else {
+    for (int i = t; i < nvec; i += G) m = amax_of<T>(xr[i], m);
+  }
+  m = group_max<G>(m);
+  if (!(m <= 3.4028235e38f)) {  // an infinity or a NaN in the row
+    for (int i = t; i < K / 4; i += G) reinterpret_cast<uint32_t*>(cr)[i] = 0;
+    if (t == 0) scales[row] = __int_as_float(0x7fc00000);
+    return;
+  }
+  const RowScale s = row_scale_of(m);
+  if (t == 0) scales[row] = s.scale;
+  if constexpr (NV > 0) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (t + i * G < nvec) store_codes<T>(u[i], s, cr + (t + i * G) * VE);
+  } else {
+    for (int i = t; i < nvec; i += G) store_codes<T>(xr[i], s, cr + (size_t)i * VE);
+  }
+}
+
+template <h3_type T, int G, int NV>
+cudaError_t run_quantize(int rows, int K, const void* x, int64_t stride_vec, void* codes,
+                         float* scales, cudaStream_t st) {
+  const int grid = G == 32 ? (rows + 7) / 8 : rows;
+  k_quantize_rows_int8<T, G, NV><<<grid, G == 32 ? 256 : G, 0, st>>>(
+      rows, K, static_cast<const uint4*>(x), stride_vec, static_cast<uint8_t*>(codes), scales);
+  return cudaGetLastError();
+}
+
+// A warp per row while the row fits a warp's registers, then a block of 256,
+// then of 1024, so that a row's loads are all in flight at once.
+template <h3_type T>
+cudaError_t quantize(int rows, int K, const void* x, int64_t stride_vec, void* codes,
+                     float* scales, cudaStream_t st) {
+  const int nvec = K / Vec<T>::N;
+#define H3_Q(G, NV) return run_quantize<T, G, NV>(rows, K, x, stride_vec, codes, scales, st)
+  if (nvec <= 64) H3_Q(32, 2);
+  if (nvec <= 256) H3_Q(32, 8);
+  if (nvec <= 1024) H3_Q(256, 4);
+  if (nvec <= 2048) H3_Q(256, 8);
+  if (nvec <= 8192) H3_Q(1024, 8);
+  H3_Q(1024, 0);
+#undef H3_Q
+}
+
+// ------------------------------------------------------------- matrix product
+
+constexpr int BM = 128;        // rows of a CTA's operand tile = TMEM lanes
+constexpr int BKB = 128;       // K bytes per stage: one 128-byte swizzled row
+constexpr int NUM_THREADS = 192;
+constexpr int A_STAGE = BM * BKB;  // 16 KB
+
+struct Out {
+  void* p;
+  int64_t stride;
+  int type;
+  const float* a_scale;
+  const float* w_scale;
+};
+
+// One output value. The accumulator becomes a float (rounded to 24 bits) and is
+// multiplied by the two scales in float32; the result is rounded once more to
+// a 16-bit type: 3 x 2^-24 relative before that.
+__device__ __forceinline__ void store_one(const Out& o, size_t off, float v) {
+  if (o.type == H3_BF16)
+    static_cast<__nv_bfloat16*>(o.p)[off] = __float2bfloat16_rn(v);
+  else if (o.type == H3_F16)
+    static_cast<__half*>(o.p)[off] = __float2half_rn(v);
+  else
+    static_cast<float*>(o.p)[off] = v;
+}
+
+// 32 neighbouring values of one row, 16-byte aligned.
+__device__ __forceinline__ void store_32(const Out& o, size_t off, const float* v) {
+  if (o.type == H3_F32) {
+    float4* d = reinterpret_cast<float4*>(static_cast<float*>(o.p) + off);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) d[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  } else {
+    uint32_t w[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      if (o.type == H3_BF16) {
+        w[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
+      } else {
+        const __half2 h = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
+        w[q] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.p) + off);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) d[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  }
+}
+
+// Many rows: the persistent CTA-pair form. A pair computes 256 x BN tiles of
+// out with cta_group::2 MMAs, each CTA holding 128 rows of A and BN / 2 of the
+// tile's weight rows per stage, 128 bytes of K (four K = 32 instructions), six
+// stages; the accumulator is double-buffered in TMEM, so the epilogue of a tile
+// overlaps the next tile's products. Warps: 0 TMA producer, 1 TMEM owner and
+// MMA issuer, 2..5 epilogue (one TMEM lane = one row per thread).
+constexpr int PNST = 6;
+template <int BN>
+constexpr int p_stage() { return A_STAGE + BN / 2 * BKB; }
+template <int BN>
+constexpr int p_smem() { return PNST * p_stage<BN>() + 1024 + 256; }
+
+template <int BN>
+__device__ __forceinline__ void pair_tile(int t, int tiles_m, int tiles_n, int group_n, int& m0,
+                                          int& n0) {
+  const int per_group = group_n * tiles_m;
+  const int g = t / per_group, r = t - g * per_group;
+  const int width = min(group_n, tiles_n - g * group_n);
+  m0 = (r / width) * 2 * BM;
+  n0 = (g * group_n + r % width) * BN;
+}
+
+template <int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+    k_int8_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
+                int M, int N, int kb_n, int group_n, const Out out, int* err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  constexpr int STAGE = p_stage<BN>();
+  static_assert(STAGE % 1024 == 0, "stage alignment");
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + PNST * STAGE);
+  uint64_t* empty = full + PNST;
+  uint64_t* tfull = empty + PNST;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const int tiles_m = (M + 2 * BM - 1) / (2 * BM), tiles_n = (N + BN - 1) / BN;
+  const int T = tiles_m * tiles_n;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < PNST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 8);  // one arrival per epilogue warp of both CTAs
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 2 * BN);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{err, abort_flag};
+  auto at = [&](uint64_t* bar, uint32_t r) { return mapa_shared(smem_u32(bar), r); };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t n = 0;
+      bool ok = true;
+      for (int t = pair; t < T && ok; t += n_pairs) {
+        int m0, n0;
+        pair_tile<BN>(t, tiles_m, tiles_n, group_n, m0, n0);
+        for (int kb = 0; kb < kb_n; ++kb) {
+          const uint32_t s = n % PNST, ph = (n / PNST) & 1;
+          if (!mbar_wait(&empty[s], ph ^ 1, wc)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + s * STAGE;
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE);
+          tma_load_2d_pair(sa, &tmA, at(&full[s], 0), kb * BKB, m0 + BM * rank);
+          tma_load_2d_pair(sa + A_STAGE, &tmW, at(&full[s], 0), kb * BKB, n0 + (BN / 2) * rank);
+          ++n;
+        }
+      }
+      if (!ok && leader) {  // let issued copies land before the CTA retires
+        const uint32_t first = n > PNST ? n - PNST : 0;
+        for (uint32_t i = first; i < n; ++i) mbar_drain(&full[i % PNST], (i / PNST) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    if (leader) {  // the whole warp runs the loop; one elected lane issues
+      constexpr uint32_t idesc = idesc_s8_s32(2 * BM, BN);
+      constexpr uint32_t hi = sdesc_hi_sw128(1024);
+      const uint32_t base_lo = sdesc_lo(smem_u32(smem), 16);
+      uint32_t n = 0, it = 0;
+      bool ok = true;
+      for (int t = pair; t < T && ok; t += n_pairs, ++it) {
+        const uint32_t acc = it & 1, aph = (it >> 1) & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], aph ^ 1, wc))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * BN;
+        for (int kb = 0; kb < kb_n; ++kb) {
+          const uint32_t s = n % PNST, ph = (n / PNST) & 1;
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, wc))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_lo = base_lo + s * (STAGE >> 4);
+          const uint32_t b_lo = a_lo + (A_STAGE >> 4);
+#pragma unroll
+          for (int k = 0; k < BKB / 32; ++k)
+            umma_ss_w_pair_elect_i8(d, a_lo + 2 * k, hi, b_lo + 2 * k, hi, idesc,
+                                    (kb | k) != 0 ? 1u : 0u);
+          umma_commit_pair_elect(at(&empty[s], 0));
+          umma_commit_pair_elect(at(&empty[s], 1));
+          ++n;
+        }
+        if (!ok) break;
+        umma_commit_pair_elect(at(&tfull[acc], 0));
+        umma_commit_pair_elect(at(&tfull[acc], 1));
+      }
+      umma_commit_pair_elect(at(drain, 0));  // every MMA issued is complete past this point
+      mbar_drain(drain, 0);
+    }
+  } else {
+    const int quarter = warp & 3;
+    const uint32_t tempty0 = at(&tempty[0], 0), tempty1 = at(&tempty[1], 0);
+    const bool vec = out.stride % (out.type == H3_F32 ? 4 : 8) == 0;
+    uint32_t it = 0;
+    for (int t = pair; t < T; t += n_pairs, ++it) {
+      const uint32_t acc = it & 1, aph = (it >> 1) & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], aph, wc))) break;
+      tc_fence_after();
+      int m0, n0;
+      pair_tile<BN>(t, tiles_m, tiles_n, group_n, m0, n0);
+      const int m = m0 + BM * rank + quarter * 32 + lane;
+      const bool row_ok = m < M;
+      const float sa = row_ok ? out.a_scale[m] : 0.f;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
+#pragma unroll 1
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(taddr + 32 * c, r);
+        tmem_wait_ld();
+        const int n = n0 + 32 * c;
+        if (n + 32 <= N && vec) {
+          float v[32];
+          const float4* w4 = reinterpret_cast<const float4*>(out.w_scale + n);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 w = __ldg(w4 + q);
+            v[4 * q] = (float)(int)r[4 * q] * (sa * w.x);
+            v[4 * q + 1] = (float)(int)r[4 * q + 1] * (sa * w.y);
+            v[4 * q + 2] = (float)(int)r[4 * q + 2] * (sa * w.z);
+            v[4 * q + 3] = (float)(int)r[4 * q + 3] * (sa * w.w);
+          }
+          if (row_ok) store_32(out, m * out.stride + n, v);
+        } else if (row_ok) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (n + i < N)
+              store_one(out, m * out.stride + n + i,
+                        (float)(int)r[i] * (sa * __ldg(out.w_scale + n + i)));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc ? tempty1 : tempty0);
+    }
+  }
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while the pair's MMAs or signals may still reach it
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 2 * BN);
+  }
+}
+
+// Few rows (at most NT): bound by the bytes of the weights. The weights take
+// the MMA's 128-row side and the tokens its N side, so a CTA streams 128 weight
+// rows; the CTAs of a cluster share the K axis of one such tile and add their
+// integer sums through distributed shared memory, each finishing a share of the
+// tokens. Out is written with neighbouring lanes on neighbouring columns.
+template <int NT>
+constexpr int s_stages() { return NT <= 32 ? 5 : NT == 64 ? 4 : 3; }
+template <int NT>
+constexpr int s_stage() { return A_STAGE + NT * BKB; }
+template <int NT>
+constexpr int s_smem() { return s_stages<NT>() * s_stage<NT>() + 1024 + 256; }
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(NUM_THREADS)
+    k_int8_skinny(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
+                  int M, int N, int kb_n, int split, const Out out, int* err) {
+  constexpr int NST = s_stages<NT>(), STAGE = s_stage<NT>();
+  static_assert(STAGE % 1024 == 0, "stage alignment");
+  static_assert(NT * BM * 4 <= NST * STAGE, "the partial sums reuse the stages");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NST * STAGE);
+  uint64_t* empty = full + NST;
+  uint64_t* done = empty + NST;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  constexpr uint32_t COLS = NT < 32 ? 32 : NT;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = split > 1 ? (int)cluster_ctarank() : 0;
+  const int n0 = (int)(blockIdx.x / split) * BM;
+  const int kb0 = (int)((long long)kb_n * rank / split);
+  const int kb1 = (int)((long long)kb_n * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmA);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{err, abort_flag};
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t n = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        const uint32_t s = n % NST, ph = (n / NST) & 1;
+        if (!mbar_wait(&empty[s], ph ^ 1, wc)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sw = smem + s * STAGE;
+        mbar_arrive_expect_tx(&full[s], STAGE);
+        tma_load_2d(sw, &tmW, &full[s], kb * BKB, n0);
+        tma_load_2d(sw + A_STAGE, &tmA, &full[s], kb * BKB, 0);
+      }
+      if (!ok) {  // let issued copies land before the CTA retires
+        const uint32_t first = n > NST ? n - NST : 0;
+        for (uint32_t i = first; i < n; ++i) mbar_drain(&full[i % NST], (i / NST) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_s8_s32(BM, NT);
+    constexpr uint32_t hi = sdesc_hi_sw128(1024);
+    const uint32_t base_lo = sdesc_lo(smem_u32(smem), 16);
+    uint32_t n = 0;
+    for (int kb = kb0; kb < kb1; ++kb, ++n) {
+      const uint32_t s = n % NST, ph = (n / NST) & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, wc))) break;
+      tc_fence_after();
+      const uint32_t a_lo = base_lo + s * (STAGE >> 4);
+      const uint32_t b_lo = a_lo + (A_STAGE >> 4);
+#pragma unroll
+      for (int k = 0; k < BKB / 32; ++k)
+        umma_ss_w_elect_i8(tmem, a_lo + 2 * k, hi, b_lo + 2 * k, hi, idesc,
+                           (n | k) != 0 ? 1u : 0u);
+      umma_commit_elect(&empty[s]);
+    }
+    umma_commit_elect(done);  // also after a wait that ran out: the sums are then void
+    if (!__all_sync(0xffffffffu, mbar_wait(done, 0, wc))) mbar_drain(done, 0);
+  }
+  // Every sum of this CTA is in TMEM and its stages are no longer read.
+  __syncthreads();
+  tc_fence_after();
+  const int quarter = warp & 3;
+  const int r = quarter * 32 + lane;
+  const int n = n0 + r;
+  const float sw = warp >= 2 && n < N ? out.w_scale[n] : 0.f;
+  uint32_t* part = reinterpret_cast<uint32_t*>(smem);  // [NT][128] sums of this CTA
+  if (warp >= 2) {
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll 1
+    for (int c = 0; c < (NT + 31) / 32; ++c) {
+      uint32_t v[32];
+      tmem_ld32(taddr + 32 * c, v);
+      tmem_wait_ld();
+      if (split > 1) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (32 * c + i < M && 32 * c + i < NT) part[(32 * c + i) * BM + r] = v[i];
+      } else if (n < N) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const int m = 32 * c + i;
+          if (m < M) store_one(out, m * out.stride + n, (float)(int)v[i] * (out.a_scale[m] * sw));
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  if (split > 1) {
+    cluster_sync();
+    if (warp >= 2 && n < N) {
+      const int m0 = M * rank / split, m1 = M * (rank + 1) / split;
+      const uint32_t mine = smem_u32(part) + r * 4;
+      for (int m = m0; m < m1; ++m) {
+        int sum = 0;
+        for (int q = 0; q < split; ++q)
+          sum += (int)ld_cluster_u32(mapa_shared(mine + m * BM * 4, q));
+        store_one(out, m * out.stride + n, (float)sum * (out.a_scale[m] * sw));
+      }
+    }
+    cluster_sync();  // no CTA leaves while another reads its sums
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, COLS);
+  }
+}
+
+bool tmap_codes(CUtensorMap* t, const void* p, int rows, int K, uint32_t box_rows) {
+  const uint64_t d[2] = {(uint64_t)K, (uint64_t)rows}, s[1] = {(uint64_t)K};
+  const uint32_t b[2] = {BKB, box_rows};
+  return make_tmap(t, p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, d, s, b);
+}
+
+template <int BN>
+cudaError_t run_pair(int M, int N, int K, const void* a, const void* w, const Out& out, int* err,
+                     cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(k_int8_pair<BN>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, p_smem<BN>());
+  if (e != cudaSuccess) return e;
+  CUtensorMap ta, tw;
+  if (!tmap_codes(&ta, a, M, K, BM) || !tmap_codes(&tw, w, N, K, BN / 2))
+    return cudaErrorInvalidValue;
+  const long long tiles_n = (N + BN - 1) / BN;
+  const long long T = (long long)((M + 2 * BM - 1) / (2 * BM)) * tiles_n;
+  if (T > 0x3fffffff) return cudaErrorInvalidValue;
+  const int max_pairs = num_sms() / 2;
+  const int n_pairs = T < max_pairs ? (int)T : max_pairs;
+  // Weight tiles kept L2-resident per group: about 48 MB.
+  long long group_n = (48ll << 20) / ((long long)BN * K);
+  if (group_n < 1) group_n = 1;
+  if (group_n > tiles_n) group_n = tiles_n;
+  k_int8_pair<BN><<<2 * n_pairs, NUM_THREADS, p_smem<BN>(), st>>>(
+      ta, tw, M, N, (K + BKB - 1) / BKB, (int)group_n, out, err);
+  return cudaGetLastError();
+}
+
+template <int NT>
+cudaError_t run_skinny(int M, int N, int K, const void* a, const void* w, const Out& out,
+                       int* err, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(k_int8_skinny<NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, s_smem<NT>());
+  if (e != cudaSuccess) return e;
+  CUtensorMap ta, tw;
+  if (!tmap_codes(&ta, a, M, K, NT) || !tmap_codes(&tw, w, N, K, BM)) return cudaErrorInvalidValue;
+  const int tiles = (N + BM - 1) / BM, kb_n = (K + BKB - 1) / BKB;
+  // Two CTAs fit an SM: split K until they are about all there, each with two
+  // K steps at least.
+  int split = 1;
+  while (split < 8 && tiles * split < 2 * num_sms() && kb_n >= 4 * split) split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = s_smem<NT>();
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_int8_skinny<NT>, tw, ta, M, N, kb_n, split, out, err);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows_int8(h3_type type, int rows, int K, const void* x,
+                                      int64_t x_stride, void* codes, float* scales,
+                                      cudaStream_t st) {
+  switch (type) {
+    case H3_BF16: return quantize<H3_BF16>(rows, K, x, x_stride / 8, codes, scales, st);
+    case H3_F16: return quantize<H3_F16>(rows, K, x, x_stride / 8, codes, scales, st);
+    case H3_F32: return quantize<H3_F32>(rows, K, x, x_stride / 4, codes, scales, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_matmul_int8(int M, int N, int K, const void* a, const float* a_scale,
+                               const void* w, const float* w_scale, h3_type out_type, void* out,
+                               int64_t out_stride, int* err, cudaStream_t st) {
+  const Out o{out, out_stride, (int)out_type, a_scale, w_scale};
+  if (M <= 16) return run_skinny<16>(M, N, K, a, w, o, err, st);
+  if (M <= 32) return run_skinny<32>(M, N, K, a, w, o, err, st);
+  if (M <= 64) return run_skinny<64>(M, N, K, a, w, o, err, st);
+  if (M <= 128) return run_skinny<128>(M, N, K, a, w, o, err, st);
+  return run_pair<256>(M, N, K, a, w, o, err, st);
+}
+
+}  // namespace h3

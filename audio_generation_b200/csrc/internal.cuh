@@ -253,6 +253,19 @@ cudaError_t launch_out_head(int B, int n, int H, int V, int C, float eps, const 
                             const float* table, const float* tmod_out, const float* W,
                             float* out, cudaStream_t st);
 
+// ---- the text model's operators ----
+// Error word of the text operators on the current device (text_api.cu).
+h3_status text_error_word(int** out);
+
+// Rows of `type` -> int8 codes and one scale per row (int8_linear.cu).
+cudaError_t launch_quantize_rows_int8(h3_type type, int rows, int K, const void* x,
+                                      int64_t x_stride, void* codes, float* scales,
+                                      cudaStream_t st);
+// out = a_scale w_scale (A . W^T), A [M, K], W [N, K] int8 codes, M, N > 0.
+cudaError_t launch_matmul_int8(int M, int N, int K, const void* a, const float* a_scale,
+                               const void* w, const float* w_scale, h3_type out_type, void* out,
+                               int64_t out_stride, int* err, cudaStream_t st);
+
 // Shape checks shared by the entry points (H3_OK or the status to return).
 h3_status check_dims(const h3_dims* d);
 

@@ -72,6 +72,9 @@ class h3_block_weights_e4m3(ctypes.Structure):
         "w2_codes", "w2_scales")]
 
 
+# h3_type: element type of the text operators' activation buffers
+H3_BF16, H3_F16, H3_F32 = 0, 1, 2
+
 H3_MAX_RANKS = 8
 
 
@@ -83,7 +86,7 @@ class h3_ulysses_peers(ctypes.Structure):
 
 _lib: Optional[ctypes.CDLL] = None
 
-_vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_vp, _i, _sz, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 _SIGNATURES = {
     "h3_status_string": (ctypes.c_char_p, [_i]),
     "h3_abi_version": (_i, []),
@@ -142,6 +145,9 @@ _SIGNATURES = {
                         ctypes.POINTER(h3_io_weights), ctypes.POINTER(h3_block_weights), _i,
                         ctypes.POINTER(h3_block_weights), _i, _vp, _vp, _i, _vp, _vp, _vp, _vp,
                         _vp, _vp, _i, _vp, _sz, _vp]),
+    "h3_quantize_int8_rows": (_i, [_i, _i, _i, _vp, _i64, _vp, _vp, _vp]),
+    "h3_matmul_int8": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _i64, _vp]),
+    "h3_text_error": (_i, []),
     "h3_stack_forward": (_i, [ctypes.POINTER(h3_dims), ctypes.POINTER(h3_block_weights), _i, _vp,
                               _vp, _vp, _i, _vp, _sz, _vp]),
 }
@@ -517,3 +523,31 @@ def h3_block_forward_e4m3(dims: h3_dims, weights: h3_block_weights, w8: h3_block
     _check(lib().h3_block_forward_e4m3(ctypes.byref(dims), ctypes.byref(weights), ctypes.byref(w8),
                                        layout.handle, _ptr(tmod), _ptr(x), B, _ptr(ws), ws_bytes,
                                        _stream(stream)), "h3_block_forward_e4m3")
+
+
+# ---------------------------------------------------------------- text model
+
+_TYPES = {"torch.bfloat16": H3_BF16, "torch.float16": H3_F16, "torch.float32": H3_F32}
+
+
+def _type(t) -> int:
+    """h3_type of a torch dtype (or an h3_type itself); -1, which the library
+    refuses, for any other."""
+    return t if isinstance(t, int) else _TYPES.get(str(t), -1)
+
+
+def h3_quantize_int8_rows(dtype, rows: int, K: int, x, x_stride: int, codes, scales,
+                          stream=None) -> None:
+    _check(lib().h3_quantize_int8_rows(_type(dtype), rows, K, _ptr(x), x_stride, _ptr(codes),
+                                       _ptr(scales), _stream(stream)), "h3_quantize_int8_rows")
+
+
+def h3_matmul_int8(M: int, N: int, K: int, a_codes, a_scales, w_codes, w_scales, out_dtype, out,
+                   out_stride: int, stream=None) -> None:
+    _check(lib().h3_matmul_int8(M, N, K, _ptr(a_codes), _ptr(a_scales), _ptr(w_codes),
+                                _ptr(w_scales), _type(out_dtype), _ptr(out), out_stride,
+                                _stream(stream)), "h3_matmul_int8")
+
+
+def h3_text_error() -> int:
+    return lib().h3_text_error()

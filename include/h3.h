@@ -536,6 +536,45 @@ H3_API h3_status h3_forward(const h3_dims* dims, const h3_io_dims* io, const h3_
                             float* core_residual, int core_mode, void* ws, size_t ws_bytes,
                             h3_stream_t stream);
 
+/* ---- the text model: 8-bit integer linear layers ---- */
+
+/* The text rows the transformer takes (h3_forward's text_states) come from a
+ * text model as large as the transformer itself. The entry points below are the
+ * operators such a model runs per layer; they use no layout object. Waits that
+ * run out in them are recorded in a library-owned error word, one per GPU, read
+ * by h3_text_error. Buffers must be memory of the current device. */
+
+/* Element type of an activation buffer. */
+typedef enum { H3_BF16 = 0, H3_F16 = 1, H3_F32 = 2 } h3_type;
+
+/* Rows [rows, K] of `type` (row r starts x_stride elements after row r - 1) ->
+ * int8 codes [rows, K] and one scale per row: scale = max|x| / 127 in float32
+ * (1 for a row of zeros), code = x / scale rounded to the nearest integer, ties
+ * to even (the exact quotient decides), limited to [-127, 127]. The pages' 8-bit
+ * form: "MiniMax H3 Inference Engine voor Mac computers", sections "Profiling
+ * en diagnostische pads" (int8 MLP and QKV) and "Sampler en DiT controls" (one
+ * activation scale per row). A row that holds an infinity or a NaN gets scale
+ * NaN and codes 0, so that whatever is computed from it is NaN. Serves
+ * activations (one scale per token) and weights (one per output channel).
+ * K % 16 == 0; x_stride >= K, x_stride % 8 == 0. Enqueues. */
+H3_API h3_status h3_quantize_int8_rows(h3_type type, int rows, int K, const void* x,
+                                       int64_t x_stride, void* codes, float* scales,
+                                       h3_stream_t stream);
+
+/* out[m, n] = a_scales[m] * w_scales[n] * sum_k a_codes[m, k] * w_codes[n, k]:
+ * int8 codes a [M, K], w [N, K] (any value, -128 too), the sum exact in 32-bit
+ * integers, scales float32, out of `out_type`, row m out_stride elements after
+ * row m - 1 (columns past N are not written). M, N >= 0; K % 16 == 0 and
+ * 0 < K <= 131056 (the sum cannot leave 32 bits); out_stride >= N. Enqueues. */
+H3_API h3_status h3_matmul_int8(int M, int N, int K, const void* a_codes, const float* a_scales,
+                                const void* w_codes, const float* w_scales, h3_type out_type,
+                                void* out, int64_t out_stride, h3_stream_t stream);
+
+/* Read and clear the current device's error word of the text operators
+ * (synchronises the device): H3_OK, or H3_ERR_TIMEOUT if a bounded in-kernel
+ * wait ran out since the last read. */
+H3_API h3_status h3_text_error(void);
+
 #ifdef __cplusplus
 }
 #endif
