@@ -39,6 +39,7 @@
 #include "host_util.cuh"
 #include "internal.cuh"
 #include "sm100.cuh"
+#include "softmax.cuh"
 
 namespace h3 {
 namespace {
@@ -68,12 +69,6 @@ struct Bars {
 };
 
 
-__device__ __forceinline__ float exp2_mufu(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 2^x on the FMA pipe, for two values at once: split x = j + f with
 // j = round(x) (adding 1.5 * 2^23 leaves the rounded integer in the low
 // mantissa bits) and f in [-1/2, 1/2]; 2^f by a cubic fitted by least squares
@@ -85,26 +80,6 @@ __device__ __forceinline__ float exp2_mufu(float x) {
 constexpr float kExpC3 = 0.05508868396f, kExpC2 = 0.24260404706f, kExpC1 = 0.69327622652f,
                 kExpC0 = 0.99992895126f;
 constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23
-
-// Packed fp32 pair arithmetic (one instruction for two lanes of work).
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 
 __device__ __forceinline__ void exp2_poly2(uint64_t x2, float& p0, float& p1) {
   float x0, x1;
@@ -131,12 +106,6 @@ __device__ __forceinline__ void exp2_poly2(uint64_t x2, float& p0, float& p1) {
 #define H3_ATTN_POLY_MASK 0x20820820u
 #endif
 constexpr uint32_t kPolyMask = H3_ATTN_POLY_MASK;
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 
 // Start of the 128 output values of row s, head h of batch element b.
 __device__ __forceinline__ __nv_bfloat16* out_row(const RowMap& m, int b, int s, int h) {

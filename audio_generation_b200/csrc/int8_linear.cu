@@ -8,6 +8,7 @@
 #include "host_util.cuh"
 #include "internal.cuh"
 #include "sm100.cuh"
+#include "softmax.cuh"
 
 namespace h3 {
 namespace {
@@ -24,12 +25,6 @@ namespace {
 // within 1e-4 of a tie take the division, in 64 bits, where the quotient of
 // two 32-bit floats cannot round onto a tie that it is not on (it is either on
 // the tie or 2^-25 of it away).
-
-__device__ __forceinline__ float max_nan(float a, float b) {  // a NaN wins
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
 

@@ -81,6 +81,14 @@ struct h3_layout {
   }
 };
 
+// The prompts object of the C ABI: the work items of one batch of packed prompts.
+struct h3_prompts {
+  int device = 0, q_heads = 0, kv_heads = 0, head_dim = 0;
+  int rows = 0;     // rows of the packed buffers up to the last prompt's end
+  int n_items = 0;  // two query tiles each
+  void* items = nullptr;  // device int4 [n_items]
+};
+
 namespace h3 {
 
 // ---- launchers (each returns cudaError_t of the launch) ----
@@ -265,6 +273,14 @@ cudaError_t launch_quantize_rows_int8(h3_type type, int rows, int K, const void*
 cudaError_t launch_matmul_int8(int M, int N, int K, const void* a, const float* a_scale,
                                const void* w, const float* w_scale, h3_type out_type, void* out,
                                int64_t out_stride, int* err, cudaStream_t st);
+
+// Work items of prompts [offsets[i], offsets[i + 1]) (prompt_attention.cu);
+// offsets checked, p's heads set. On failure nothing is allocated.
+h3_status build_prompts(h3_prompts* p, const int32_t* offsets, int n_prompts);
+cudaError_t launch_prompt_attention(const h3_prompts* p, bool f16, const void* q,
+                                    int64_t q_stride, const void* k, int64_t k_stride,
+                                    const void* v, int64_t v_stride, float scale, void* o,
+                                    int64_t o_stride, int* err, cudaStream_t st);
 
 // Shape checks shared by the entry points (H3_OK or the status to return).
 h3_status check_dims(const h3_dims* d);

@@ -1,0 +1,503 @@
+// Causal attention over packed prompts of different lengths, grouped heads:
+//   o[i, h] = sum_{j <= i} softmax_j(scale q[i, h] . k[j, h / G]) v[j, h / G]
+// over the tokens of i's own prompt, G = q_heads / kv_heads.
+//
+// Flash style on tcgen05, one pass over the keys with a running maximum and
+// sum, the roles and tensor-memory plan of the packed-sequence attention kernel:
+// a CTA takes two 128-row query tiles of one kv head, so that the tensor core
+// works on one tile while the other's softmax runs. Warps 0..3 and 4..7 are the
+// tiles' softmax (one row per thread = one TMEM lane), warp 8 the TMA producer,
+// warp 9 the TMEM owner and MMA issuer, warps 10 and 11 idle (their registers go
+// to the softmax). S_i takes 128 TMEM columns, P overwrites its first 64, O_i
+// takes D.
+//
+// A tile's rows are (position, head of the group): 128 / G positions with all G
+// heads that share the K and V tile. Compared with 128 positions of one head, a
+// short prompt fills its tiles G times better, the diagonal costs G times fewer
+// masked keys, and K and V are fetched once per group. One 3-D TMA box (64
+// channels, G heads, 128 / G tokens) lays such a tile down as 128-byte rows.
+// Where G does not divide 128 the last rows of a tile are idle.
+//
+// Work items (two tiles each) come from the prompts object, longest key range
+// first, so that the long ones do not end the launch alone.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "host_util.cuh"
+#include "internal.cuh"
+#include "sm100.cuh"
+#include "softmax.cuh"
+
+namespace h3 {
+namespace {
+
+constexpr int HALF = 128 * 64 * 2;  // 128 rows x 64 channels: 16 KB
+constexpr int NUM_THREADS = 384;
+// 2 * 128 * kSoftmaxRegs + 128 * kControlRegs must not exceed the 384 * 168
+// registers of the launch.
+constexpr uint32_t kSoftmaxRegs = 216, kControlRegs = 72;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= 384 * 168, "register split");
+constexpr int TMEM_COLS = 512;
+constexpr float kLazyRescale = 8.0f;  // log2 units
+
+struct Bars {
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2],
+      p_full[2], o_final[2], drain;
+};
+
+// smem: Q0 Q1 | K0 K1 | V0 V1 | barriers
+template <int D>
+constexpr int tile_bytes() { return D / 64 * HALF; }
+template <int D>
+constexpr int smem_bytes() { return 6 * tile_bytes<D>() + 256 + 1024; }
+
+struct Args {
+  const uint16_t *q, *k, *v;
+  uint16_t* o;
+  int64_t q_stride, k_stride, v_stride, o_stride;
+  const int4* items;  // {first row of the prompt, first position, length, 0}
+  int kv_heads, group, tile_pos;  // tile_pos = 128 / group positions per tile
+  float scale_log2;
+  int* err;
+};
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return pack_bf16x2(lo, hi);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ float to_float(uint16_t u) {
+  if constexpr (F16) return __half2float(__ushort_as_half(u));
+  return __uint_as_float((uint32_t)u << 16);
+}
+
+// One output row by plain arithmetic, a warp together: for rows whose tiles gave
+// an infinity or a NaN. A key outside the row's range carries the weight 0, but
+// 0 times an infinite or NaN v of a later or a neighbouring prompt's token is
+// NaN in a matrix product; here only the row's own keys are touched, so what
+// they give is the row's true result.
+template <int D, bool F16>
+__device__ __noinline__ void plain_row(const Args& a, int start, int pos, int head) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int kvh = head / a.group;
+  const uint16_t* q = a.q + (start + pos) * a.q_stride + head * D + lane * E;
+  float qv[E], acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    qv[e] = to_float<F16>(q[e]);
+    acc[e] = 0.f;
+  }
+  float m = -INFINITY, l = 0.f;
+  for (int j = 0; j <= pos; ++j) {
+    const uint16_t* k = a.k + (start + j) * a.k_stride + kvh * D + lane * E;
+    const uint16_t* v = a.v + (start + j) * a.v_stride + kvh * D + lane * E;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(qv[e], to_float<F16>(k[e]), s);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    s *= a.scale_log2;
+    if (s > m) {
+      const float alpha = exp2_mufu(m - s);
+      l *= alpha;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= alpha;
+      m = s;
+    }
+    const float p = s == -INFINITY ? 0.f : exp2_mufu(s - m);
+    l += p;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(p, to_float<F16>(v[e]), acc[e]);
+  }
+  uint16_t* o = a.o + (start + pos) * a.o_stride + head * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(o + e) = pack2<F16>(acc[e] / l, acc[e + 1] / l);
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    k_prompt_attention(const __grid_constant__ CUtensorMap tq,
+                       const __grid_constant__ CUtensorMap tk,
+                       const __grid_constant__ CUtensorMap tv, const __grid_constant__ Args a) {
+  constexpr int TILE = tile_bytes<D>();
+  constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE, OFF_BAR = 6 * TILE;
+  // fp16 P: weights are stored times 2^7 (at most 2^15 with the lazy maximum),
+  // so that they stay normal numbers down to 2^-21 of the largest.
+  constexpr float kShift = F16 ? 7.f : 0.f;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = blockIdx.x / a.kv_heads, kvh = blockIdx.x - item * a.kv_heads;
+  const int4 it = a.items[item];
+  const int start = it.x, pos0 = it.y, len = it.z, P = a.tile_pos;
+  // key tiles each query tile visits: up to its last existing position
+  const int n0 = (min(pos0 + P, len) - 1) / 128 + 1;
+  const int n1 = pos0 + P < len ? (min(pos0 + 2 * P, len) - 1) / 128 + 1 : 0;
+  const int n = max(n0, n1);
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->k_full[i], 1);
+      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->v_full[i], 1);
+      mbar_init(&bars->v_empty[i], 1);
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_half[i], 4);  // one arrival per softmax warp
+      mbar_init(&bars->p_full[i], 4);
+      mbar_init(&bars->o_final[i], 1);
+    }
+    mbar_init(&bars->drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{a.err, abort_flag};
+
+  if (warp >= 8) {
+    setmaxnreg_dec<kControlRegs>();
+    if (warp == 8) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        const int tiles = n1 > 0 ? 2 : 1;
+        mbar_arrive_expect_tx(&bars->q_full, tiles * (D / 64) * P * a.group * 128);
+        for (int i = 0; i < tiles; ++i)
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(smem + OFF_Q + i * TILE + h * HALF, &tq, &bars->q_full, 64 * h,
+                        kvh * a.group, start + pos0 + i * P);
+        int nk = 0, nv = 0;
+        bool ok = true;
+        for (int j = 0; j < n && ok; ++j) {
+          const int st = j & 1;
+          const uint32_t ph = ((j >> 1) & 1) ^ 1;
+          if (!mbar_wait(&bars->k_empty[st], ph, wc)) { ok = false; break; }
+          mbar_arrive_expect_tx(&bars->k_full[st], TILE);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(smem + OFF_K + st * TILE + h * HALF, &tk, &bars->k_full[st], 64 * h, kvh,
+                        start + j * 128);
+          ++nk;
+          if (!mbar_wait(&bars->v_empty[st], ph, wc)) { ok = false; break; }
+          mbar_arrive_expect_tx(&bars->v_full[st], TILE);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(smem + OFF_V + st * TILE + h * HALF, &tv, &bars->v_full[st], 64 * h, kvh,
+                        start + j * 128);
+          ++nv;
+        }
+        if (!ok) {  // let issued copies land before the CTA retires
+          mbar_drain(&bars->q_full, 0);
+          for (int j = nk > 2 ? nk - 2 : 0; j < nk; ++j) mbar_drain(&bars->k_full[j & 1], (j >> 1) & 1);
+          for (int j = nv > 2 ? nv - 2 : 0; j < nv; ++j) mbar_drain(&bars->v_full[j & 1], (j >> 1) & 1);
+        }
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_s = idesc_f16_f32(128, 128, false, false, !F16);
+      constexpr uint32_t idesc_pv = idesc_f16_f32(128, D, false, true, !F16);
+      constexpr uint32_t hi = sdesc_hi_sw128(1024);
+      const uint32_t q_lo = sdesc_lo(smem_u32(smem + OFF_Q), 16);
+      const uint32_t k_lo = sdesc_lo(smem_u32(smem + OFF_K), 16);
+      const uint32_t v_lo = sdesc_lo(smem_u32(smem + OFF_V), HALF);
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
+      };
+      bool ok = wait_all(&bars->q_full, 0);
+      tc_fence_after();
+      // Tile 0 uses key tile j first where it visits it, tile 1 last; tile 1's
+      // range is at least tile 0's unless tile 1 is empty.
+      auto issue_s = [&](int i, int j) -> bool {
+        const int st = j & 1;
+        if (i == 0 || j >= n0) {
+          if (!wait_all(&bars->k_full[st], (j >> 1) & 1)) return false;
+          tc_fence_after();
+        }
+        const uint32_t kl = k_lo + st * (TILE >> 4);
+        const uint32_t ql = q_lo + i * (TILE >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+          umma_ss_w_elect(tmem + i * 128, ql + off, hi, kl + off, hi, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit_elect(&bars->s_full[i]);
+        if (i == 1 || j >= n1) umma_commit_elect(&bars->k_empty[st]);
+        return true;
+      };
+      // O_i += P_i(j) V_j in two halves of the keys, each as soon as it is stored
+      auto issue_pv = [&](int i, int j) -> bool {
+        const int st = j & 1;
+        if (!wait_all(&bars->p_half[i], j & 1)) return false;
+        if ((i == 0 || j >= n0) && !wait_all(&bars->v_full[st], (j >> 1) & 1)) return false;
+        tc_fence_after();
+        const uint32_t vl = v_lo + st * (TILE >> 4);
+        const uint32_t o = tmem + 256 + i * 128, p = tmem + i * 128;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ts_w_elect(o, p + kk * 8, vl + kk * (2048 >> 4), hi, idesc_pv,
+                          (j > 0 || kk > 0) ? 1u : 0u);
+        if (!wait_all(&bars->p_full[i], j & 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 4; kk < 8; ++kk)
+          umma_ts_w_elect(o, p + kk * 8, vl + kk * (2048 >> 4), hi, idesc_pv, 1u);
+        if (i == 1 || j >= n1) umma_commit_elect(&bars->v_empty[st]);
+        if (j == (i == 0 ? n0 : n1) - 1) umma_commit_elect(&bars->o_final[i]);
+        return true;
+      };
+      if (ok) ok = issue_s(0, 0);
+      if (ok && n1 > 0) ok = issue_s(1, 0);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j < n0) ok = issue_pv(0, j);
+        if (ok && j + 1 < n0) ok = issue_s(0, j + 1);
+        if (ok && j < n1) ok = issue_pv(1, j);
+        if (ok && j + 1 < n1) ok = issue_s(1, j + 1);
+      }
+      umma_commit_elect(&bars->drain);  // every MMA issued is complete past this point
+      mbar_drain(&bars->drain, 0);
+    }
+  } else {
+    setmaxnreg_inc<kSoftmaxRegs>();
+    // ------------------------------------------------------------ softmax (warps 0..7)
+    const int i = warp >> 2;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // row in the tile = TMEM lane
+    const int rp = r / a.group;         // its position in the tile, its head in the group
+    const int tile0 = pos0 + i * P, pos = tile0 + rp;
+    const int my_n = i == 0 ? n0 : n1;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_col = lane_base + i * 128;
+    const uint32_t o_col = lane_base + 256 + i * 128;
+    float m_run = -INFINITY, l_run = 0.f;
+    const uint64_t scale2 = f2_pack(a.scale_log2, a.scale_log2);
+    bool ok = true;
+    for (int j = 0; j < my_n; ++j) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[i], j & 1, wc))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float sc[128];
+      {
+        uint32_t rr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, rr[c]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sc[32 * c + e] = __uint_as_float(rr[c][e]);
+      }
+      if (128 * j + 127 > tile0) {  // the diagonal: keys after the row's own position
+        const int last = pos - 128 * j;
+#pragma unroll
+        for (int e = 0; e < 128; ++e)
+          if (e > last) sc[e] = -INFINITY;
+      }
+      float pm[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) pm[k] = max3(sc[2 * k], sc[2 * k + 1], sc[16 + 2 * k]);
+#pragma unroll
+      for (int e = 32; e < 128; e += 16)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pm[k] = max3(pm[k], sc[e + 2 * k], sc[e + 2 * k + 1]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], sc[16 + 2 * k + 1]);
+      float mx = max3(max3(pm[0], pm[1], pm[2]), max3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+      mx *= a.scale_log2;
+      // O_i is stable here: the commit that signalled S_i(j) follows PV_i(j-1).
+      const bool need = mx > m_run + kLazyRescale;
+      if (__any_sync(0xffffffffu, need)) {
+        const float m_new = need ? mx : m_run;
+        if (j > 0) {
+          const float alpha = need ? exp2_mufu(m_run - m_new) : 1.f;
+          l_run *= alpha;
+          uint32_t rr[32];
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            tmem_ld32(o_col + 32 * c, rr);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) rr[e] = __float_as_uint(__uint_as_float(rr[e]) * alpha);
+            tmem_st32(o_col + 32 * c, rr);
+          }
+        }
+        m_run = m_new;
+      }
+      // P = 2^(s * scale - m + shift) in the type of v, over S columns already
+      // held in registers, in two halves (one arrival per warp each).
+      const uint64_t negm2 = f2_pack(kShift - m_run, kShift - m_run);
+      uint64_t sum2[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int key = 64 * h + 2 * e;
+          const uint64_t x2 = f2_fma(f2_pack(sc[key], sc[key + 1]), scale2, negm2);
+          float x0, x1;
+          f2_unpack(x2, x0, x1);
+          const float p0 = exp2_mufu(x0), p1 = exp2_mufu(x1);
+          sum2[e & 3] = f2_add(sum2[e & 3], f2_pack(p0, p1));
+          pk[e] = pack2<F16>(p0, p1);
+        }
+        tmem_st32(s_col + 32 * h, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(h == 0 ? &bars->p_half[i] : &bars->p_full[i]);
+      }
+      float a0, a1, b0, b1;
+      f2_unpack(f2_add(sum2[0], sum2[1]), a0, a1);
+      f2_unpack(f2_add(sum2[2], sum2[3]), b0, b1);
+      l_run += (a0 + a1) + (b0 + b1);
+    }
+    if (ok && my_n > 0)
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_final[i], 0, wc));
+    if (ok && my_n > 0) {
+      tc_fence_after();
+      const int head = kvh * a.group + r - rp * a.group;
+      const bool row_ok = rp < P && pos < len;
+      const float inv_l = 1.f / l_run;
+      uint16_t* dst = a.o + (row_ok ? (start + pos) * a.o_stride + head * D : 0);
+      float worst = 0.f;  // NaN or infinite if any value of the row is
+      uint32_t rr[32];
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        tmem_ld32(o_col + 32 * c, rr);
+        tmem_wait_ld();
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          v[e] = __uint_as_float(rr[e]) * inv_l;
+          worst = max_nan(worst, fabsf(v[e]));
+        }
+        if (row_ok) {
+          uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            d4[q] = make_uint4(pack2<F16>(v[8 * q], v[8 * q + 1]),
+                               pack2<F16>(v[8 * q + 2], v[8 * q + 3]),
+                               pack2<F16>(v[8 * q + 4], v[8 * q + 5]),
+                               pack2<F16>(v[8 * q + 6], v[8 * q + 7]));
+        }
+      }
+      tc_fence_before();
+      uint32_t again = __ballot_sync(0xffffffffu, row_ok && !(worst <= 3.4028235e38f));
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        plain_row<D, F16>(a, start, __shfl_sync(0xffffffffu, pos, src),
+                          __shfl_sync(0xffffffffu, head, src));
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+bool tmap_heads(CUtensorMap* t, const void* p, bool f16, int D, int heads, int rows,
+                int64_t stride, int box_heads, int box_rows) {
+  const uint64_t d[3] = {(uint64_t)D, (uint64_t)heads, (uint64_t)rows};
+  const uint64_t s[2] = {(uint64_t)D * 2, (uint64_t)stride * 2};
+  const uint32_t b[3] = {64, (uint32_t)box_heads, (uint32_t)box_rows};
+  return make_tmap(t, p, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   3, d, s, b);
+}
+
+template <int D, bool F16>
+cudaError_t run(const h3_prompts* p, const Args& a, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(k_prompt_attention<D, F16>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem_bytes<D>());
+  if (e != cudaSuccess) return e;
+  CUtensorMap tq, tk, tv;
+  if (!tmap_heads(&tq, a.q, F16, D, p->q_heads, p->rows, a.q_stride, a.group, a.tile_pos) ||
+      !tmap_heads(&tk, a.k, F16, D, p->kv_heads, p->rows, a.k_stride, 1, 128) ||
+      !tmap_heads(&tv, a.v, F16, D, p->kv_heads, p->rows, a.v_stride, 1, 128))
+    return cudaErrorInvalidValue;
+  k_prompt_attention<D, F16><<<(unsigned)(p->n_items * p->kv_heads), NUM_THREADS, smem_bytes<D>(),
+                               st>>>(tq, tk, tv, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+h3_status build_prompts(h3_prompts* p, const int32_t* offsets, int n_prompts) {
+  const int P = 128 / (p->q_heads / p->kv_heads);
+  long long count = 0;
+  for (int i = 0; i < n_prompts; ++i)
+    count += ((long long)offsets[i + 1] - offsets[i] + 2 * P - 1) / (2 * P);
+  if (count * p->kv_heads > 0x7fffffffLL) return H3_ERR_SHAPE;
+  p->n_items = (int)count;
+  if (count == 0) return H3_OK;
+  std::vector<int4> items;
+  try {
+    items.reserve(count);
+    for (int i = 0; i < n_prompts; ++i) {
+      const int len = offsets[i + 1] - offsets[i];
+      for (long long pos = 0; pos < len; pos += 2 * P)
+        items.push_back(make_int4(offsets[i], (int)pos, len, 0));
+    }
+    std::stable_sort(items.begin(), items.end(),
+                     [](const int4& x, const int4& y) { return x.y > y.y; });
+  } catch (...) {
+    return H3_ERR_CUDA;
+  }
+  if (cudaMalloc(&p->items, count * sizeof(int4)) != cudaSuccess) return H3_ERR_CUDA;
+  if (cudaMemcpy(p->items, items.data(), count * sizeof(int4), cudaMemcpyHostToDevice) !=
+      cudaSuccess) {
+    cudaFree(p->items);
+    p->items = nullptr;
+    return H3_ERR_CUDA;
+  }
+  return H3_OK;
+}
+
+cudaError_t launch_prompt_attention(const h3_prompts* p, bool f16, const void* q,
+                                    int64_t q_stride, const void* k, int64_t k_stride,
+                                    const void* v, int64_t v_stride, float scale, void* o,
+                                    int64_t o_stride, int* err, cudaStream_t st) {
+  Args a;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.o = static_cast<uint16_t*>(o);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.o_stride = o_stride;
+  a.items = static_cast<const int4*>(p->items);
+  a.kv_heads = p->kv_heads;
+  a.group = p->q_heads / p->kv_heads;
+  a.tile_pos = 128 / a.group;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.err = err;
+  if (p->head_dim == 128) return f16 ? run<128, true>(p, a, st) : run<128, false>(p, a, st);
+  return f16 ? run<64, true>(p, a, st) : run<64, false>(p, a, st);
+}
+
+}  // namespace h3

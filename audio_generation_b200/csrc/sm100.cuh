@@ -221,6 +221,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          | ((uint32_t)(M >> 4) << 24);    // M / 16
 }
 
+// The same with A and B both bf16, or both fp16 (format code 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major,
+                                                     bool b_mn_major, bool bf16) {
+  return idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & (bf16 ? ~0u : ~((1u << 7) | (1u << 10)));
+}
+
 // Instruction descriptor for kind::f8f6f4 with e4m3 A/B (format code 0) and
 // fp32 D: the same fields as kind::f16, with the 8-bit formats.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {

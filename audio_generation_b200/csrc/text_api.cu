@@ -1,5 +1,10 @@
 // C ABI entry points of the text model's operators: argument checks and the
-// library-owned error word. The kernels are in int8_linear.cu.
+// library-owned error word. The kernels are in int8_linear.cu and
+// prompt_attention.cu.
+#include <math.h>
+
+#include <new>
+
 #include "internal.cuh"
 #include "sm100.cuh"
 
@@ -22,6 +27,12 @@ inline h3_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return H3_OK;
   if (e == cudaErrorInvalidValue) return H3_ERR_ARG;
   return H3_ERR_CUDA;
+}
+
+// Rows of `width` 2-byte elements, `stride` apart: aligned, apart, and within
+// the 2^40 bytes a tensor map's stride may have.
+inline bool row_stride_ok(int64_t stride, int64_t width) {
+  return stride >= width && stride % 8 == 0 && stride < (1ll << 38);
 }
 
 inline bool known_type(h3_type t) { return t == H3_BF16 || t == H3_F16 || t == H3_F32; }
@@ -78,6 +89,68 @@ h3_status h3_matmul_int8(int M, int N, int K, const void* a_codes, const float* 
   if (rc != H3_OK) return rc;
   return cuda_status(launch_matmul_int8(M, N, K, a_codes, a_scales, w_codes, w_scales, out_type,
                                         out, out_stride, err, as_stream(stream)));
+}
+
+h3_status h3_prompts_prepare(const int32_t* offsets_host, int n_prompts, int q_heads,
+                             int kv_heads, int head_dim, h3_prompts_t* out) {
+  if (!out) return H3_ERR_ARG;
+  *out = nullptr;
+  if (!offsets_host || n_prompts < 0 || q_heads <= 0 || kv_heads <= 0) return H3_ERR_ARG;
+  if (q_heads % kv_heads != 0 || q_heads / kv_heads > 128 || (head_dim != 64 && head_dim != 128))
+    return H3_ERR_SHAPE;
+  if (offsets_host[0] < 0) return H3_ERR_LAYOUT;
+  for (int i = 0; i < n_prompts; ++i)
+    if (offsets_host[i + 1] < offsets_host[i]) return H3_ERR_LAYOUT;
+  h3_prompts* p = new (std::nothrow) h3_prompts();
+  if (!p) return H3_ERR_CUDA;
+  p->q_heads = q_heads;
+  p->kv_heads = kv_heads;
+  p->head_dim = head_dim;
+  p->rows = offsets_host[n_prompts];
+  h3_status rc = cudaGetDevice(&p->device) == cudaSuccess ? H3_OK : H3_ERR_CUDA;
+  if (rc == H3_OK) rc = build_prompts(p, offsets_host, n_prompts);
+  if (rc != H3_OK) {
+    delete p;
+    return rc;
+  }
+  *out = p;
+  return H3_OK;
+}
+
+void h3_prompts_destroy(h3_prompts_t p) {
+  if (!p) return;
+  if (p->items) {
+    int current = 0;
+    const bool known = cudaGetDevice(&current) == cudaSuccess;
+    if (known && current != p->device) cudaSetDevice(p->device);
+    cudaDeviceSynchronize();
+    cudaFree(p->items);
+    if (known && current != p->device) cudaSetDevice(current);
+  }
+  delete p;
+}
+
+h3_status h3_prompt_attention(h3_prompts_t p, h3_type type, const void* q, int64_t q_stride,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                              float scale, void* o, int64_t o_stride, h3_stream_t stream) {
+  if (!p || (type != H3_BF16 && type != H3_F16)) return H3_ERR_ARG;
+  if (!(scale > 0.f) || !isfinite(scale)) return H3_ERR_ARG;
+  const int64_t qw = (int64_t)p->q_heads * p->head_dim, kw = (int64_t)p->kv_heads * p->head_dim;
+  if (!row_stride_ok(q_stride, qw) || !row_stride_ok(o_stride, qw) ||
+      !row_stride_ok(k_stride, kw) || !row_stride_ok(v_stride, kw))
+    return H3_ERR_SHAPE;
+  if (p->n_items == 0) return H3_OK;
+  if (!q || !k || !v || !o) return H3_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return H3_ERR_ALIGN;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return H3_ERR_CUDA;
+  if (device != p->device) return H3_ERR_ARG;
+  int* err = nullptr;
+  const h3_status rc = text_error_word(&err);
+  if (rc != H3_OK) return rc;
+  return cuda_status(launch_prompt_attention(p, type == H3_F16, q, q_stride, k, k_stride, v,
+                                             v_stride, scale, o, o_stride, err,
+                                             as_stream(stream)));
 }
 
 }  // extern "C"

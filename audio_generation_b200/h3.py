@@ -148,6 +148,10 @@ _SIGNATURES = {
     "h3_quantize_int8_rows": (_i, [_i, _i, _i, _vp, _i64, _vp, _vp, _vp]),
     "h3_matmul_int8": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _i64, _vp]),
     "h3_text_error": (_i, []),
+    "h3_prompts_prepare": (_i, [_vp, _i, _i, _i, _i, ctypes.POINTER(_vp)]),
+    "h3_prompts_destroy": (None, [_vp]),
+    "h3_prompt_attention": (_i, [_vp, _i, _vp, _i64, _vp, _i64, _vp, _i64, ctypes.c_float, _vp,
+                                 _i64, _vp]),
     "h3_stack_forward": (_i, [ctypes.POINTER(h3_dims), ctypes.POINTER(h3_block_weights), _i, _vp,
                               _vp, _vp, _i, _vp, _sz, _vp]),
 }
@@ -551,3 +555,45 @@ def h3_matmul_int8(M: int, N: int, K: int, a_codes, a_scales, w_codes, w_scales,
 
 def h3_text_error() -> int:
     return lib().h3_text_error()
+
+
+class Prompts:
+    """Owns an h3_prompts_t; released by close() or garbage collection."""
+
+    def __init__(self, handle: int, rows: int):
+        self.handle = handle
+        self.rows = rows
+
+    def close(self) -> None:
+        if self.handle:
+            lib().h3_prompts_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def h3_prompts_prepare(offsets: Sequence[int], q_heads: int, kv_heads: int,
+                       head_dim: int) -> Prompts:
+    """offsets: the n_prompts + 1 row numbers, host integers."""
+    if len(offsets) == 0:
+        raise H3Error(H3_ERR_ARG, "h3_prompts_prepare")
+    arr = (ctypes.c_int32 * len(offsets))(*offsets)
+    out = ctypes.c_void_p()
+    _check(lib().h3_prompts_prepare(arr, len(offsets) - 1, q_heads, kv_heads, head_dim,
+                                    ctypes.byref(out)), "h3_prompts_prepare")
+    return Prompts(out.value, int(arr[len(offsets) - 1]))
+
+
+def h3_prompts_destroy(prompts: Prompts) -> None:
+    prompts.close()
+
+
+def h3_prompt_attention(prompts: Prompts, dtype, q, q_stride: int, k, k_stride: int, v,
+                        v_stride: int, scale: float, o, o_stride: int, stream=None) -> None:
+    _check(lib().h3_prompt_attention(prompts.handle, _type(dtype), _ptr(q), q_stride, _ptr(k),
+                                     k_stride, _ptr(v), v_stride, scale, _ptr(o), o_stride,
+                                     _stream(stream)), "h3_prompt_attention")

@@ -570,6 +570,40 @@ H3_API h3_status h3_matmul_int8(int M, int N, int K, const void* a_codes, const 
                                 const void* w_codes, const float* w_scales, h3_type out_type,
                                 void* out, int64_t out_stride, h3_stream_t stream);
 
+/* ---- the text model: causal attention over packed prompts ---- */
+
+typedef struct h3_prompts* h3_prompts_t;
+
+/* The work list of one batch of prompts packed into rows: prompt i holds rows
+ * [offsets_host[i], offsets_host[i + 1]) (a HOST array of n_prompts + 1 row
+ * numbers that never decrease, the first >= 0; read during the call only). One
+ * object serves every layer that runs on the batch. q_heads % kv_heads == 0 with
+ * at most 128 query heads per kv head; head_dim 64 or 128. H3_ERR_LAYOUT for
+ * offsets that decrease or start below 0. Allocates device memory on the current
+ * device and copies the list there (synchronous; not inside a stream capture). */
+H3_API h3_status h3_prompts_prepare(const int32_t* offsets_host, int n_prompts, int q_heads,
+                                    int kv_heads, int head_dim, h3_prompts_t* out);
+
+/* Release a prompts object (synchronises its device first). NULL is ignored. A
+ * captured graph that uses it must not run any more. */
+H3_API void h3_prompts_destroy(h3_prompts_t prompts);
+
+/* o[i, h] = sum over j <= i of softmax_j(scale * q[i, h] . k[j, g]) v[j, g], i
+ * and j rows of the same prompt, g = h / (q_heads / kv_heads). q [rows, q_heads,
+ * head_dim], k and v [rows, kv_heads, head_dim], o like q, of `type` (H3_BF16 or
+ * H3_F16), heads contiguous inside a row, each with its own row stride in
+ * elements (>= heads * head_dim, a multiple of 8), so that slices of one
+ * projection's output can be given as they are. scale > 0, finite. o may not
+ * overlap the inputs. Rows of o outside every prompt are left as they were. Sums
+ * and softmax statistics are float32; the softmax weights are rounded to `type`
+ * before the product with v. What a row holds does not depend on the values of
+ * rows it does not attend, infinities and NaN included. Runs on the device of
+ * the prompts object, which must be current (else H3_ERR_ARG). Enqueues. */
+H3_API h3_status h3_prompt_attention(h3_prompts_t prompts, h3_type type, const void* q,
+                                     int64_t q_stride, const void* k, int64_t k_stride,
+                                     const void* v, int64_t v_stride, float scale, void* o,
+                                     int64_t o_stride, h3_stream_t stream);
+
 /* Read and clear the current device's error word of the text operators
  * (synchronises the device): H3_OK, or H3_ERR_TIMEOUT if a bounded in-kernel
  * wait ran out since the last read. */

@@ -49,3 +49,31 @@ def test_binding_names_types_by_torch_dtype():
     assert h3._type(torch.float64) == -1
     with pytest.raises(h3.H3Error):
         h3.h3_quantize_int8_rows(torch.float64, 1, 16, 256, 16, 256, 256, stream=0)
+
+
+def _prepare(offsets=(0, 5), n=None, q=8, kv=2, D=128, out=True):
+    arr = (ctypes.c_int32 * len(offsets))(*offsets)
+    p = ctypes.c_void_p()
+    return h3.lib().h3_prompts_prepare(arr, len(offsets) - 1 if n is None else n, q, kv, D,
+                                       ctypes.byref(p) if out else None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(out=False), h3.H3_ERR_ARG), (dict(n=-1), h3.H3_ERR_ARG), (dict(q=0), h3.H3_ERR_ARG),
+    (dict(kv=0), h3.H3_ERR_ARG), (dict(kv=3), h3.H3_ERR_SHAPE),
+    (dict(q=258, kv=2), h3.H3_ERR_SHAPE), (dict(D=96), h3.H3_ERR_SHAPE),
+    (dict(D=0), h3.H3_ERR_SHAPE), (dict(offsets=(-1, 5)), h3.H3_ERR_LAYOUT),
+    (dict(offsets=(0, 5, 4)), h3.H3_ERR_LAYOUT),
+    (dict(offsets=(0, 2147483647, -2147483648)), h3.H3_ERR_LAYOUT)])
+def test_prompts_refusals(kw, status):
+    assert _prepare(**kw) == status
+
+
+def test_prompts_null_arguments():
+    L = h3.lib()
+    p = ctypes.c_void_p()
+    assert L.h3_prompts_prepare(None, 0, 8, 2, 128, ctypes.byref(p)) == h3.H3_ERR_ARG
+    L.h3_prompts_destroy(None)
+    assert L.h3_prompt_attention(None, 0, P, 8, P, 8, P, 8, 1.0, P, 8, None) == h3.H3_ERR_ARG
+    with pytest.raises(h3.H3Error):
+        h3.h3_prompts_prepare([], 8, 2, 128)
