@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "host_util.cuh"
+#include "int8_code.cuh"
 #include "internal.cuh"
 #include "sm100.cuh"
 #include "softmax.cuh"
@@ -18,69 +19,7 @@ namespace {
 // keeps its row in registers between the two passes over it (maximum, codes),
 // so a row is read once; rows too long for that (K > 65536 in 16 bits) are
 // read twice.
-//
-// The code is the nearest integer to the exact quotient x / scale. A product
-// with the rounded reciprocal is within 2^-22 of the quotient relative to it,
-// below 4e-5 in absolute terms for |quotient| <= 127.001; only elements
-// within 1e-4 of a tie take the division, in 64 bits, where the quotient of
-// two 32-bit floats cannot round onto a tie that it is not on (it is either on
-// the tie or 2^-25 of it away).
-
-constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
-
-struct RowScale {
-  float scale, inv;
-  bool slow;  // the reciprocal is not a normal float: divide everywhere
-};
-
-__device__ __forceinline__ RowScale row_scale_of(float amax) {
-  RowScale s;
-  s.scale = amax / 127.f;
-  if (s.scale == 0.f) s.scale = 1.f;  // zeros, or a maximum below the smallest scale
-  s.inv = 1.f / s.scale;
-  s.slow = s.scale < 1e-30f;
-  return s;
-}
-
-__device__ __noinline__ int code_by_division(float x, float scale) {
-  const double q = rint((double)x / (double)scale);
-  return (int)fmin(fmax(q, -127.0), 127.0);
-}
-
-// Low byte of the result is the code.
-__device__ __forceinline__ uint32_t code_of(float x, const RowScale& s) {
-  const float r = fmaf(x, s.inv, kMagic);
-  const float d = fmaf(x, s.inv, kMagic - r);  // quotient - rounded quotient
-  if (s.slow || fabsf(d) > 0.4999f) return (uint32_t)code_by_division(x, s.scale);
-  return __float_as_uint(r);
-}
-
-__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
-}
-
-// 16 bytes of a row as floats: 8 elements of 2 bytes, or 4 of 4.
-template <h3_type T>
-struct Vec {
-  static constexpr int N = T == H3_F32 ? 4 : 8;
-};
-template <h3_type T>
-__device__ __forceinline__ void unpack(const uint4& u, float* v) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (T == H3_BF16) {
-      v[2 * i] = bf16lo(w[i]);
-      v[2 * i + 1] = bf16hi(w[i]);
-    } else if constexpr (T == H3_F16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    } else {
-      v[i] = __uint_as_float(w[i]);
-    }
-  }
-}
+// The rounding is in int8_code.cuh.
 
 template <h3_type T>
 __device__ __forceinline__ float amax_of(const uint4& u, float m) {
@@ -145,12 +84,14 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G)
     for (int i = t; i < nvec; i += G) m = amax_of<T>(xr[i], m);
   }
   m = group_max<G>(m);
-  if (!(m <= 3.4028235e38f)) {  // an infinity or a NaN in the row
+  if (!(m <= kMaxFinite)) {  // an infinity or a NaN in the row
     for (int i = t; i < K / 4; i += G) reinterpret_cast<uint32_t*>(cr)[i] = 0;
     if (t == 0) scales[row] = __int_as_float(0x7fc00000);
     return;
   }
-  const RowScale s = row_scale_of(m);
+  float scale = m / 127.f;
+  if (scale == 0.f) scale = 1.f;  // zeros, or a maximum below the smallest scale
+  const RowScale s = row_scale(scale);
   if (t == 0) scales[row] = s.scale;
   if constexpr (NV > 0) {
 #pragma unroll

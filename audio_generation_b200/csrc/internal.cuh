@@ -282,6 +282,19 @@ cudaError_t launch_prompt_attention(const h3_prompts* p, bool f16, const void* q
                                     const void* v, int64_t v_stride, float scale, void* o,
                                     int64_t o_stride, int* err, cudaStream_t st);
 
+// The 8-bit key / value cache (kv_cache.cu); arguments checked.
+cudaError_t launch_kv_cache_store(const h3_kv_cache& c, int n_seq, int max_new,
+                                  const int32_t* table, int width, const int32_t* lengths,
+                                  const int32_t* offsets, bool f16, int rows, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride, int* err,
+                                  cudaStream_t st);
+size_t cache_attention_workspace(const h3_kv_cache& c, int n_seq, int q_heads, int width);
+cudaError_t launch_cache_attention(const h3_kv_cache& c, int n_seq, int q_heads,
+                                   const int32_t* table, int width, const int32_t* lengths,
+                                   bool f16, const void* q, int64_t q_stride, float scale,
+                                   void* o, int64_t o_stride, void* ws, int* err,
+                                   cudaStream_t st);
+
 // Shape checks shared by the entry points (H3_OK or the status to return).
 h3_status check_dims(const h3_dims* d);
 

@@ -1,6 +1,6 @@
 // C ABI entry points of the text model's operators: argument checks and the
-// library-owned error word. The kernels are in int8_linear.cu and
-// prompt_attention.cu.
+// library-owned error word. The kernels are in int8_linear.cu,
+// prompt_attention.cu and kv_cache.cu.
 #include <math.h>
 
 #include <new>
@@ -11,8 +11,9 @@
 namespace h3 {
 namespace {
 
-// A wait that runs out in a text operator records H3_DEVERR_TIMEOUT here (one
-// int per GPU that loads the library); h3_text_error reads and clears it.
+// A wait that runs out in a text operator records H3_DEVERR_TIMEOUT here, a
+// device table that makes no sense H3_DEVERR_LAYOUT (one int per GPU that loads
+// the library); h3_text_error reads and clears it.
 static __device__ int g_text_err;
 
 SymbolAddressCache g_text_err_cache;
@@ -37,6 +38,29 @@ inline bool row_stride_ok(int64_t stride, int64_t width) {
 
 inline bool known_type(h3_type t) { return t == H3_BF16 || t == H3_F16 || t == H3_F32; }
 
+h3_status check_cache(const h3_kv_cache* c) {
+  if (!c || c->n_blocks < 0 || c->kv_heads <= 0) return H3_ERR_ARG;
+  if (c->block_tokens != 32 && c->block_tokens != 64 && c->block_tokens != 128)
+    return H3_ERR_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 128) return H3_ERR_SHAPE;
+  return H3_OK;
+}
+
+// The parts that a call with work to do dereferences.
+h3_status check_cache_pointers(const h3_kv_cache* c) {
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return H3_ERR_ARG;
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) ||
+      !aligned16(c->v_scales))
+    return H3_ERR_ALIGN;
+  return H3_OK;
+}
+
+// A table of `width` blocks per sequence whose token numbers fit an int.
+h3_status check_table(const h3_kv_cache* c, int width) {
+  if (width < 0) return H3_ERR_ARG;
+  return (long long)width * c->block_tokens > 0x7fffffffLL ? H3_ERR_SHAPE : H3_OK;
+}
+
 }  // namespace
 
 h3_status text_error_word(int** out) {
@@ -59,7 +83,7 @@ h3_status h3_text_error(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return H3_ERR_CUDA;
   if (cudaMemcpy(&v, p, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return H3_ERR_CUDA;
   if (v != 0 && cudaMemset(p, 0, 4) != cudaSuccess) return H3_ERR_CUDA;
-  return v == 0 ? H3_OK : H3_ERR_TIMEOUT;
+  return v == 0 ? H3_OK : v == H3_DEVERR_LAYOUT ? H3_ERR_LAYOUT : H3_ERR_TIMEOUT;
 }
 
 h3_status h3_quantize_int8_rows(h3_type type, int rows, int K, const void* x, int64_t x_stride,
@@ -151,6 +175,72 @@ h3_status h3_prompt_attention(h3_prompts_t p, h3_type type, const void* q, int64
   return cuda_status(launch_prompt_attention(p, type == H3_F16, q, q_stride, k, k_stride, v,
                                              v_stride, scale, o, o_stride, err,
                                              as_stream(stream)));
+}
+
+h3_status h3_kv_cache_store(const h3_kv_cache* cache, int n_seq, int max_new,
+                            const int32_t* block_table, int table_width, const int32_t* lengths,
+                            const int32_t* offsets, h3_type type, int rows, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride,
+                            h3_stream_t stream) {
+  h3_status rc = check_cache(cache);
+  if (rc != H3_OK) return rc;
+  if (n_seq < 0 || max_new < 0 || rows < 0 || (type != H3_BF16 && type != H3_F16))
+    return H3_ERR_ARG;
+  if ((rc = check_table(cache, table_width)) != H3_OK) return rc;
+  const int64_t w = (int64_t)cache->kv_heads * cache->head_dim;
+  if (!row_stride_ok(k_stride, w) || !row_stride_ok(v_stride, w)) return H3_ERR_SHAPE;
+  if (n_seq == 0 || max_new == 0 || rows == 0) return H3_OK;
+  if (table_width == 0) return H3_ERR_SHAPE;  // new tokens, and no block to hold them
+  if (!block_table || !lengths || !offsets || !k || !v) return H3_ERR_ARG;
+  if ((rc = check_cache_pointers(cache)) != H3_OK) return rc;
+  if (!aligned16(block_table) || !aligned16(lengths) || !aligned16(offsets) || !aligned16(k) ||
+      !aligned16(v))
+    return H3_ERR_ALIGN;
+  int* err = nullptr;
+  if ((rc = text_error_word(&err)) != H3_OK) return rc;
+  return cuda_status(launch_kv_cache_store(*cache, n_seq, max_new, block_table, table_width,
+                                           lengths, offsets, type == H3_F16, rows, k, k_stride, v,
+                                           v_stride, err, as_stream(stream)));
+}
+
+size_t h3_cache_attention_workspace_size(const h3_kv_cache* cache, int n_seq, int q_heads,
+                                         int table_width) {
+  if (check_cache(cache) != H3_OK || n_seq <= 0 || q_heads <= 0 ||
+      q_heads % cache->kv_heads != 0 || check_table(cache, table_width) != H3_OK ||
+      table_width == 0)
+    return 0;
+  return cache_attention_workspace(*cache, n_seq, q_heads, table_width);
+}
+
+h3_status h3_cache_attention(const h3_kv_cache* cache, int n_seq, int q_heads,
+                             const int32_t* block_table, int table_width, const int32_t* lengths,
+                             h3_type type, const void* q, int64_t q_stride, float scale, void* o,
+                             int64_t o_stride, void* ws, size_t ws_bytes, h3_stream_t stream) {
+  h3_status rc = check_cache(cache);
+  if (rc != H3_OK) return rc;
+  if (n_seq < 0 || q_heads <= 0 || (type != H3_BF16 && type != H3_F16) || !(scale > 0.f) ||
+      !isfinite(scale))
+    return H3_ERR_ARG;
+  if ((rc = check_table(cache, table_width)) != H3_OK) return rc;
+  const int64_t w = (int64_t)q_heads * cache->head_dim;
+  if (q_heads % cache->kv_heads != 0 || !row_stride_ok(q_stride, w) ||
+      !row_stride_ok(o_stride, w))
+    return H3_ERR_SHAPE;
+  if (n_seq == 0) return H3_OK;
+  if (table_width == 0) return H3_ERR_SHAPE;
+  if (!block_table || !lengths || !q || !o) return H3_ERR_ARG;
+  if ((rc = check_cache_pointers(cache)) != H3_OK) return rc;
+  const size_t need = cache_attention_workspace(*cache, n_seq, q_heads, table_width);
+  if (ws_bytes < need) return H3_ERR_WORKSPACE;
+  if (need > 0 && !ws) return H3_ERR_ARG;
+  if (!aligned16(block_table) || !aligned16(lengths) || !aligned16(q) || !aligned16(o) ||
+      (need > 0 && !aligned16(ws)))
+    return H3_ERR_ALIGN;
+  int* err = nullptr;
+  if ((rc = text_error_word(&err)) != H3_OK) return rc;
+  return cuda_status(launch_cache_attention(*cache, n_seq, q_heads, block_table, table_width,
+                                            lengths, type == H3_F16, q, q_stride, scale, o,
+                                            o_stride, ws, err, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -84,9 +84,15 @@ class h3_ulysses_peers(ctypes.Structure):
                 ("v", ctypes.c_void_p * H3_MAX_RANKS), ("o", ctypes.c_void_p * H3_MAX_RANKS)]
 
 
+class h3_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_blocks", "block_tokens", "kv_heads", "head_dim")
+                ] + [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _vp, _i, _sz, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
+_pc = ctypes.POINTER(h3_kv_cache)
 _SIGNATURES = {
     "h3_status_string": (ctypes.c_char_p, [_i]),
     "h3_abi_version": (_i, []),
@@ -148,6 +154,11 @@ _SIGNATURES = {
     "h3_quantize_int8_rows": (_i, [_i, _i, _i, _vp, _i64, _vp, _vp, _vp]),
     "h3_matmul_int8": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp, _i64, _vp]),
     "h3_text_error": (_i, []),
+    "h3_kv_cache_store": (_i, [_pc, _i, _i, _vp, _i, _vp, _vp, _i, _i, _vp, _i64, _vp, _i64,
+                               _vp]),
+    "h3_cache_attention_workspace_size": (_sz, [_pc, _i, _i, _i]),
+    "h3_cache_attention": (_i, [_pc, _i, _i, _vp, _i, _vp, _i, _vp, _i64, ctypes.c_float, _vp,
+                                _i64, _vp, _sz, _vp]),
     "h3_prompts_prepare": (_i, [_vp, _i, _i, _i, _i, ctypes.POINTER(_vp)]),
     "h3_prompts_destroy": (None, [_vp]),
     "h3_prompt_attention": (_i, [_vp, _i, _vp, _i64, _vp, _i64, _vp, _i64, ctypes.c_float, _vp,
@@ -597,3 +608,40 @@ def h3_prompt_attention(prompts: Prompts, dtype, q, q_stride: int, k, k_stride: 
     _check(lib().h3_prompt_attention(prompts.handle, _type(dtype), _ptr(q), q_stride, _ptr(k),
                                      k_stride, _ptr(v), v_stride, scale, _ptr(o), o_stride,
                                      _stream(stream)), "h3_prompt_attention")
+
+
+def make_kv_cache(k_codes, v_codes, k_scales, v_scales) -> h3_kv_cache:
+    """The cache descriptor of a pool's tensors, sizes from k_codes [n_blocks,
+    kv_heads, block_tokens, head_dim] (the caller keeps the tensors)."""
+    n_blocks, kv_heads, block_tokens, head_dim = k_codes.shape
+    if tuple(v_codes.shape) != (n_blocks, kv_heads, head_dim, block_tokens):
+        raise H3Error(H3_ERR_SHAPE, "make_kv_cache")
+    return h3_kv_cache(n_blocks, block_tokens, kv_heads, head_dim, _ptr(k_codes), _ptr(v_codes),
+                       _ptr(k_scales), _ptr(v_scales))
+
+
+def h3_kv_cache_store(cache: h3_kv_cache, n_seq: int, max_new: int, block_table,
+                      table_width: int, lengths, offsets, dtype, k, k_stride: int, v,
+                      v_stride: int, rows: Optional[int] = None, stream=None) -> None:
+    """rows: the rows of k and v (from k's first dimension by default)."""
+    if rows is None:
+        rows = int(k.shape[0])
+    _check(lib().h3_kv_cache_store(ctypes.byref(cache), n_seq, max_new, _ptr(block_table),
+                                   table_width, _ptr(lengths), _ptr(offsets), _type(dtype), rows,
+                                   _ptr(k), k_stride, _ptr(v), v_stride, _stream(stream)),
+           "h3_kv_cache_store")
+
+
+def h3_cache_attention_workspace_size(cache: h3_kv_cache, n_seq: int, q_heads: int,
+                                      table_width: int) -> int:
+    return int(lib().h3_cache_attention_workspace_size(ctypes.byref(cache), n_seq, q_heads,
+                                                       table_width))
+
+
+def h3_cache_attention(cache: h3_kv_cache, n_seq: int, q_heads: int, block_table,
+                       table_width: int, lengths, dtype, q, q_stride: int, scale: float, o,
+                       o_stride: int, ws, ws_bytes: int, stream=None) -> None:
+    _check(lib().h3_cache_attention(ctypes.byref(cache), n_seq, q_heads, _ptr(block_table),
+                                    table_width, _ptr(lengths), _type(dtype), _ptr(q), q_stride,
+                                    scale, _ptr(o), o_stride, _ptr(ws), ws_bytes,
+                                    _stream(stream)), "h3_cache_attention")

@@ -604,9 +604,73 @@ H3_API h3_status h3_prompt_attention(h3_prompts_t prompts, h3_type type, const v
                                      const void* v, int64_t v_stride, float scale, void* o,
                                      int64_t o_stride, h3_stream_t stream);
 
+/* ---- the text model: an 8-bit key / value cache ---- */
+
+/* A pool of cache blocks, each block_tokens (32, 64 or 128) tokens of one
+ * sequence for all kv heads, head_dim 64 or 128. DEVICE pointers:
+ *   k_codes  [n_blocks, kv_heads, block_tokens, head_dim] int8
+ *   v_codes  [n_blocks, kv_heads, head_dim, block_tokens] int8 (V transposed)
+ *   k_scales, v_scales [n_blocks, kv_heads] f32: a code stands for code * scale.
+ * Which blocks hold a sequence is the caller's block table [n_seq, table_width]
+ * i32: token p of sequence s is in slot p % block_tokens of block
+ * table[s, p / block_tokens]; entries past a sequence's tokens are not read.
+ * Sequences may share blocks that are only read. What a block held before its
+ * first token is stored does not matter (nothing needs to start at zero). */
+typedef struct {
+  int n_blocks, block_tokens, kv_heads, head_dim;
+  void* k_codes;
+  void* v_codes;
+  float* k_scales;
+  float* v_scales;
+} h3_kv_cache;
+
+/* New tokens enter the cache: rows [offsets[s], offsets[s + 1]) of k and v
+ * ([rows, kv_heads, head_dim] of `type` H3_BF16 or H3_F16, row strides in elements
+ * as for h3_prompt_attention) become the tokens lengths[s], lengths[s] + 1, ...
+ * of sequence s; lengths [n_seq] and offsets [n_seq + 1] i32 are DEVICE arrays,
+ * lengths as before the call (the caller raises them afterwards). Per block and
+ * kv head: scale = max|new values| / 127 in float32, or the block's scale if it
+ * holds earlier tokens and that is larger; code = value / scale rounded to
+ * nearest, ties to even (the exact quotient decides). If the scale of a block
+ * with earlier tokens grows, their codes are rounded again to the same values
+ * under the new scale. A block of zeros has scale 0. An infinity or a NaN marks its block and kv head:
+ * scale NaN, codes 0 (attention over it gives NaN). max_new: the largest number
+ * of new tokens of one sequence; `rows`: the rows of k and v. A sequence whose
+ * lengths or offsets are negative, whose new tokens are more than max_new, leave
+ * `rows` or do not fit table_width blocks is not stored, nor is a token whose
+ * table entry names no block: both record an error (h3_text_error,
+ * H3_ERR_LAYOUT). A block that is written must be in one sequence's table only.
+ * Enqueues. */
+H3_API h3_status h3_kv_cache_store(const h3_kv_cache* cache, int n_seq, int max_new,
+                                   const int32_t* block_table, int table_width,
+                                   const int32_t* lengths, const int32_t* offsets, h3_type type,
+                                   int rows, const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, h3_stream_t stream);
+
+/* Attention of one query token per sequence over its cached tokens (the single-
+ * token form of h3_prompt_attention): o[s, h] = sum over p < lengths[s] of
+ * softmax_p(scale * q[s, h] . k[p, g]) v[p, g], k and v the values the cache
+ * stands for, g = h / (q_heads / kv_heads). lengths as of now, the query's own
+ * token included if it has been stored. q, o [n_seq, q_heads, head_dim] of `type`
+ * (H3_BF16 or H3_F16) with row strides in elements. A sequence of length 0 gets
+ * zeros. scale > 0, finite; q_heads % kv_heads == 0. A length that is negative
+ * or past the table is limited to it, and a table entry that names no block
+ * counts as tokens that are not there: both record an error (h3_text_error,
+ * H3_ERR_LAYOUT). ws: h3_cache_attention_workspace_size bytes (0 for few tokens),
+ * used only during the call's work: calls that overlap on the GPU need one each.
+ * The result does not depend on the order in which the GPU runs things. Enqueues. */
+H3_API size_t h3_cache_attention_workspace_size(const h3_kv_cache* cache, int n_seq, int q_heads,
+                                                int table_width);
+H3_API h3_status h3_cache_attention(const h3_kv_cache* cache, int n_seq, int q_heads,
+                                    const int32_t* block_table, int table_width,
+                                    const int32_t* lengths, h3_type type, const void* q,
+                                    int64_t q_stride, float scale, void* o, int64_t o_stride,
+                                    void* ws, size_t ws_bytes, h3_stream_t stream);
+
 /* Read and clear the current device's error word of the text operators
- * (synchronises the device): H3_OK, or H3_ERR_TIMEOUT if a bounded in-kernel
- * wait ran out since the last read. */
+ * (synchronises the device): H3_OK, H3_ERR_TIMEOUT if a bounded in-kernel wait
+ * ran out since the last read, or H3_ERR_LAYOUT if a call met lengths, offsets
+ * or block tables that make no sense. */
 H3_API h3_status h3_text_error(void);
 
 #ifdef __cplusplus

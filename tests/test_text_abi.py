@@ -77,3 +77,81 @@ def test_prompts_null_arguments():
     assert L.h3_prompt_attention(None, 0, P, 8, P, 8, P, 8, 1.0, P, 8, None) == h3.H3_ERR_ARG
     with pytest.raises(h3.H3Error):
         h3.h3_prompts_prepare([], 8, 2, 128)
+
+
+def _cache(n_blocks=4, block=64, kv=2, D=128, k=256, v=256, ks=256, vs=256):
+    return h3.h3_kv_cache(n_blocks, block, kv, D, k, v, ks, vs)
+
+
+_BAD_CACHES = [
+    (dict(n_blocks=-1), h3.H3_ERR_ARG), (dict(kv=0), h3.H3_ERR_ARG),
+    (dict(block=16), h3.H3_ERR_SHAPE), (dict(block=0), h3.H3_ERR_SHAPE),
+    (dict(block=96), h3.H3_ERR_SHAPE), (dict(D=32), h3.H3_ERR_SHAPE),
+    (dict(k=None), h3.H3_ERR_ARG), (dict(v=None), h3.H3_ERR_ARG), (dict(ks=None), h3.H3_ERR_ARG),
+    (dict(vs=None), h3.H3_ERR_ARG), (dict(k=264), h3.H3_ERR_ALIGN), (dict(v=264), h3.H3_ERR_ALIGN),
+    (dict(ks=264), h3.H3_ERR_ALIGN), (dict(vs=264), h3.H3_ERR_ALIGN)]
+
+
+def _store(cache=None, n=2, most=3, table=P, width=4, lengths=P, offsets=P, type=h3.H3_BF16, rows=6,
+           k=P, ks=256, v=P, vs=256):
+    return h3.lib().h3_kv_cache_store(ctypes.byref(cache or _cache()), n, most, table, width,
+                                      lengths, offsets, type, rows, k, ks, v, vs, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=-1), h3.H3_ERR_ARG), (dict(most=-1), h3.H3_ERR_ARG), (dict(rows=-1), h3.H3_ERR_ARG),
+    (dict(type=h3.H3_F32), h3.H3_ERR_ARG), (dict(type=9), h3.H3_ERR_ARG),
+    (dict(width=-1), h3.H3_ERR_ARG), (dict(width=0), h3.H3_ERR_SHAPE),
+    (dict(width=1 << 26), h3.H3_ERR_SHAPE), (dict(ks=248), h3.H3_ERR_SHAPE),
+    (dict(vs=260), h3.H3_ERR_SHAPE), (dict(table=None), h3.H3_ERR_ARG),
+    (dict(lengths=None), h3.H3_ERR_ARG), (dict(offsets=None), h3.H3_ERR_ARG),
+    (dict(k=None), h3.H3_ERR_ARG), (dict(v=None), h3.H3_ERR_ARG), (dict(k=ODD), h3.H3_ERR_ALIGN),
+    (dict(v=ODD), h3.H3_ERR_ALIGN), (dict(table=ODD), h3.H3_ERR_ALIGN),
+    (dict(lengths=ODD), h3.H3_ERR_ALIGN), (dict(offsets=ODD), h3.H3_ERR_ALIGN),
+    (dict(n=0, table=None), h3.H3_OK), (dict(most=0, k=None), h3.H3_OK),
+    (dict(rows=0, k=None), h3.H3_OK)])
+def test_store_refusals(kw, status):
+    assert _store(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", _BAD_CACHES)
+def test_bad_caches(kw, status):
+    assert _store(cache=_cache(**kw)) == status
+    assert _attend(cache=_cache(**kw), ws_bytes=1 << 40) == status
+
+
+def _attend(cache=None, n=2, q_heads=8, table=P, width=4, lengths=P, type=h3.H3_F16, q=P, qs=1024,
+            scale=0.1, o=P, os=1024, ws=P, ws_bytes=1 << 30):
+    return h3.lib().h3_cache_attention(ctypes.byref(cache or _cache()), n, q_heads, table, width,
+                                       lengths, type, q, qs, scale, o, os, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=-1), h3.H3_ERR_ARG), (dict(q_heads=0), h3.H3_ERR_ARG),
+    (dict(type=h3.H3_F32), h3.H3_ERR_ARG), (dict(scale=0.0), h3.H3_ERR_ARG),
+    (dict(scale=-0.1), h3.H3_ERR_ARG), (dict(scale=float("nan")), h3.H3_ERR_ARG),
+    (dict(scale=float("inf")), h3.H3_ERR_ARG), (dict(width=-1), h3.H3_ERR_ARG),
+    (dict(width=0), h3.H3_ERR_SHAPE), (dict(width=1 << 27), h3.H3_ERR_SHAPE),
+    (dict(q_heads=7, qs=896, os=896), h3.H3_ERR_SHAPE), (dict(qs=1016), h3.H3_ERR_SHAPE),
+    (dict(os=1028), h3.H3_ERR_SHAPE), (dict(table=None), h3.H3_ERR_ARG),
+    (dict(lengths=None), h3.H3_ERR_ARG), (dict(q=None), h3.H3_ERR_ARG),
+    (dict(o=None), h3.H3_ERR_ARG), (dict(ws=None), h3.H3_ERR_ARG),
+    (dict(ws_bytes=16), h3.H3_ERR_WORKSPACE), (dict(q=ODD), h3.H3_ERR_ALIGN),
+    (dict(o=ODD), h3.H3_ERR_ALIGN), (dict(ws=ODD), h3.H3_ERR_ALIGN),
+    (dict(table=ODD), h3.H3_ERR_ALIGN), (dict(lengths=ODD), h3.H3_ERR_ALIGN),
+    (dict(n=0, q=None), h3.H3_OK)])
+def test_cache_attention_refusals(kw, status):
+    assert _attend(**kw) == status
+
+
+def test_cache_attention_workspace_size():
+    c = _cache()
+    size = h3.h3_cache_attention_workspace_size
+    assert size(c, 1, 8, 1) == 0 and size(c, 0, 8, 9) == 0 and size(c, 1, 7, 9) == 0
+    assert size(c, 2, 8, 4) > 0
+    # a partial sum of 128 floats and two statistics per head and range at most
+    for n, w in ((1, 63), (40, 375)):
+        assert 0 < size(c, n, 8, w) <= n * 8 * w * (128 * 4 + 8) + 512
+    with pytest.raises(h3.H3Error):
+        import torch
+        h3.make_kv_cache(torch.zeros(1, 1, 32, 64), torch.zeros(1, 1, 32, 64), None, None)
