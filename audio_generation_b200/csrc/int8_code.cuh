@@ -1,9 +1,9 @@
 // Rounding to int8 codes, shared by the kernels that quantize.
 //
 // The code is the nearest integer to the exact quotient x / scale, ties to even.
-// A product with the rounded reciprocal is within 2^-22 of the quotient
-// relative to it, below 4e-5 in absolute terms for |quotient| <= 127.001; only
-// elements within 1e-4 of a tie take the division, in 64 bits, where the
+// A product with the correctly rounded reciprocal is within 2^-24 of the
+// quotient relative to it, below 8e-6 in absolute terms for |quotient| <= 127.01;
+// only elements within 1e-5 of a tie take the division, in 64 bits, where the
 // quotient of two 32-bit floats cannot round onto a tie that it is not on (it is
 // either on the tie or 2^-25 of it away).
 #pragma once
@@ -13,6 +13,7 @@
 
 #include "internal.cuh"
 #include "sm100.cuh"
+#include "softmax.cuh"
 
 namespace h3 {
 
@@ -37,26 +38,60 @@ __device__ __noinline__ inline int code_by_division(float x, float factor, float
   return (int)fmin(fmax(q, -127.0), 127.0);
 }
 
-// The low byte of the result is the code of x.
-__device__ __forceinline__ uint32_t code_of(float x, const RowScale& s) {
-  const float r = fmaf(x, s.inv, kCodeMagic);
-  const float d = fmaf(x, s.inv, kCodeMagic - r);  // quotient - rounded quotient
-  if (s.slow || fabsf(d) > 0.4999f) return (uint32_t)code_by_division(x, 1.f, s.scale);
-  return __float_as_uint(r);
-}
-
-// The code of code * from under another scale (ratio = from / to): the quotient
-// (code * from) / to has a 31-bit numerator, exact in 64 bits.
-__device__ __forceinline__ uint32_t code_again(int code, float from, float to, float ratio) {
-  const float r = fmaf((float)code, ratio, kCodeMagic);
-  const float d = fmaf((float)code, ratio, kCodeMagic - r);
-  if (to < 1e-30f || fabsf(d) > 0.4999f) return (uint32_t)code_by_division((float)code, from, to);
-  return __float_as_uint(r);
+// Eight codes by division, one call for all: the rare way.
+__device__ __noinline__ inline uint2 codes8_by_division(float a, float b, float c, float d, float e,
+                                                        float f, float g, float h, float scale) {
+  uint32_t w[2] = {0, 0};
+  const float x[8] = {a, b, c, d, e, f, g, h};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    w[i / 4] |= ((uint32_t)code_by_division(x[i], 1.f, scale) & 0xffu) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
 }
 
 // The low bytes of four words as one word.
 __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// The codes of x[0..7], or of x[0..3] (FOUR; .y is then void). Two elements per
+// instruction, and one branch for all.
+template <bool FOUR = false>
+__device__ __forceinline__ uint2 codes_of(const float* x, const RowScale& s) {
+  constexpr int N = FOUR ? 2 : 4;
+  const uint64_t inv = f2_pack(s.inv, s.inv), magic = f2_pack(kCodeMagic, kCodeMagic);
+  const uint64_t minus = f2_pack(-1.f, -1.f);
+  float r[2 * N], far = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint64_t v = f2_pack(x[2 * i], x[2 * i + 1]);
+    const uint64_t rr = f2_fma(v, inv, magic);
+    float d0, d1;  // quotient - rounded quotient
+    f2_unpack(f2_fma(v, inv, f2_fma(rr, minus, magic)), d0, d1);
+    f2_unpack(rr, r[2 * i], r[2 * i + 1]);
+    far = max3(far, fabsf(d0), fabsf(d1));
+  }
+  if (s.slow || far > 0.49999f) {
+    if constexpr (FOUR)
+      return codes8_by_division(x[0], x[1], x[2], x[3], 0.f, 0.f, 0.f, 0.f, s.scale);
+    else
+      return codes8_by_division(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], s.scale);
+  }
+  uint32_t u[2 * N];
+#pragma unroll
+  for (int i = 0; i < 2 * N; ++i) u[i] = __float_as_uint(r[i]);
+  uint2 c = make_uint2(pack4(u[0], u[1], u[2], u[3]), 0);
+  if constexpr (!FOUR) c.y = pack4(u[4], u[5], u[6], u[7]);
+  return c;
+}
+
+// The code of code * from under another scale (ratio = from / to, within 2^-22):
+// the quotient (code * from) / to has a 31-bit numerator, exact in 64 bits.
+__device__ __forceinline__ uint32_t code_again(int code, float from, float to, float ratio) {
+  const float r = fmaf((float)code, ratio, kCodeMagic);
+  const float d = fmaf((float)code, ratio, kCodeMagic - r);
+  if (to < 1e-30f || fabsf(d) > 0.4999f) return (uint32_t)code_by_division((float)code, from, to);
+  return __float_as_uint(r);
 }
 
 // 16 bytes of a row as floats: 8 elements of 2 bytes, or 4 of 4.
@@ -81,5 +116,44 @@ __device__ __forceinline__ void unpack(const uint4& u, float* v) {
     }
   }
 }
+
+// max(m, |elements|) of 16 bytes of a row, a NaN winning: 16-bit types by pairs in
+// their own type, where maxima are exact.
+template <h3_type T>
+struct AbsMax;
+template <>
+struct AbsMax<H3_F32> {
+  float m = 0.f;
+  __device__ __forceinline__ void add(const uint4& u) {
+    m = max_nan(m, fabsf(__uint_as_float(u.x)));
+    m = max_nan(m, fabsf(__uint_as_float(u.y)));
+    m = max_nan(m, fabsf(__uint_as_float(u.z)));
+    m = max_nan(m, fabsf(__uint_as_float(u.w)));
+  }
+  __device__ __forceinline__ float value() const { return m; }
+};
+template <>
+struct AbsMax<H3_BF16> {
+  uint32_t m = 0;
+  __device__ __forceinline__ void one(uint32_t w) {
+    w &= 0x7fff7fffu;
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+  }
+  __device__ __forceinline__ void add(const uint4& u) { one(u.x), one(u.y), one(u.z), one(u.w); }
+  __device__ __forceinline__ float value() const { return max_nan(bf16lo(m), bf16hi(m)); }
+};
+template <>
+struct AbsMax<H3_F16> {
+  uint32_t m = 0;
+  __device__ __forceinline__ void one(uint32_t w) {
+    w &= 0x7fff7fffu;
+    asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+  }
+  __device__ __forceinline__ void add(const uint4& u) { one(u.x), one(u.y), one(u.z), one(u.w); }
+  __device__ __forceinline__ float value() const {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return max_nan(f.x, f.y);
+  }
+};
 
 }  // namespace h3

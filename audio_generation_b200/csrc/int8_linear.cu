@@ -22,25 +22,14 @@ namespace {
 // The rounding is in int8_code.cuh.
 
 template <h3_type T>
-__device__ __forceinline__ float amax_of(const uint4& u, float m) {
-  float v[Vec<T>::N];
-  unpack<T>(u, v);
-#pragma unroll
-  for (int k = 0; k < Vec<T>::N; ++k) m = max_nan(m, fabsf(v[k]));
-  return m;
-}
-
-template <h3_type T>
 __device__ __forceinline__ void store_codes(const uint4& u, const RowScale& s, void* dst) {
   float v[Vec<T>::N];
   unpack<T>(u, v);
-  const uint32_t a = pack4(code_of(v[0], s), code_of(v[1], s), code_of(v[2], s), code_of(v[3], s));
-  if constexpr (T == H3_F32) {
-    *reinterpret_cast<uint32_t*>(dst) = a;
-  } else {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(
-        a, pack4(code_of(v[4], s), code_of(v[5], s), code_of(v[6], s), code_of(v[7], s)));
-  }
+  const uint2 c = codes_of<T == H3_F32>(v, s);
+  if constexpr (T == H3_F32)
+    *reinterpret_cast<uint32_t*>(dst) = c.x;
+  else
+    *reinterpret_cast<uint2*>(dst) = c;
 }
 
 template <int G>
@@ -72,18 +61,18 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G)
   const uint4* xr = x + row * stride_vec;
   uint8_t* cr = codes + (size_t)row * K;
   uint4 u[NV > 0 ? NV : 1];
-  float m = 0.f;
+  AbsMax<T> peak;
   if constexpr (NV > 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (t + i * G < nvec) u[i] = __ldcs(xr + t + i * G);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (t + i * G < nvec) m = amax_of<T>(u[i], m);
+      if (t + i * G < nvec) peak.add(u[i]);
   } else {
-    for (int i = t; i < nvec; i += G) m = amax_of<T>(xr[i], m);
+    for (int i = t; i < nvec; i += G) peak.add(xr[i]);
   }
-  m = group_max<G>(m);
+  const float m = group_max<G>(peak.value());
   if (!(m <= kMaxFinite)) {  // an infinity or a NaN in the row
     for (int i = t; i < K / 4; i += G) reinterpret_cast<uint32_t*>(cr)[i] = 0;
     if (t == 0) scales[row] = __int_as_float(0x7fc00000);
@@ -367,16 +356,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 }
 
 // Few rows (at most NT): bound by the bytes of the weights. The weights take
-// the MMA's 128-row side and the tokens its N side, so a CTA streams 128 weight
-// rows; the CTAs of a cluster share the K axis of one such tile and add their
-// integer sums through distributed shared memory, each finishing a share of the
-// tokens. Out is written with neighbouring lanes on neighbouring columns.
-template <int NT>
-constexpr int s_stages() { return NT <= 32 ? 5 : NT == 64 ? 4 : 3; }
+// the MMA's 128-row side and the tokens its N side, so a CTA streams tiles of 128
+// weight rows through a ring that fills most of its SM's shared memory (the
+// bytes in flight are what carries the bandwidth), one CTA per SM, the ring
+// running on from tile to tile. With few tiles the CTAs of a cluster share the K
+// axis of one and add their integer sums through distributed shared memory,
+// each finishing a share of the tokens. Neighbouring lanes store neighbouring
+// columns of out. Warps as above; the accumulator is double-buffered.
 template <int NT>
 constexpr int s_stage() { return A_STAGE + NT * BKB; }
 template <int NT>
-constexpr int s_smem() { return s_stages<NT>() * s_stage<NT>() + 1024 + 256; }
+constexpr int s_stages() { return 200 * 1024 / s_stage<NT>(); }
+template <int NT>
+constexpr int s_smem() { return s_stages<NT>() * s_stage<NT>() + 1024 + 512; }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   uint32_t v;
@@ -385,7 +377,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 }
 
 template <int NT>
-__global__ void __launch_bounds__(NUM_THREADS)
+__global__ void __launch_bounds__(NUM_THREADS, 1)
     k_int8_skinny(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                   int M, int N, int kb_n, int split, const Out out, int* err) {
   constexpr int NST = s_stages<NT>(), STAGE = s_stage<NT>();
@@ -396,14 +388,17 @@ __global__ void __launch_bounds__(NUM_THREADS)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + NST * STAGE);
   uint64_t* empty = full + NST;
-  uint64_t* done = empty + NST;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* tfull = empty + NST;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  constexpr uint32_t COLS = NT < 32 ? 32 : NT;
+  constexpr uint32_t ACC = NT < 32 ? 32 : NT;  // columns of one accumulator
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)cluster_ctarank() : 0;
-  const int n0 = (int)(blockIdx.x / split) * BM;
+  const int tiles = (N + BM - 1) / BM;
+  const int tile0 = (int)(blockIdx.x / split), step = (int)(gridDim.x / split);
   const int kb0 = (int)((long long)kb_n * rank / split);
   const int kb1 = (int)((long long)kb_n * (rank + 1) / split);
 
@@ -412,14 +407,18 @@ __global__ void __launch_bounds__(NUM_THREADS)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(done, 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 4);  // one arrival per epilogue warp
+    }
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmA);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, COLS);
+    tmem_alloc(tmem_slot, 2 * ACC);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -432,16 +431,18 @@ __global__ void __launch_bounds__(NUM_THREADS)
     if (lane == 0) {
       uint32_t n = 0;
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb, ++n) {
-        const uint32_t s = n % NST, ph = (n / NST) & 1;
-        if (!mbar_wait(&empty[s], ph ^ 1, wc)) {
-          ok = false;
-          break;
+      for (int t = tile0; t < tiles && ok; t += step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++n) {
+          const uint32_t s = n % NST, ph = (n / NST) & 1;
+          if (!mbar_wait(&empty[s], ph ^ 1, wc)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sw = smem + s * STAGE;
+          mbar_arrive_expect_tx(&full[s], STAGE);
+          tma_load_2d(sw, &tmW, &full[s], kb * BKB, t * BM);
+          tma_load_2d(sw + A_STAGE, &tmA, &full[s], kb * BKB, 0);
         }
-        uint8_t* sw = smem + s * STAGE;
-        mbar_arrive_expect_tx(&full[s], STAGE);
-        tma_load_2d(sw, &tmW, &full[s], kb * BKB, n0);
-        tma_load_2d(sw + A_STAGE, &tmA, &full[s], kb * BKB, 0);
       }
       if (!ok) {  // let issued copies land before the CTA retires
         const uint32_t first = n > NST ? n - NST : 0;
@@ -452,56 +453,78 @@ __global__ void __launch_bounds__(NUM_THREADS)
     constexpr uint32_t idesc = idesc_s8_s32(BM, NT);
     constexpr uint32_t hi = sdesc_hi_sw128(1024);
     const uint32_t base_lo = sdesc_lo(smem_u32(smem), 16);
-    uint32_t n = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++n) {
-      const uint32_t s = n % NST, ph = (n / NST) & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, wc))) break;
+    uint32_t n = 0, it = 0;
+    bool ok = true;
+    for (int t = tile0; t < tiles && ok; t += step, ++it) {
+      const uint32_t acc = it & 1, aph = (it >> 1) & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], aph ^ 1, wc))) break;
       tc_fence_after();
-      const uint32_t a_lo = base_lo + s * (STAGE >> 4);
-      const uint32_t b_lo = a_lo + (A_STAGE >> 4);
+      const uint32_t d = tmem + acc * ACC;
+      for (int kb = kb0; kb < kb1; ++kb, ++n) {
+        const uint32_t s = n % NST, ph = (n / NST) & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, wc))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a_lo = base_lo + s * (STAGE >> 4);
+        const uint32_t b_lo = a_lo + (A_STAGE >> 4);
 #pragma unroll
-      for (int k = 0; k < BKB / 32; ++k)
-        umma_ss_w_elect_i8(tmem, a_lo + 2 * k, hi, b_lo + 2 * k, hi, idesc,
-                           (n | k) != 0 ? 1u : 0u);
-      umma_commit_elect(&empty[s]);
+        for (int k = 0; k < BKB / 32; ++k)
+          umma_ss_w_elect_i8(d, a_lo + 2 * k, hi, b_lo + 2 * k, hi, idesc,
+                             (kb > kb0 || k > 0) ? 1u : 0u);
+        umma_commit_elect(&empty[s]);
+      }
+      if (!ok) break;
+      umma_commit_elect(&tfull[acc]);
     }
-    umma_commit_elect(done);  // also after a wait that ran out: the sums are then void
-    if (!__all_sync(0xffffffffu, mbar_wait(done, 0, wc))) mbar_drain(done, 0);
-  }
-  // Every sum of this CTA is in TMEM and its stages are no longer read.
-  __syncthreads();
-  tc_fence_after();
-  const int quarter = warp & 3;
-  const int r = quarter * 32 + lane;
-  const int n = n0 + r;
-  const float sw = warp >= 2 && n < N ? out.w_scale[n] : 0.f;
-  uint32_t* part = reinterpret_cast<uint32_t*>(smem);  // [NT][128] sums of this CTA
-  if (warp >= 2) {
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    umma_commit_elect(drain);  // every MMA issued is complete past this point
+    mbar_drain(drain, 0);
+  } else {
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // weight row of the tile
+    uint32_t it = 0;
+    for (int t = tile0; t < tiles; t += step, ++it) {
+      const uint32_t acc = it & 1, aph = (it >> 1) & 1;
+      const int n = t * BM + r;
+      const float sw = n < N ? out.w_scale[n] : 0.f;
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], aph, wc))) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * ACC;
+      // with a shared K axis: [NT][128] sums of this CTA, over its stages (the
+      // one tile's products are complete, so nothing reads them any more)
+      uint32_t* part = reinterpret_cast<uint32_t*>(smem);
 #pragma unroll 1
-    for (int c = 0; c < (NT + 31) / 32; ++c) {
-      uint32_t v[32];
-      tmem_ld32(taddr + 32 * c, v);
-      tmem_wait_ld();
-      if (split > 1) {
+      for (int c = 0; c < (NT + 31) / 32; ++c) {
+        uint32_t v[32];
+        tmem_ld32(taddr + 32 * c, v);
+        tmem_wait_ld();
+        if (split > 1) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (32 * c + i < M && 32 * c + i < NT) part[(32 * c + i) * BM + r] = v[i];
-      } else if (n < N) {
+          for (int i = 0; i < 32; ++i)
+            if (32 * c + i < M && 32 * c + i < NT) part[(32 * c + i) * BM + r] = v[i];
+        } else if (n < N) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const int m = 32 * c + i;
-          if (m < M) store_one(out, m * out.stride + n, (float)(int)v[i] * (out.a_scale[m] * sw));
+          for (int i = 0; i < 32; ++i) {
+            const int m = 32 * c + i;
+            if (m < M)
+              store_one(out, m * out.stride + n, (float)(int)v[i] * (out.a_scale[m] * sw));
+          }
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[acc]);
     }
-    tc_fence_before();
   }
   if (split > 1) {
+    __syncwarp();
     cluster_sync();
+    const int r = (warp & 3) * 32 + lane, n = tile0 * BM + r;
     if (warp >= 2 && n < N) {
+      const float sw = out.w_scale[n];
       const int m0 = M * rank / split, m1 = M * (rank + 1) / split;
-      const uint32_t mine = smem_u32(part) + r * 4;
+      const uint32_t mine = smem_u32(smem) + r * 4;
       for (int m = m0; m < m1; ++m) {
         int sum = 0;
         for (int q = 0; q < split; ++q)
@@ -516,7 +539,7 @@ __global__ void __launch_bounds__(NUM_THREADS)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, COLS);
+    tmem_dealloc(tmem, 2 * ACC);
   }
 }
 
@@ -549,6 +572,24 @@ cudaError_t run_pair(int M, int N, int K, const void* a, const void* w, const Ou
   return cudaGetLastError();
 }
 
+// Clusters of `split` CTAs that the current device runs at once (asked once).
+template <int NT>
+int clusters_at_once(cudaLaunchConfig_t cfg, int split) {
+  static int known[64][9] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (known[dev][split] == 0) {
+    int n = 0;
+    cfg.gridDim = dim3((unsigned)split);
+    if (cudaOccupancyMaxActiveClusters(&n, k_int8_skinny<NT>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    known[dev][split] = n > 0 ? n : -1;
+  }
+  return known[dev][split];
+}
+
 template <int NT>
 cudaError_t run_skinny(int M, int N, int K, const void* a, const void* w, const Out& out,
                        int* err, cudaStream_t st) {
@@ -558,22 +599,27 @@ cudaError_t run_skinny(int M, int N, int K, const void* a, const void* w, const 
   CUtensorMap ta, tw;
   if (!tmap_codes(&ta, a, M, K, NT) || !tmap_codes(&tw, w, N, K, BM)) return cudaErrorInvalidValue;
   const int tiles = (N + BM - 1) / BM, kb_n = (K + BKB - 1) / BKB;
-  // Two CTAs fit an SM: split K until they are about all there, each with two
-  // K steps at least.
-  int split = 1;
-  while (split < 8 && tiles * split < 2 * num_sms() && kb_n >= 4 * split) split *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * split));
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = s_smem<NT>();
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  // As many CTAs share a tile's K axis as leave every tile a cluster that runs at
+  // once, each with two K steps at least; with more tiles a CTA takes whole ones.
+  int split = num_sms() / tiles;
+  if (split > kb_n / 2) split = kb_n / 2;
+  if (split > 8) split = 8;
+  for (;; --split) {
+    if (split < 1) split = 1;
+    at[0].val.clusterDim.x = (unsigned)split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    if (split == 1 || clusters_at_once<NT>(cfg, split) >= tiles) break;
+  }
+  const int ctas = split > 1 ? tiles * split : (tiles < num_sms() ? tiles : num_sms());
+  cfg.gridDim = dim3((unsigned)ctas);
   return cudaLaunchKernelEx(&cfg, k_int8_skinny<NT>, tw, ta, M, N, kb_n, split, out, err);
 }
 

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
   const uint16_t* x = (is_v ? a.v : a.k) + (first + lo - before) * stride + head * D;
   uint4 u[NV];
-  float m = 0.f;
+  AbsMax<T> peak;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int idx = t + i * kStoreThreads;
@@ -85,12 +85,8 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (t + i * kStoreThreads < n * RV) {
-      float f[8];
-      unpack<T>(u[i], f);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) m = max_nan(m, fabsf(f[k]));
-    }
+    if (t + i * kStoreThreads < n * RV) peak.add(u[i]);
+  float m = peak.value();
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((t & 31) == 0) part[t >> 5] = m;
@@ -118,9 +114,7 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
     float f[8];
     unpack<T>(w, f);
     if (zero) return make_uint2(0, 0);
-    return make_uint2(
-        pack4(code_of(f[0], s), code_of(f[1], s), code_of(f[2], s), code_of(f[3], s)),
-        pack4(code_of(f[4], s), code_of(f[5], s), code_of(f[6], s), code_of(f[7], s)));
+    return codes_of(f, s);
   };
   auto word_again = [&](uint32_t w) {
     if (zero) return 0u;
@@ -291,6 +285,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) k_cache_attention(const AttnA
   constexpr int ND = D / 8;      // 8-channel column tiles of the output
   constexpr float kShift = 10.f;
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) __half qs[kRows * (D + 8)];
   __shared__ uint64_t full[R::STAGES], empty[R::STAGES];
   __shared__ Entry list[kMaxChunk];
   __shared__ float q_mul[kRows];
@@ -298,8 +293,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2) k_cache_attention(const AttnA
   __shared__ int s_n;
   __shared__ int s_abort;
   static_assert(kConsumers * kRows * D * 4 <= R::BYTES, "the sums reuse the stages");
-  static_assert(kRows * (D + 8) * 2 <= R::BYTES, "q passes through the stages");
 
+  asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may be set up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int id = blockIdx.x;
   const int heads = a.kv_heads * a.row_groups;
@@ -321,31 +316,37 @@ __global__ void __launch_bounds__(kAttnThreads, 2) k_cache_attention(const AttnA
     return;
   }
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < R::STAGES; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 2);  // the two warps of a pair
-    }
-    s_abort = 0;
-    fence_mbar_init();
-  }
+  auto load = [&](int i, int block) {  // entry i of the list into its stage
+    const int s = i % R::STAGES;
+    const size_t at = ((size_t)block * a.kv_heads + kvh) * R::BLOCK;
+    mbar_arrive_expect_tx(&full[s], 2 * R::BLOCK);
+    bulk_load(smem + s * 2 * R::BLOCK, a.k_codes + at, R::BLOCK, &full[s]);
+    bulk_load(smem + s * 2 * R::BLOCK + R::BLOCK, a.v_codes + at, R::BLOCK, &full[s]);
+  };
   if (warp == kConsumers) {  // the cache blocks of this range, those that exist
+    if (lane < R::STAGES) {
+      mbar_init(&full[lane], 1);
+      mbar_init(&empty[lane], 2);  // the two warps of a pair
+    }
+    if (lane == 0) s_abort = 0;
+    fence_mbar_init();
+    __syncwarp();
     int n = 0;
     for (int p = p0; p < p1; p += 32) {
       const int b = p + lane < p1
                         ? block_of(a.table, a.width, seq, p + lane, a.n_blocks, a.err) : -1;
       const uint32_t mask = __ballot_sync(0xffffffffu, b >= 0);
       if (b >= 0) {
+        const int i = n + __popc(mask & ((1u << lane) - 1u));
+        if (i < R::STAGES) load(i, b);  // the first ones go out at once
         const size_t at = (size_t)b * a.kv_heads + kvh;
-        list[n + __popc(mask & ((1u << lane) - 1u))] =
-            Entry{b, p + lane, a.k_scales[at], a.v_scales[at]};
+        list[i] = Entry{b, p + lane, a.k_scales[at], a.v_scales[at]};
       }
       n += __popc(mask);
     }
     if (lane == 0) s_n = n;
   } else {
     // q rows -> fp16 times a power of two, through shared memory
-    __half* qs = reinterpret_cast<__half*>(smem);
     for (int r = warp; r < kRows; r += kConsumers) {
       float x[D / 32], m = 0.f;
 #pragma unroll
@@ -372,38 +373,30 @@ __global__ void __launch_bounds__(kAttnThreads, 2) k_cache_attention(const AttnA
   const int g = lane >> 2, t = lane & 3;
   uint32_t qa[KM][4];
   if (warp < kConsumers) {
-    const uint8_t* qs = smem;
 #pragma unroll
     for (int m = 0; m < KM; ++m) {
       const int d = 64 * (m >> 2) + 16 * t + 4 * (m & 3);  // the thread's four channels
-      const uint2 lo = *reinterpret_cast<const uint2*>(qs + (g * (D + 8) + d) * 2);
-      const uint2 hi = *reinterpret_cast<const uint2*>(qs + ((g + 8) * (D + 8) + d) * 2);
+      const uint2 lo = *reinterpret_cast<const uint2*>(qs + g * (D + 8) + d);
+      const uint2 hi = *reinterpret_cast<const uint2*>(qs + (g + 8) * (D + 8) + d);
       qa[m][0] = lo.x;
       qa[m][1] = hi.x;
       qa[m][2] = lo.y;
       qa[m][3] = hi.y;
     }
-    // the bulk copies that follow overwrite what these threads have just read
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  __syncthreads();  // q is in registers: the stages are free
 
   float acc[ND][4];
   float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
   if (warp == kConsumers) {
     if (lane == 0) {
-      int i = 0;
+      int i = min(n, R::STAGES);
       bool ok = true;
       for (; i < n; ++i) {
-        const int s = i % R::STAGES;
-        if (!mbar_wait(&empty[s], ((i / R::STAGES) & 1) ^ 1, wc)) {
+        if (!mbar_wait(&empty[i % R::STAGES], ((i / R::STAGES) & 1) ^ 1, wc)) {
           ok = false;
           break;
         }
-        const size_t at = ((size_t)list[i].block * a.kv_heads + kvh) * R::BLOCK;
-        mbar_arrive_expect_tx(&full[s], 2 * R::BLOCK);
-        bulk_load(smem + s * 2 * R::BLOCK, a.k_codes + at, R::BLOCK, &full[s]);
-        bulk_load(smem + s * 2 * R::BLOCK + R::BLOCK, a.v_codes + at, R::BLOCK, &full[s]);
+        load(i, list[i].block);
       }
       if (!ok)  // let issued copies land before the block retires
         for (int j = i > R::STAGES ? i - R::STAGES : 0; j < i; ++j)
@@ -426,19 +419,28 @@ __global__ void __launch_bounds__(kAttnThreads, 2) k_cache_attention(const AttnA
       float sc[NJ][4];
       const uint8_t* krow = kb + (half * HT + (HT / 4) * (g >> 1) + (g & 1)) * D + 16 * t;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          const uint4 w = *reinterpret_cast<const uint4*>(krow + 2 * j * D + 64 * h);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      for (int h = 0; h < D / 64; ++h) {
+        constexpr int JB = NJ < 4 ? NJ : 4;  // independent products in flight
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            uint32_t b0, b1;
-            codes_to_f16(ww[m], b0, b1);
-            mma_f16(sc[j], qa[4 * h + m], b0, b1);
+        for (int j0 = 0; j0 < NJ; j0 += JB) {
+          uint32_t w[JB][4];
+#pragma unroll
+          for (int j = 0; j < JB; ++j) {
+            const uint4 x = *reinterpret_cast<const uint4*>(krow + 2 * (j0 + j) * D + 64 * h);
+            w[j][0] = x.x, w[j][1] = x.y, w[j][2] = x.z, w[j][3] = x.w;
           }
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int j = 0; j < JB; ++j) {
+              uint32_t b0, b1;
+              codes_to_f16(w[j][m], b0, b1);
+              mma_f16(sc[j0 + j], qa[4 * h + m], b0, b1);
+            }
         }
       }
       const float f0 = mul0 * en.ks, f1 = mul1 * en.ks;
@@ -568,26 +570,57 @@ __global__ void __launch_bounds__(kAttnThreads, 2) k_cache_attention(const AttnA
   }
 }
 
-// Joins the ranges of the sequences that had more than one: a thread per channel.
+// Joins the ranges of the sequences that had more than one: a block per
+// (sequence, head), kJoinParts threads per channel, each taking every
+// kJoinParts-th range, so that the partial sums are fetched side by side.
+constexpr int kJoinParts = 4, kJoinTile = 128;
+
 template <int D, int BT>
-__global__ void __launch_bounds__(D) k_cache_join(const AttnArgs a) {
+__global__ void __launch_bounds__(D * kJoinParts) k_cache_join(const AttnArgs a) {
+  __shared__ float factor[kJoinTile];
+  __shared__ float sums[kJoinParts][D], weights[kJoinParts];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the ranges' kernel is complete
   const int q_heads = a.kv_heads * a.group;
-  const int seq = blockIdx.x / q_heads, head = blockIdx.x - seq * q_heads, d = threadIdx.x;
+  const int seq = blockIdx.x / q_heads, head = blockIdx.x - seq * q_heads;
+  const int d = threadIdx.x % D, p = threadIdx.x / D, lane = threadIdx.x & 31;
   const long long most = (long long)a.width * BT;
   const int len = (int)min((long long)max(a.lengths[seq], 0), most);
   const int n = ((len + BT - 1) / BT + a.chunk - 1) / a.chunk;
   if (n <= 1) return;
   const size_t at = (size_t)blockIdx.x * a.splits;
-  float m = -INFINITY;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, a.stat[at + i].x);
+  float m = -INFINITY;  // every warp for itself
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.stat[at + i].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float sum = 0.f, l = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const float2 ml = a.stat[at + i];
-    const float f = ml.x == m ? 1.f : exp2_mufu(ml.x - m);
-    sum = fmaf(a.part[(at + i) * D + d], f, sum);
-    l = fmaf(ml.y, f, l);
+  for (int i0 = 0; i0 < n; i0 += kJoinTile) {
+    const int k = min(kJoinTile, n - i0);
+    __syncthreads();
+    if (threadIdx.x < k) {
+      const float2 ml = a.stat[at + i0 + threadIdx.x];
+      const float f = ml.x == m ? 1.f : exp2_mufu(ml.x - m);
+      factor[threadIdx.x] = f;
+      l = fmaf(ml.y, f, l);
+    }
+    __syncthreads();
+    const float* part = a.part + (at + i0) * D + d;
+#pragma unroll 8
+    for (int i = p; i < k; i += kJoinParts) sum = fmaf(part[(size_t)i * D], factor[i], sum);
   }
-  a.o[seq * a.o_stride + head * D + d] = float_to_act(l == 0.f ? 0.f : sum / l, a.f16);
+  sums[p][d] = sum;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  // the threads that held a weight are the first kJoinTile = 4 warps
+  if (lane == 0 && threadIdx.x < kJoinTile) weights[threadIdx.x / 32] = l;
+  __syncthreads();
+  if (p == 0) {
+    float total = 0.f, w = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinParts; ++i) total += sums[i][d];
+#pragma unroll
+    for (int i = 0; i < kJoinTile / 32; ++i) w += weights[i];
+    a.o[seq * a.o_stride + head * D + d] = float_to_act(w == 0.f ? 0.f : total / w, a.f16);
+  }
 }
 
 // How the tokens are split: cache blocks per thread block, such that two thread
@@ -595,8 +628,8 @@ __global__ void __launch_bounds__(D) k_cache_join(const AttnArgs a) {
 // kMaxChunk; and the number of ranges that gives.
 void split_of(int n_seq, int heads, int width, int& chunk, int& splits) {
   const long long units = (long long)n_seq * heads * width;
-  long long c = units / (2 * num_sms());
-  if (c < 1) c = 1;
+  const long long at_once = 2 * num_sms();
+  long long c = (units + at_once - 1) / at_once;
   if (c > kMaxChunk) c = kMaxChunk;
   if (c > width) c = width;
   chunk = (int)c;
@@ -613,8 +646,19 @@ cudaError_t run_attention(AttnArgs& a, int n_seq, cudaStream_t st) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   k_cache_attention<D, BT><<<(unsigned)blocks, kAttnThreads, BYTES, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
-  k_cache_join<D, BT><<<(unsigned)((long long)n_seq * a.kv_heads * a.group), D, 0, st>>>(a);
-  return cudaGetLastError();
+  const long long heads = (long long)n_seq * a.kv_heads * a.group;
+  if (heads > 0x7fffffffLL) return cudaErrorInvalidValue;
+  // launched while the ranges run, to wait for them on the GPU
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)heads);
+  cfg.blockDim = dim3(D * kJoinParts);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_cache_join<D, BT>, a);
 }
 
 template <h3_type T, int D>

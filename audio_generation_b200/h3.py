@@ -192,13 +192,15 @@ def _ptr(t) -> Optional[int]:
         return None
     if isinstance(t, int):
         return t
-    return int(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        if torch.cuda.is_initialized():  # the current stream without an object made for it
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -542,13 +544,18 @@ def h3_block_forward_e4m3(dims: h3_dims, weights: h3_block_weights, w8: h3_block
 
 # ---------------------------------------------------------------- text model
 
-_TYPES = {"torch.bfloat16": H3_BF16, "torch.float16": H3_F16, "torch.float32": H3_F32}
+_TYPES = {H3_BF16: H3_BF16, H3_F16: H3_F16, H3_F32: H3_F32}
 
 
 def _type(t) -> int:
     """h3_type of a torch dtype (or an h3_type itself); -1, which the library
     refuses, for any other."""
-    return t if isinstance(t, int) else _TYPES.get(str(t), -1)
+    code = _TYPES.get(t)
+    if code is None:  # a dtype not seen before
+        code = {"torch.bfloat16": H3_BF16, "torch.float16": H3_F16,
+                "torch.float32": H3_F32}.get(str(t), -1)
+        _TYPES[t] = code
+    return code
 
 
 def h3_quantize_int8_rows(dtype, rows: int, K: int, x, x_stride: int, codes, scales,
