@@ -1,11 +1,13 @@
 // Rounding to int8 codes, shared by the kernels that quantize.
 //
 // The code is the nearest integer to the exact quotient x / scale, ties to even.
-// A product with the correctly rounded reciprocal is within 2^-24 of the
-// quotient relative to it, below 8e-6 in absolute terms for |quotient| <= 127.01;
-// only elements within 1e-5 of a tie take the division, in 64 bits, where the
-// quotient of two 32-bit floats cannot round onto a tie that it is not on (it is
-// either on the tie or 2^-25 of it away).
+// x times the correctly rounded reciprocal is within 2^-24 of the quotient
+// relative to it, so its rounding r is the code or, next to a tie, its neighbour.
+// The rest x - r scale decides: it is a multiple of half a unit of the scale's
+// last place and at most about half the scale, so one fused multiply-add gives it
+// exactly, and r moves by one if the rest is more than half the scale, or equal
+// to it and r odd. (Near-ties are not rare: with x and the maximum in bfloat16
+// the quotient is 127 times a ratio of two 8-bit numbers.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -22,7 +24,7 @@ constexpr float kMaxFinite = 3.4028235e38f;
 
 struct RowScale {
   float scale, inv;
-  bool slow;  // the reciprocal is not a normal float: divide everywhere
+  bool slow;  // too small for exact rests: divide everywhere, in 64 bits
 };
 
 __device__ __forceinline__ RowScale row_scale(float scale) {
@@ -54,28 +56,34 @@ __device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, ui
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// The codes of x[0..7], or of x[0..3] (FOUR; .y is then void). Two elements per
-// instruction, and one branch for all.
+// The codes of x[0..7], or of x[0..3] (FOUR; .y is then void).
 template <bool FOUR = false>
 __device__ __forceinline__ uint2 codes_of(const float* x, const RowScale& s) {
   constexpr int N = FOUR ? 2 : 4;
-  const uint64_t inv = f2_pack(s.inv, s.inv), magic = f2_pack(kCodeMagic, kCodeMagic);
-  const uint64_t minus = f2_pack(-1.f, -1.f);
-  float r[2 * N], far = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint64_t v = f2_pack(x[2 * i], x[2 * i + 1]);
-    const uint64_t rr = f2_fma(v, inv, magic);
-    float d0, d1;  // quotient - rounded quotient
-    f2_unpack(f2_fma(v, inv, f2_fma(rr, minus, magic)), d0, d1);
-    f2_unpack(rr, r[2 * i], r[2 * i + 1]);
-    far = max3(far, fabsf(d0), fabsf(d1));
-  }
-  if (s.slow || far > 0.49999f) {
+  if (s.slow) {
     if constexpr (FOUR)
       return codes8_by_division(x[0], x[1], x[2], x[3], 0.f, 0.f, 0.f, 0.f, s.scale);
     else
       return codes8_by_division(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], s.scale);
+  }
+  const uint64_t inv = f2_pack(s.inv, s.inv), magic = f2_pack(kCodeMagic, kCodeMagic);
+  const uint64_t unmagic = f2_pack(-kCodeMagic, -kCodeMagic);
+  const uint64_t minus_scale = f2_pack(-s.scale, -s.scale);
+  const uint32_t half = __float_as_uint(0.5f * s.scale);
+  float r[2 * N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint64_t v = f2_pack(x[2 * i], x[2 * i + 1]);
+    const uint64_t rr = f2_fma(v, inv, magic);
+    float rest[2];
+    f2_unpack(f2_fma(f2_add(rr, unmagic), minus_scale, v), rest[0], rest[1]);
+    f2_unpack(rr, r[2 * i], r[2 * i + 1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      // above half the scale, or from half the scale on where r is odd
+      const float limit = __uint_as_float(half - (__float_as_uint(r[2 * i + k]) & 1u));
+      if (fabsf(rest[k]) > limit) r[2 * i + k] += copysignf(1.f, rest[k]);
+    }
   }
   uint32_t u[2 * N];
 #pragma unroll

@@ -22,35 +22,36 @@ __device__ __forceinline__ int block_of(const int32_t* table, int width, int seq
 }
 
 // ------------------------------------------------------------- store
-// A thread block per (sequence, cache block touched, kv head, K or V): the
-// block's new values are read once into registers, their maximum sets the
-// scale, and the codes are written. Where the block holds earlier tokens and
-// the scale grows, their codes are rounded again under the new scale. HBM-bound
-// for prompts (2 bytes in, 1 out per value), launch-bound for single tokens.
-// V's codes are turned through shared memory, so that global stores run along
-// the tokens.
+// A thread block per (sequence, cache block touched, kv head): the block's new
+// values of K and V are read once into registers, their maxima set the scales,
+// and the codes are written. Where the block holds earlier tokens and a scale
+// grows, their codes are rounded again under the new one. HBM-bound for prompts
+// (2 bytes in, 1 out per value), launch-bound for single tokens. A thread holds
+// eight channels of four neighbouring slots, so that V's codes turn in
+// registers to words of four tokens; these pass through shared memory (with the
+// word's place XORed by the channel, against bank conflicts), so that global
+// stores run along the tokens.
 constexpr int kStoreThreads = 256;
 
 struct StoreArgs {
   const int32_t *table, *lengths, *offsets;
-  const uint16_t *k, *v;
-  int64_t k_stride, v_stride;
-  uint8_t *k_codes, *v_codes;
-  float *k_scales, *v_scales;
+  const uint16_t* x[2];  // k, v
+  int64_t stride[2];
+  uint8_t* codes[2];
+  float* scales[2];
   int n_blocks, kv_heads, width, max_new, rows, pages;
   int* err;
 };
 
 template <h3_type T, int D, int BT>
 __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
-  constexpr int RV = D / 8;                                // 16-byte vectors per token
-  constexpr int NV = (BT * RV + kStoreThreads - 1) / kStoreThreads;
-  constexpr int PITCH = BT + 4;
-  __shared__ __align__(16) uint8_t turned[D * PITCH];
-  __shared__ float part[kStoreThreads / 32];
+  constexpr int RV = D / 8;                 // 16-byte vectors per token
+  constexpr int WR = BT / 4;                // words of four slots per channel
+  constexpr int GROUPS = WR * RV;           // (word, vector) pairs
+  constexpr int NG = (GROUPS + kStoreThreads - 1) / kStoreThreads;
+  __shared__ uint32_t turned[D * WR];
+  __shared__ float part[2][kStoreThreads / 32];
   int id = blockIdx.x;
-  const bool is_v = id & 1;
-  id >>= 1;
   const int head = id % a.kv_heads;
   id /= a.kv_heads;
   const int nth = id % a.pages, seq = id / a.pages;
@@ -68,121 +69,152 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
   const int page = before / BT + nth;
   const int lo = max(before, page * BT), hi = min(before + count, (page + 1) * BT);
   if (lo >= hi) return;
+  const int held = nth == 0 ? before % BT : 0;  // earlier tokens of the block
+  const int slot0 = lo - page * BT, to = hi - page * BT;
+
+  uint4 u[2][NG][4];
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const int idx = t + i * kStoreThreads;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int slot = 4 * (idx / RV) + j;
+        u[w][i][j] = make_uint4(0, 0, 0, 0);
+        if (idx < GROUPS && slot >= slot0 && slot < to)
+          u[w][i][j] = __ldcs(reinterpret_cast<const uint4*>(
+              a.x[w] + (first + (page * BT + slot - before)) * a.stride[w] + head * D +
+              (idx % RV) * 8));
+      }
+    }
   const int block = block_of(a.table, a.width, seq, page, a.n_blocks, a.err);
   if (block < 0) return;
-  const int held = nth == 0 ? before % BT : 0;             // earlier tokens of the block
-  const int slot0 = lo - page * BT, n = hi - lo;
-
-  const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  const uint16_t* x = (is_v ? a.v : a.k) + (first + lo - before) * stride + head * D;
-  uint4 u[NV];
-  AbsMax<T> peak;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int idx = t + i * kStoreThreads;
-    if (idx < n * RV)
-      u[i] = __ldcs(reinterpret_cast<const uint4*>(x + (idx / RV) * stride) + idx % RV);
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (t + i * kStoreThreads < n * RV) peak.add(u[i]);
-  float m = peak.value();
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((t & 31) == 0) part[t >> 5] = m;
-  __syncthreads();
-  m = 0.f;
-#pragma unroll
-  for (int w = 0; w < kStoreThreads / 32; ++w) m = max_nan(m, part[w]);
-
   const size_t at = (size_t)block * a.kv_heads + head;
-  float* scales = is_v ? a.v_scales : a.k_scales;
-  uint8_t* codes = (is_v ? a.v_codes : a.k_codes) + at * (BT * D);
-  const float old = held > 0 ? scales[at] : 0.f;
-  float scale = max_nan(m / 127.f, old);
-  // an infinity or a NaN marks the whole block: scale NaN, codes 0
-  const bool bad = !(m <= kMaxFinite) || !(old <= kMaxFinite);
-  if (bad) scale = __int_as_float(0x7fc00000);
-  const bool zero = bad || scale == 0.f;
-  const RowScale s = row_scale(zero ? 1.f : scale);
-  const bool again = held > 0 && (bad || scale > old);      // earlier codes change
-  const float ratio = old * s.inv;
-  __syncthreads();  // every thread has read the old scale
-  if (t == 0) scales[at] = scale;
-
-  auto vec_codes = [&](const uint4& w) {
-    float f[8];
-    unpack<T>(w, f);
-    if (zero) return make_uint2(0, 0);
-    return codes_of(f, s);
-  };
-  auto word_again = [&](uint32_t w) {
-    if (zero) return 0u;
-    uint32_t c[4];
+  float old[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      c[k] = code_again((int)(int8_t)(w >> (8 * k)), old, scale, ratio);
-    return pack4(c[0], c[1], c[2], c[3]);
-  };
-
-  if (!is_v) {
+  for (int w = 0; w < 2; ++w) old[w] = held > 0 ? a.scales[w][at] : 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int idx = t + i * kStoreThreads;
-      if (idx < n * RV) reinterpret_cast<uint2*>(codes)[slot0 * RV + idx] = vec_codes(u[i]);
-    }
-    if (again)
-      for (int w = t; w < held * D / 4; w += kStoreThreads) {
-        uint32_t* p = reinterpret_cast<uint32_t*>(codes) + w;
-        *p = word_again(*p);
-      }
-    return;
+  for (int w = 0; w < 2; ++w) {
+    AbsMax<T> peak;
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) peak.add(u[w][i][j]);
+    float m = peak.value();
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((t & 31) == 0) part[w][t >> 5] = m;
   }
+  __syncthreads();  // also: every thread has read the old scales
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int idx = t + i * kStoreThreads;
-    if (idx < n * RV) {
-      const uint2 c = vec_codes(u[i]);
-      uint8_t* dst = turned + (idx % RV) * 8 * PITCH + slot0 + idx / RV;
+  for (int w = 0; w < 2; ++w) {
+    float m = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        dst[k * PITCH] = (uint8_t)((k < 4 ? c.x : c.y) >> (8 * (k & 3)));
-    }
-  }
-  __syncthreads();
-  const int from = again ? 0 : slot0, to = slot0 + n;
-  const int w0 = from / 4, words = (to + 3) / 4 - w0;
-  for (int i = t; i < D * words; i += kStoreThreads) {
-    const int d = i / words, w = w0 + i % words;
-    uint32_t* p = reinterpret_cast<uint32_t*>(codes + d * BT) + w;
-    uint32_t c = *reinterpret_cast<const uint32_t*>(turned + d * PITCH + 4 * w);
-    if (4 * w < slot0 || 4 * w + 4 > to) {  // the word also holds earlier or later tokens
-      const uint32_t was = *p;
-      const uint32_t early = again ? word_again(was) : was;
+    for (int k = 0; k < kStoreThreads / 32; ++k) m = max_nan(m, part[w][k]);
+    float scale = max_nan(m / 127.f, old[w]);
+    // an infinity or a NaN marks the whole block: scale NaN, codes 0
+    const bool bad = !(m <= kMaxFinite) || !(old[w] <= kMaxFinite);
+    if (bad) scale = __int_as_float(0x7fc00000);
+    if (t == 0) a.scales[w][at] = scale;
+    const bool zero = bad || scale == 0.f;
+    const RowScale s = row_scale(zero ? 1.f : scale);
+    const bool again = held > 0 && (bad || scale > old[w]);  // earlier codes change
+    const float ratio = old[w] * s.inv;
+    uint8_t* codes = a.codes[w] + at * (BT * D);
+    auto word_again = [&](uint32_t x) {
+      if (zero) return 0u;
+      uint32_t c[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int slot = 4 * w + k;
-        const uint32_t mask = 0xffu << (8 * k);
-        if (slot < slot0) c = (c & ~mask) | (early & mask);
-        if (slot >= to) c = (c & ~mask) | (was & mask);
+      for (int k = 0; k < 4; ++k)
+        c[k] = code_again((int)(int8_t)(x >> (8 * k)), old[w], scale, ratio);
+      return pack4(c[0], c[1], c[2], c[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      const int idx = t + i * kStoreThreads, word = idx / RV, vec = idx % RV;
+      if (idx >= GROUPS || 4 * word + 4 <= slot0 || 4 * word >= to) continue;
+      uint2 c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float f[8];
+        unpack<T>(u[w][i][j], f);
+        c[j] = zero ? make_uint2(0, 0) : codes_of(f, s);
+      }
+      if (w == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int slot = 4 * word + j;
+          if (slot >= slot0 && slot < to)
+            *reinterpret_cast<uint2*>(codes + slot * D + vec * 8) = c[j];
+        }
+      } else {
+        uint32_t* dst = turned + vec * 8 * WR + (word ^ (vec & (WR - 1)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t c0 = h ? c[0].y : c[0].x, c1 = h ? c[1].y : c[1].x;
+          const uint32_t c2 = h ? c[2].y : c[2].x, c3 = h ? c[3].y : c[3].x;
+          const uint32_t p = __byte_perm(c0, c1, 0x5140), q = __byte_perm(c2, c3, 0x5140);
+          const uint32_t r = __byte_perm(c0, c1, 0x7362), x = __byte_perm(c2, c3, 0x7362);
+          dst[(4 * h) * WR] = __byte_perm(p, q, 0x5410);
+          dst[(4 * h + 1) * WR] = __byte_perm(p, q, 0x7632);
+          dst[(4 * h + 2) * WR] = __byte_perm(r, x, 0x5410);
+          dst[(4 * h + 3) * WR] = __byte_perm(r, x, 0x7632);
+        }
       }
     }
-    *p = c;
+    if (w == 0) {
+      if (again)
+        for (int i = t; i < held * D / 4; i += kStoreThreads) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
+          *p = word_again(*p);
+        }
+      continue;
+    }
+    __syncthreads();
+    const int from = again ? 0 : slot0;
+#pragma unroll
+    for (int i = t; i < D * WR; i += kStoreThreads) {
+      const int d = i / WR, word = i % WR;
+      if (4 * word + 4 <= from || 4 * word >= to) continue;
+      uint32_t* p = reinterpret_cast<uint32_t*>(codes + d * BT) + word;
+      uint32_t c = turned[d * WR + (word ^ ((d / 8) & (WR - 1)))];
+      if (4 * word < slot0 || 4 * word + 4 > to) {  // also earlier or later tokens' codes
+        const uint32_t was = *p;
+        const uint32_t early = again ? word_again(was) : was;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int slot = 4 * word + k;
+          const uint32_t mask = 0xffu << (8 * k);
+          if (slot < slot0) c = (c & ~mask) | (early & mask);
+          if (slot >= to) c = (c & ~mask) | (was & mask);
+        }
+      }
+      *p = c;
+    }
   }
 }
 
 // ------------------------------------------------------------- attention
 // o[s, h] = softmax_j(scale q[s, h] . k[j]) v[j] over the sequence's cached
 // tokens. Bound by the bytes of the cache (2 D per token and kv head), so the
-// query heads of a group (16 at a time) share one pass over it, and the tokens
-// are split over thread blocks, whose partial results a second kernel joins.
+// query heads of a group (16 at a time) share one pass over it.
 //
-// A block has one producer warp, which streams cache blocks into a ring of
-// shared-memory stages with bulk copies, and four consumer warps: two pairs take
-// the ring's entries in turn, the warps of a pair half the tokens each, every
-// warp with its own running maximum, sum and accumulator (joined at the end), so
-// nothing waits but on its data. The products run on m16n8k16 fp16 MMAs (the
-// query heads fill the 16 rows; the kernel is bound by bytes, and this form
+// The work is the list of all (sequence, head group, cache block) units in that
+// order, cut into equal ranges, one per thread block, as many as run at once:
+// lengths may differ as they like, every thread block streams the same number
+// of bytes, and its ring of stages runs on from one sequence to the next. A pair
+// (sequence, head group) that lies in one range is finished there; the parts of
+// one that is cut go to the workspace and a second kernel joins them. At most
+// the first and the last pair of a range are cut, so the workspace does not grow
+// with the sequences.
+//
+// A thread block has one producer warp, which streams cache blocks into shared-
+// memory stages with bulk copies, and four consumer warps: two pairs take the
+// stages in turn, the warps of a pair half the tokens each, every warp with its
+// own running maximum, sum and accumulator (joined at the end of a segment), so
+// that nothing waits but on its data. The products run on m16n8k16 fp16 MMAs
+// (the query heads fill the 16 rows; the kernel is bound by bytes, and this form
 // takes its operands from registers, where the codes become fp16 exactly): the
 // 16-byte pieces a thread reads of a K row serve as four k-steps, since the order
 // of the channels inside a product is free, and the tokens are assigned to
@@ -195,14 +227,19 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
 // that they stay normal numbers down to 2^-24 of the largest.
 constexpr int kAttnThreads = 160, kConsumers = 4;
 constexpr int kRows = 16;
-constexpr int kMaxChunk = 64;  // cache blocks per thread block
-constexpr int kRingBytes = 96 * 1024;
+constexpr int kListSize = 64;   // entries of the producer's list, two batches of 32
+constexpr int kMinUnits = 2;    // cache blocks a thread block takes at least
 
 template <int D, int BT>
 struct Ring {
-  static constexpr int BLOCK = BT * D;                   // bytes of K (or V) codes
-  static constexpr int STAGES = kRingBytes / (2 * BLOCK) < 16 ? kRingBytes / (2 * BLOCK) : 16;
-  static constexpr int BYTES = STAGES * 2 * BLOCK;
+  static constexpr int BLOCK = BT * D;  // bytes of K (or V) codes
+  // Thread blocks per SM, and the stages that fit beside the sums.
+  static constexpr int PER_SM = BLOCK >= 16384 ? 2 : 3;
+  static constexpr int STAGES = BLOCK >= 16384 ? 2 : 49152 / (2 * BLOCK) < 16 ? 49152 / (2 * BLOCK)
+                                                                              : 16;
+  static constexpr int SUMS = 2 * kRows * D * 4;  // two warps' accumulators
+  static constexpr int BYTES = STAGES * 2 * BLOCK + SUMS;
+  static_assert(STAGES <= kListSize - 32, "a list entry outlives its stage");
 };
 
 struct Entry {
@@ -217,9 +254,13 @@ struct AttnArgs {
   const uint16_t* q;
   uint16_t* o;
   int64_t q_stride, o_stride;
-  float* part;     // [n_seq * q_heads * splits][D] sums
-  float2* stat;    // [n_seq * q_heads * splits] maximum (log2 units), sum of weights
-  int n_blocks, kv_heads, group, row_groups, width, splits, chunk;
+  // workspace, per thread block: two parts (0: a pair begun earlier, 1: a pair
+  // that goes on) of 16 rows of sums and of (maximum, sum of weights), and which
+  // pair part 1 belongs to, with the number of its parts
+  float* part;    // [blocks][2][16][D]
+  float2* stat;   // [blocks][2][16]
+  int4* cut;      // [blocks] {sequence, head group, parts, 0}
+  int n_seq, n_blocks, kv_heads, group, row_groups, width;
   float scale_log2;
   bool f16;
   int* err;
@@ -276,77 +317,162 @@ __device__ __forceinline__ int length_of(const AttnArgs& a, int seq, int block_t
   return len < 0 ? 0 : (int)most;
 }
 
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
 template <int D, int BT>
-__global__ void __launch_bounds__(kAttnThreads, 2) k_cache_attention(const AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
+    k_cache_attention(const AttnArgs a) {
   using R = Ring<D, BT>;
   constexpr int HT = BT / 2;     // tokens of a warp per cache block
   constexpr int NJ = HT / 8;     // its 8-token column tiles
-  constexpr int KM = D / 16;     // k-steps of the score product
   constexpr int ND = D / 8;      // 8-channel column tiles of the output
+  constexpr int QP = D + 4;      // row pitch of q: its 8-byte pieces meet no bank twice
   constexpr float kShift = 10.f;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) __half qs[kRows * (D + 8)];
+  __shared__ __align__(16) __half qs[kRows * QP];
   __shared__ uint64_t full[R::STAGES], empty[R::STAGES];
-  __shared__ Entry list[kMaxChunk];
+  __shared__ Entry list[kListSize];
   __shared__ float q_mul[kRows];
   __shared__ float2 stat[kConsumers][kRows];
-  __shared__ int s_n;
-  __shared__ int s_abort;
-  static_assert(kConsumers * kRows * D * 4 <= R::BYTES, "the sums reuse the stages");
+  __shared__ long long warp_sum[kAttnThreads / 32];
+  __shared__ long long s_before;  // cache blocks before the range's first sequence
+  __shared__ int s_seq, s_abort;
 
   asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may be set up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int id = blockIdx.x;
-  const int heads = a.kv_heads * a.row_groups;
-  const int hg = id % heads;
-  id /= heads;
-  const int split = id % a.splits, seq = id / a.splits;
-  const int kvh = hg / a.row_groups, h0 = (hg % a.row_groups) * kRows;
-  const int rows = min(kRows, a.group - h0), q_heads = a.kv_heads * a.group;
-  const int head0 = kvh * a.group + h0;
+  const int heads = a.kv_heads * a.row_groups, q_heads = a.kv_heads * a.group;
 
-  const int len = length_of(a, seq, BT);
-  const int pages = (len + BT - 1) / BT;
-  const int p0 = split * a.chunk, p1 = min(pages, p0 + a.chunk);
-  const bool alone = pages <= a.chunk;  // this block's result is the result
-  if (p0 >= p1) {
-    if (split == 0)  // nothing cached: zeros
-      for (int i = threadIdx.x; i < rows * D; i += kAttnThreads)
-        a.o[seq * a.o_stride + (head0 + i / D) * D + i % D] = 0;
-    return;
+  // ---- this thread block's range of units: a scan over the sequences' lengths
+  const int per = (a.n_seq + kAttnThreads - 1) / kAttnThreads;
+  const int seq0 = min(a.n_seq, (int)threadIdx.x * per), seq1 = min(a.n_seq, seq0 + per);
+  long long mine = 0;
+  for (int s = seq0; s < seq1; ++s) mine += (length_of(a, s, BT) + BT - 1) / BT;
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
   }
-
-  auto load = [&](int i, int block) {  // entry i of the list into its stage
-    const int s = i % R::STAGES;
-    const size_t at = ((size_t)block * a.kv_heads + kvh) * R::BLOCK;
-    mbar_arrive_expect_tx(&full[s], 2 * R::BLOCK);
-    bulk_load(smem + s * 2 * R::BLOCK, a.k_codes + at, R::BLOCK, &full[s]);
-    bulk_load(smem + s * 2 * R::BLOCK + R::BLOCK, a.v_codes + at, R::BLOCK, &full[s]);
-  };
-  if (warp == kConsumers) {  // the cache blocks of this range, those that exist
+  if (lane == 31) warp_sum[warp] = upto;
+  if (warp == kConsumers) {
     if (lane < R::STAGES) {
       mbar_init(&full[lane], 1);
       mbar_init(&empty[lane], 2);  // the two warps of a pair
     }
     if (lane == 0) s_abort = 0;
     fence_mbar_init();
-    __syncwarp();
-    int n = 0;
-    for (int p = p0; p < p1; p += 32) {
-      const int b = p + lane < p1
-                        ? block_of(a.table, a.width, seq, p + lane, a.n_blocks, a.err) : -1;
-      const uint32_t mask = __ballot_sync(0xffffffffu, b >= 0);
-      if (b >= 0) {
-        const int i = n + __popc(mask & ((1u << lane) - 1u));
-        if (i < R::STAGES) load(i, b);  // the first ones go out at once
-        const size_t at = (size_t)b * a.kv_heads + kvh;
-        list[i] = Entry{b, p + lane, a.k_scales[at], a.v_scales[at]};
-      }
-      n += __popc(mask);
+  }
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kAttnThreads / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  before += upto - mine;  // cache blocks of the sequences before seq0
+  const long long units = total * heads;
+  long long ranges = (units + kMinUnits - 1) / kMinUnits;
+  if (ranges > gridDim.x) ranges = gridDim.x;
+  const bool idle = (long long)blockIdx.x >= ranges;
+  const long long u0 = idle ? 0 : units * blockIdx.x / ranges;
+  const long long u1 = idle ? 0 : units * (blockIdx.x + 1) / ranges;
+  if (!idle && u0 >= before * heads && u0 < (before + mine) * heads) {
+    int s = seq0;
+    long long at = before;
+    for (;; ++s) {
+      const int pages = (length_of(a, s, BT) + BT - 1) / BT;
+      if (u0 < (at + pages) * heads) break;
+      at += pages;
     }
-    if (lane == 0) s_n = n;
-  } else {
-    // q rows -> fp16 times a power of two, through shared memory
+    s_seq = s;
+    s_before = at;
+  }
+  // sequences with nothing cached get zeros
+  for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x)
+    if (length_of(a, s, BT) == 0)
+      for (int i = threadIdx.x; i < q_heads * D; i += kAttnThreads) a.o[s * a.o_stride + i] = 0;
+  if (idle) {
+    if (threadIdx.x == 0 && a.cut) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  __syncthreads();
+  int seq = s_seq;
+  int len = length_of(a, seq, BT), pages = (len + BT - 1) / BT;
+  int hg, page;
+  {
+    const long long in = u0 - s_before * heads;
+    hg = (int)(in / pages);
+    page = (int)(in - (long long)hg * pages);
+  }
+  const int n_units = (int)(u1 - u0);  // at most 2^31: a range is a fraction of the pool
+  // on to the next (sequence, head group)
+  auto next_pair = [&]() {
+    page = 0;
+    if (++hg < heads) return;
+    hg = 0;
+    do ++seq; while ((len = length_of(a, seq, BT)) == 0);
+    pages = (len + BT - 1) / BT;
+  };
+  const WaitCtx wc{a.err, &s_abort};
+
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------ producer
+    bool ok = true;
+    int i = 0;  // units listed and issued
+    while (i < n_units && ok) {
+      const int n = min(min(32, pages - page), n_units - i);
+      const int kvh = hg / a.row_groups;
+      if (lane < n) {
+        const int b = block_of(a.table, a.width, seq, page + lane, a.n_blocks, a.err);
+        const size_t at = (size_t)max(b, 0) * a.kv_heads + kvh;
+        list[(i + lane) % kListSize] = Entry{b, page + lane, b < 0 ? 0.f : a.k_scales[at],
+                                             b < 0 ? 0.f : a.v_scales[at]};
+      }
+      __syncwarp();
+      if (lane == 0) {
+        for (int k = i; k < i + n; ++k) {
+          const int s = k % R::STAGES;
+          if (!mbar_wait(&empty[s], ((k / R::STAGES) & 1) ^ 1, wc)) {
+            ok = false;
+            // let issued copies land before the block retires
+            for (int j = k > R::STAGES ? k - R::STAGES : 0; j < k; ++j)
+              mbar_drain(&full[j % R::STAGES], (j / R::STAGES) & 1);
+            break;
+          }
+          const int block = list[k % kListSize].block;
+          if (block < 0) {
+            mbar_arrive(&full[s]);  // nothing to load, nothing to attend
+            continue;
+          }
+          const size_t at = ((size_t)block * a.kv_heads + kvh) * R::BLOCK;
+          uint8_t* dst = smem + R::SUMS + s * 2 * R::BLOCK;
+          mbar_arrive_expect_tx(&full[s], 2 * R::BLOCK);
+          bulk_load(dst, a.k_codes + at, R::BLOCK, &full[s]);
+          bulk_load(dst + R::BLOCK, a.v_codes + at, R::BLOCK, &full[s]);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      i += n;
+      page += n;
+      if (i < n_units && page == pages) next_pair();
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g = lane >> 2, t = lane & 3;
+  const int half = warp & 1;
+  float* sums = reinterpret_cast<float*>(smem);  // [2][16][D]
+  int unit = 0;
+  bool have_cut = false;
+  while (unit < n_units) {
+    const int kvh = hg / a.row_groups, h0 = (hg - kvh * a.row_groups) * kRows;
+    const int rows = min(kRows, a.group - h0), head0 = kvh * a.group + h0;
+    const int n = min(pages - page, n_units - unit);  // this segment's units
+    const bool begins = page == 0, ends = page + n == pages;
+    // q rows -> fp16 times a power of two
     for (int r = warp; r < kRows; r += kConsumers) {
       float x[D / 32], m = 0.f;
 #pragma unroll
@@ -363,61 +489,37 @@ __global__ void __launch_bounds__(kAttnThreads, 2) k_cache_attention(const AttnA
       const bool fine = m <= kMaxFinite;
 #pragma unroll
       for (int e = 0; e < D / 32; ++e)
-        qs[r * (D + 8) + e * 32 + lane] = __float2half_rn(fine ? x[e] * down : 0.f);
+        qs[r * QP + e * 32 + lane] = __float2half_rn(fine ? x[e] * down : 0.f);
       if (lane == 0) q_mul[r] = fine ? up * a.scale_log2 : __int_as_float(0x7fc00000);
     }
-  }
-  __syncthreads();
-  const int n = s_n;
-  const WaitCtx wc{a.err, &s_abort};
-  const int g = lane >> 2, t = lane & 3;
-  uint32_t qa[KM][4];
-  if (warp < kConsumers) {
-#pragma unroll
-    for (int m = 0; m < KM; ++m) {
-      const int d = 64 * (m >> 2) + 16 * t + 4 * (m & 3);  // the thread's four channels
-      const uint2 lo = *reinterpret_cast<const uint2*>(qs + g * (D + 8) + d);
-      const uint2 hi = *reinterpret_cast<const uint2*>(qs + (g + 8) * (D + 8) + d);
-      qa[m][0] = lo.x;
-      qa[m][1] = hi.x;
-      qa[m][2] = lo.y;
-      qa[m][3] = hi.y;
-    }
-  }
-
-  float acc[ND][4];
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-  if (warp == kConsumers) {
-    if (lane == 0) {
-      int i = min(n, R::STAGES);
-      bool ok = true;
-      for (; i < n; ++i) {
-        if (!mbar_wait(&empty[i % R::STAGES], ((i / R::STAGES) & 1) ^ 1, wc)) {
-          ok = false;
-          break;
-        }
-        load(i, list[i].block);
-      }
-      if (!ok)  // let issued copies land before the block retires
-        for (int j = i > R::STAGES ? i - R::STAGES : 0; j < i; ++j)
-          mbar_drain(&full[j % R::STAGES], (j / R::STAGES) & 1);
-    }
-  } else {
+    consumers_sync();
+    float acc[ND][4];
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[d][e] = 0.f;
-    const int half = warp & 1;
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     const float mul0 = q_mul[g], mul1 = q_mul[g + 8];
-    for (int i = warp >> 1; i < n; i += kConsumers / 2) {
+    bool ok = true;
+    // unit i belongs to the pair of warps i % 2
+    for (int i = unit + ((unit ^ (warp >> 1)) & 1); i < unit + n; i += 2) {
       const int s = i % R::STAGES;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (i / R::STAGES) & 1, wc))) break;
-      const Entry en = list[i];
-      const uint8_t* kb = smem + s * 2 * R::BLOCK;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (i / R::STAGES) & 1, wc))) {
+        ok = false;
+        break;
+      }
+      const Entry en = list[i % kListSize];
+      if (en.block < 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        continue;
+      }
+      const uint8_t* kb = smem + R::SUMS + s * 2 * R::BLOCK;
       const uint8_t* vb = kb + R::BLOCK;
       // column c of tile j is token HT / 4 * (c / 2) + 2 j + c % 2 of the half
       float sc[NJ][4];
       const uint8_t* krow = kb + (half * HT + (HT / 4) * (g >> 1) + (g & 1)) * D + 16 * t;
+      const __half* qrow = qs + g * QP + 16 * t;
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -434,13 +536,18 @@ __global__ void __launch_bounds__(kAttnThreads, 2) k_cache_attention(const AttnA
             w[j][0] = x.x, w[j][1] = x.y, w[j][2] = x.z, w[j][3] = x.w;
           }
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
+          for (int m = 0; m < 4; ++m) {
+            // the thread's four channels of rows g and g + 8
+            const uint2 lo = *reinterpret_cast<const uint2*>(qrow + 64 * h + 4 * m);
+            const uint2 hi = *reinterpret_cast<const uint2*>(qrow + 8 * QP + 64 * h + 4 * m);
+            const uint32_t qa[4] = {lo.x, hi.x, lo.y, hi.y};
 #pragma unroll
             for (int j = 0; j < JB; ++j) {
               uint32_t b0, b1;
               codes_to_f16(w[j][m], b0, b1);
-              mma_f16(sc[j0 + j], qa[4 * h + m], b0, b1);
+              mma_f16(sc[j0 + j], qa, b0, b1);
             }
+          }
         }
       }
       const float f0 = mul0 * en.ks, f1 = mul1 * en.ks;
@@ -524,146 +631,165 @@ __global__ void __launch_bounds__(kAttnThreads, 2) k_cache_attention(const AttnA
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
+    // ---- the segment's end: the warps' results become one
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
       l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
     }
-  }
-  __syncthreads();  // every stage has been read
-  float* sums = reinterpret_cast<float*>(smem);  // [consumer][16][D]
-  if (warp < kConsumers) {
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      float* p = sums + (warp * kRows + g) * D + 8 * d + 2 * t;
-      *reinterpret_cast<float2*>(p) = make_float2(acc[d][0], acc[d][1]);
-      *reinterpret_cast<float2*>(p + 8 * D) = make_float2(acc[d][2], acc[d][3]);
-    }
     if (t == 0) {
       stat[warp][g] = make_float2(m_run[0], l_run[0]);
       stat[warp][g + 8] = make_float2(m_run[1], l_run[1]);
     }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * D; i += kAttnThreads) {
-    const int r = i / D, d = i % D;
-    float m = -INFINITY;
+    consumers_sync();
+    float m_all[2], f[2], l_all[2] = {0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, stat[w][r].x);
-    float sum = 0.f, l = 0.f;
+    for (int r = 0; r < 2; ++r) {
+      m_all[r] = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kConsumers; ++w) {
-      const float2 ml = stat[w][r];
-      // a NaN sum has to survive: its maximum may be -inf
-      const float f = ml.x == m ? 1.f : exp2_mufu(ml.x - m);
-      sum = fmaf(sums[(w * kRows + r) * D + d], f, sum);
-      l = fmaf(ml.y, f, l);
+      for (int w = 0; w < kConsumers; ++w) m_all[r] = fmaxf(m_all[r], stat[w][g + 8 * r].x);
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) {
+        const float2 ml = stat[w][g + 8 * r];
+        // a NaN sum has to survive: its maximum may be -inf
+        l_all[r] = fmaf(ml.y, ml.x == m_all[r] ? 1.f : exp2_mufu(ml.x - m_all[r]), l_all[r]);
+      }
+      f[r] = m_run[r] == m_all[r] ? 1.f : exp2_mufu(m_run[r] - m_all[r]);
     }
-    if (alone) {
-      a.o[seq * a.o_stride + (head0 + r) * D + d] =
-          float_to_act(l == 0.f ? 0.f : sum / l, a.f16);
-    } else {
-      const size_t at = ((size_t)seq * q_heads + head0 + r) * a.splits + split;
-      a.part[at * D + d] = sum;
-      if (d == 0) a.stat[at] = make_float2(m, l);
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[d][e] *= f[e >> 1];
+    auto put = [&](float* to) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        float* p = to + g * D + 8 * d + 2 * t;
+        *reinterpret_cast<float2*>(p) = make_float2(acc[d][0], acc[d][1]);
+        *reinterpret_cast<float2*>(p + 8 * D) = make_float2(acc[d][2], acc[d][3]);
+      }
+    };
+    auto add = [&](const float* from) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const float* p = from + g * D + 8 * d + 2 * t;
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        const float2 y = *reinterpret_cast<const float2*>(p + 8 * D);
+        acc[d][0] += x.x, acc[d][1] += x.y, acc[d][2] += y.x, acc[d][3] += y.y;
+      }
+    };
+    if (warp >= 2) put(sums + (warp - 2) * kRows * D);
+    consumers_sync();
+    if (warp < 2) add(sums + warp * kRows * D);
+    if (warp == 1) put(sums + kRows * D);  // where this warp has just read
+    consumers_sync();
+    if (warp == 0) {
+      add(sums + kRows * D);
+      if (begins && ends) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          if (g + 8 * r >= rows) continue;
+          const float inv = l_all[r] == 0.f ? 0.f : 1.f / l_all[r];
+          uint16_t* o = a.o + seq * a.o_stride + (head0 + g + 8 * r) * D + 2 * t;
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+            *reinterpret_cast<uint32_t*>(o + 8 * d) =
+                (uint32_t)float_to_act(acc[d][2 * r] * inv, a.f16) |
+                (uint32_t)float_to_act(acc[d][2 * r + 1] * inv, a.f16) << 16;
+        }
+      } else {
+        const size_t at = ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kRows;
+        put(a.part + at * D);
+        if (t == 0) {
+          a.stat[at + g] = make_float2(m_all[0], l_all[0]);
+          a.stat[at + g + 8] = make_float2(m_all[1], l_all[1]);
+        }
+        if (begins) {
+          // the pair's last unit, the range it is in, and so the number of parts
+          const long long last = u0 + unit + pages - 1;
+          const int to = (int)(((last + 1) * ranges - 1) / units);
+          if (lane == 0)
+            a.cut[blockIdx.x] = make_int4(seq, hg, to - (int)blockIdx.x + 1, 0);
+          have_cut = true;
+        }
+      }
     }
+    unit += n;
+    page += n;
+    if (!ok) break;
+    if (unit < n_units) next_pair();
   }
+  if (threadIdx.x == 0 && !have_cut && a.cut) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
 }
 
-// Joins the ranges of the sequences that had more than one: a block per
-// (sequence, head), kJoinParts threads per channel, each taking every
-// kJoinParts-th range, so that the partial sums are fetched side by side.
-constexpr int kJoinParts = 4, kJoinTile = 128;
-
-template <int D, int BT>
-__global__ void __launch_bounds__(D * kJoinParts) k_cache_join(const AttnArgs a) {
-  __shared__ float factor[kJoinTile];
-  __shared__ float sums[kJoinParts][D], weights[kJoinParts];
+// Joins the parts of the pairs that were cut: a thread block per (range, row of
+// its last pair), a thread per channel.
+template <int D>
+__global__ void __launch_bounds__(D) k_cache_join(const AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the ranges' kernel is complete
-  const int q_heads = a.kv_heads * a.group;
-  const int seq = blockIdx.x / q_heads, head = blockIdx.x - seq * q_heads;
-  const int d = threadIdx.x % D, p = threadIdx.x / D, lane = threadIdx.x & 31;
-  const long long most = (long long)a.width * BT;
-  const int len = (int)min((long long)max(a.lengths[seq], 0), most);
-  const int n = ((len + BT - 1) / BT + a.chunk - 1) / a.chunk;
-  if (n <= 1) return;
-  const size_t at = (size_t)blockIdx.x * a.splits;
-  float m = -INFINITY;  // every warp for itself
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.stat[at + i].x);
+  const int4 cut = a.cut[blockIdx.x];
+  const int n = cut.z, r = blockIdx.y, d = threadIdx.x;
+  const int kvh = cut.y / a.row_groups, h0 = (cut.y - kvh * a.row_groups) * kRows;
+  if (n == 0 || h0 + r >= a.group) return;
+  // part 1 of its own range, part 0 of the following ones
+  auto at = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kRows + r; };
+  float m = -INFINITY;
+  for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, a.stat[at(i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float sum = 0.f, l = 0.f;
-  for (int i0 = 0; i0 < n; i0 += kJoinTile) {
-    const int k = min(kJoinTile, n - i0);
-    __syncthreads();
-    if (threadIdx.x < k) {
-      const float2 ml = a.stat[at + i0 + threadIdx.x];
-      const float f = ml.x == m ? 1.f : exp2_mufu(ml.x - m);
-      factor[threadIdx.x] = f;
-      l = fmaf(ml.y, f, l);
-    }
-    __syncthreads();
-    const float* part = a.part + (at + i0) * D + d;
 #pragma unroll 8
-    for (int i = p; i < k; i += kJoinParts) sum = fmaf(part[(size_t)i * D], factor[i], sum);
+  for (int i = 0; i < n; ++i) {
+    const float2 ml = a.stat[at(i)];
+    const float f = ml.x == m ? 1.f : exp2_mufu(ml.x - m);
+    sum = fmaf(a.part[at(i) * D + d], f, sum);
+    l = fmaf(ml.y, f, l);
   }
-  sums[p][d] = sum;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  // the threads that held a weight are the first kJoinTile = 4 warps
-  if (lane == 0 && threadIdx.x < kJoinTile) weights[threadIdx.x / 32] = l;
-  __syncthreads();
-  if (p == 0) {
-    float total = 0.f, w = 0.f;
-#pragma unroll
-    for (int i = 0; i < kJoinParts; ++i) total += sums[i][d];
-#pragma unroll
-    for (int i = 0; i < kJoinTile / 32; ++i) w += weights[i];
-    a.o[seq * a.o_stride + head * D + d] = float_to_act(w == 0.f ? 0.f : total / w, a.f16);
-  }
+  a.o[cut.x * a.o_stride + (kvh * a.group + h0 + r) * D + d] =
+      float_to_act(l == 0.f ? 0.f : sum / l, a.f16);
 }
 
-// How the tokens are split: cache blocks per thread block, such that two thread
-// blocks per SM exist when every sequence is as long as its table, at most
-// kMaxChunk; and the number of ranges that gives.
-void split_of(int n_seq, int heads, int width, int& chunk, int& splits) {
+// Thread blocks of an attention call: as many as run at once, at most one per
+// kMinUnits units of tables that are full.
+template <int D, int BT>
+int ranges_of(int n_seq, int heads, int width) {
   const long long units = (long long)n_seq * heads * width;
-  const long long at_once = 2 * num_sms();
-  long long c = (units + at_once - 1) / at_once;
-  if (c > kMaxChunk) c = kMaxChunk;
-  if (c > width) c = width;
-  chunk = (int)c;
-  splits = (width + chunk - 1) / chunk;
+  const long long most = (long long)num_sms() * Ring<D, BT>::PER_SM;
+  const long long n = (units + kMinUnits - 1) / kMinUnits;
+  return (int)(n < most ? n : most);
 }
+
+size_t part_bytes(int ranges, int D) { return (size_t)ranges * 2 * kRows * D * 4; }
+size_t stat_bytes(int ranges) { return (size_t)ranges * 2 * kRows * 8; }
 
 template <int D, int BT>
-cudaError_t run_attention(AttnArgs& a, int n_seq, cudaStream_t st) {
+cudaError_t run_attention(AttnArgs& a, void* ws, cudaStream_t st) {
   constexpr int BYTES = Ring<D, BT>::BYTES;
   cudaError_t e = cudaFuncSetAttribute(k_cache_attention<D, BT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
   if (e != cudaSuccess) return e;
-  const long long blocks = (long long)n_seq * a.splits * a.kv_heads * a.row_groups;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  k_cache_attention<D, BT><<<(unsigned)blocks, kAttnThreads, BYTES, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
-  const long long heads = (long long)n_seq * a.kv_heads * a.group;
-  if (heads > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int ranges = ranges_of<D, BT>(a.n_seq, a.kv_heads * a.row_groups, a.width);
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  a.part = reinterpret_cast<float*>(p);
+  a.stat = reinterpret_cast<float2*>(p + part_bytes(ranges, D));
+  a.cut = reinterpret_cast<int4*>(p + part_bytes(ranges, D) + stat_bytes(ranges));
+  k_cache_attention<D, BT><<<(unsigned)ranges, kAttnThreads, BYTES, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // launched while the ranges run, to wait for them on the GPU
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)heads);
-  cfg.blockDim = dim3(D * kJoinParts);
+  cfg.gridDim = dim3((unsigned)ranges, (unsigned)(a.group < kRows ? a.group : kRows));
+  cfg.blockDim = dim3(D);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_cache_join<D, BT>, a);
+  return cudaLaunchKernelEx(&cfg, k_cache_join<D>, a);
 }
 
 template <h3_type T, int D>
 cudaError_t run_store(const StoreArgs& a, int n_seq, int block_tokens, cudaStream_t st) {
-  const long long blocks = 2ll * n_seq * a.pages * a.kv_heads;
+  const long long blocks = (long long)n_seq * a.pages * a.kv_heads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)blocks;
   if (block_tokens == 32) k_kv_store<T, D, 32><<<grid, kStoreThreads, 0, st>>>(a);
@@ -671,8 +797,6 @@ cudaError_t run_store(const StoreArgs& a, int n_seq, int block_tokens, cudaStrea
   else k_kv_store<T, D, 128><<<grid, kStoreThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
-
-size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
@@ -685,14 +809,14 @@ cudaError_t launch_kv_cache_store(const h3_kv_cache& c, int n_seq, int max_new,
   a.table = table;
   a.lengths = lengths;
   a.offsets = offsets;
-  a.k = static_cast<const uint16_t*>(k);
-  a.v = static_cast<const uint16_t*>(v);
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.k_codes = static_cast<uint8_t*>(c.k_codes);
-  a.v_codes = static_cast<uint8_t*>(c.v_codes);
-  a.k_scales = c.k_scales;
-  a.v_scales = c.v_scales;
+  a.x[0] = static_cast<const uint16_t*>(k);
+  a.x[1] = static_cast<const uint16_t*>(v);
+  a.stride[0] = k_stride;
+  a.stride[1] = v_stride;
+  a.codes[0] = static_cast<uint8_t*>(c.k_codes);
+  a.codes[1] = static_cast<uint8_t*>(c.v_codes);
+  a.scales[0] = c.k_scales;
+  a.scales[1] = c.v_scales;
   a.n_blocks = c.n_blocks;
   a.kv_heads = c.kv_heads;
   a.width = width;
@@ -710,12 +834,14 @@ cudaError_t launch_kv_cache_store(const h3_kv_cache& c, int n_seq, int max_new,
 }
 
 size_t cache_attention_workspace(const h3_kv_cache& c, int n_seq, int q_heads, int width) {
-  const int group = q_heads / c.kv_heads;
-  int chunk, splits;
-  split_of(n_seq, c.kv_heads * ((group + kRows - 1) / kRows), width, chunk, splits);
-  if (splits == 1) return 0;
-  const size_t n = (size_t)n_seq * q_heads * splits;
-  return align256(n * c.head_dim * 4) + align256(n * 8);
+  const int heads = c.kv_heads * ((q_heads / c.kv_heads + kRows - 1) / kRows);
+#define H3_RANGES(D)                                                      \
+  (c.block_tokens == 32 ? ranges_of<D, 32>(n_seq, heads, width)           \
+   : c.block_tokens == 64 ? ranges_of<D, 64>(n_seq, heads, width)         \
+                          : ranges_of<D, 128>(n_seq, heads, width))
+  const int ranges = c.head_dim == 128 ? H3_RANGES(128) : H3_RANGES(64);
+#undef H3_RANGES
+  return part_bytes(ranges, c.head_dim) + stat_bytes(ranges) + (size_t)ranges * sizeof(int4);
 }
 
 cudaError_t launch_cache_attention(const h3_kv_cache& c, int n_seq, int q_heads,
@@ -734,23 +860,19 @@ cudaError_t launch_cache_attention(const h3_kv_cache& c, int n_seq, int q_heads,
   a.o = static_cast<uint16_t*>(o);
   a.q_stride = q_stride;
   a.o_stride = o_stride;
+  a.n_seq = n_seq;
   a.n_blocks = c.n_blocks;
   a.kv_heads = c.kv_heads;
   a.group = q_heads / c.kv_heads;
   a.row_groups = (a.group + kRows - 1) / kRows;
   a.width = width;
-  split_of(n_seq, a.kv_heads * a.row_groups, width, a.chunk, a.splits);
-  a.part = static_cast<float*>(ws);
-  a.stat = reinterpret_cast<float2*>(
-      static_cast<uint8_t*>(ws) +
-      align256((size_t)n_seq * q_heads * a.splits * c.head_dim * 4));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.f16 = f16;
   a.err = err;
 #define H3_RUN(D)                                                        \
-  (c.block_tokens == 32 ? run_attention<D, 32>(a, n_seq, st)             \
-   : c.block_tokens == 64 ? run_attention<D, 64>(a, n_seq, st)           \
-                          : run_attention<D, 128>(a, n_seq, st))
+  (c.block_tokens == 32 ? run_attention<D, 32>(a, ws, st)                \
+   : c.block_tokens == 64 ? run_attention<D, 64>(a, ws, st)              \
+                          : run_attention<D, 128>(a, ws, st))
   return c.head_dim == 128 ? H3_RUN(128) : H3_RUN(64);
 #undef H3_RUN
 }

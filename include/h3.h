@@ -656,7 +656,7 @@ H3_API h3_status h3_kv_cache_store(const h3_kv_cache* cache, int n_seq, int max_
  * zeros. scale > 0, finite; q_heads % kv_heads == 0. A length that is negative
  * or past the table is limited to it, and a table entry that names no block
  * counts as tokens that are not there: both record an error (h3_text_error,
- * H3_ERR_LAYOUT). ws: h3_cache_attention_workspace_size bytes (0 for few tokens),
+ * H3_ERR_LAYOUT). ws: h3_cache_attention_workspace_size bytes (a few MB at most),
  * used only during the call's work: calls that overlap on the GPU need one each.
  * The result does not depend on the order in which the GPU runs things. Enqueues. */
 H3_API size_t h3_cache_attention_workspace_size(const h3_kv_cache* cache, int n_seq, int q_heads,
