@@ -213,33 +213,44 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
 // memory stages with bulk copies, and four consumer warps: two pairs take the
 // stages in turn, the warps of a pair half the tokens each, every warp with its
 // own running maximum, sum and accumulator (joined at the end of a segment), so
-// that nothing waits but on its data. The products run on m16n8k16 fp16 MMAs
-// (the query heads fill the 16 rows; the kernel is bound by bytes, and this form
-// takes its operands from registers, where the codes become fp16 exactly): the
-// 16-byte pieces a thread reads of a K row serve as four k-steps, since the order
-// of the channels inside a product is free, and the tokens are assigned to
-// columns so that the weights' registers are the A operand of the second product
-// and its V operand is one contiguous piece of a transposed V row.
+// that nothing waits but on its data.
 //
-// q enters fp16 times a power of two per row (exact but for elements below 2^-14
-// of the row's largest); the K scale is applied to the scores, the V scale to
-// each block's sum, both in float32. Weights are stored in fp16 times 2^10, so
-// that they stay normal numbers down to 2^-24 of the largest.
+// Both products have the tokens or channels on the 16-row side of the MMA and
+// the query heads on the 8-column side, eight heads per column tile. (This form
+// takes its operands from registers as the codes lie in shared memory; the kernel
+// is bound by bytes and then by the instructions per byte, not by the tensor
+// rate.) Scores: s^T = K q^T on 8-bit integers (m16n8k32), q as two 8-bit limbs of
+// a 16-bit fixed-point row (an error of at most 2^-16 of the row's largest
+// element), the sums exact. Values: o^T += V^T w^T on fp16 (m16n8k16), where the
+// codes become fp16 exactly and the weights are fp16, times 2^10 so that they
+// stay normal numbers down to 2^-24 of the largest, and times the block's V scale
+// over the largest one met so far, so that the sums of all blocks share one
+// accumulator. The K scale is applied to the scores in float32. A thread reads
+// 16-byte pieces of a K row as four k-quads, since the order of the channels in a
+// product is free, and the tokens are assigned to rows so that its V operand is
+// one contiguous piece of a transposed V row; the weights turn between the two
+// layouts by 8 x 8 transposes across the warp.
 constexpr int kAttnThreads = 160, kConsumers = 4;
-constexpr int kRows = 16;
+constexpr int kMaxCols = 2;     // column tiles of eight heads a warp takes at most
 constexpr int kListSize = 64;   // entries of the producer's list, two batches of 32
 constexpr int kMinUnits = 2;    // cache blocks a thread block takes at least
 
-template <int D, int BT>
+template <int D, int BT, int NC>  // NC column tiles: ROWS = 8 NC query heads per pass
 struct Ring {
+  static constexpr int ROWS = 8 * NC;
   static constexpr int BLOCK = BT * D;  // bytes of K (or V) codes
-  // Thread blocks per SM, and the stages that fit beside the sums.
-  static constexpr int PER_SM = BLOCK >= 16384 ? 2 : 3;
-  static constexpr int STAGES = BLOCK >= 16384 ? 2 : 49152 / (2 * BLOCK) < 16 ? 49152 / (2 * BLOCK)
-                                                                              : 16;
-  static constexpr int SUMS = 2 * kRows * D * 4;  // two warps' accumulators
+  // thread blocks per SM: three where the accumulators leave the registers for it
+  static constexpr int PER_SM = BLOCK >= 16384 || D * NC == 256 ? 2 : 3;
+  static constexpr int FIT = (PER_SM == 2 ? 98304 : 65536) / (2 * BLOCK);
+  // Even, so that a stage always serves the same pair of warps: a warp that waits
+  // for a stage's next fill has then seen its last one, and cannot take an older
+  // phase of the same parity for the one it waits for.
+  static constexpr int STAGES = FIT < 16 ? FIT / 2 * 2 : 16;
+  static constexpr int PITCH = D + 4;   // floats; the accumulators' stores meet no bank twice
+  static constexpr int SUMS = 2 * ROWS * PITCH * 4;  // two warps' accumulators
   static constexpr int BYTES = STAGES * 2 * BLOCK + SUMS;
   static_assert(STAGES <= kListSize - 32, "a list entry outlives its stage");
+  static_assert(SUMS % 128 == 0, "stage alignment");
 };
 
 struct Entry {
@@ -255,12 +266,12 @@ struct AttnArgs {
   uint16_t* o;
   int64_t q_stride, o_stride;
   // workspace, per thread block: two parts (0: a pair begun earlier, 1: a pair
-  // that goes on) of 16 rows of sums and of (maximum, sum of weights), and which
-  // pair part 1 belongs to, with the number of its parts
-  float* part;    // [blocks][2][16][D]
-  float2* stat;   // [blocks][2][16]
+  // that goes on) of `pass` rows of sums and of (maximum, sum of weights), and
+  // which pair part 1 belongs to, with the number of its parts
+  float* part;    // [blocks][2][pass][D]
+  float2* stat;   // [blocks][2][pass]
   int4* cut;      // [blocks] {sequence, head group, parts, 0}
-  int n_seq, n_blocks, kv_heads, group, row_groups, width;
+  int n_seq, n_blocks, kv_heads, group, row_groups, pass, width;
   float scale_log2;
   bool f16;
   int* err;
@@ -284,6 +295,22 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_s8(int (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The 8 x 8 matrix of 16-bit elements held two a thread, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 // Four int8 codes as two fp16 pairs: code + 128 in the mantissa of 1024 + x.
 __device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
   c ^= 0x80808080u;
@@ -300,9 +327,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ float act_to_float(uint16_t u, bool f16) {
-  return f16 ? __half2float(__ushort_as_half(u)) : __uint_as_float((uint32_t)u << 16);
-}
 __device__ __forceinline__ uint16_t float_to_act(float v, bool f16) {
   return f16 ? __half_as_ushort(__float2half_rn(v))
              : __bfloat16_as_ushort(__float2bfloat16_rn(v));
@@ -321,21 +345,21 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
-template <int D, int BT>
-__global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
+template <int D, int BT, int NC>
+__global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
     k_cache_attention(const AttnArgs a) {
-  using R = Ring<D, BT>;
+  using R = Ring<D, BT, NC>;
+  constexpr int ROWS = R::ROWS, PITCH = R::PITCH;
   constexpr int HT = BT / 2;     // tokens of a warp per cache block
-  constexpr int NJ = HT / 8;     // its 8-token column tiles
-  constexpr int ND = D / 8;      // 8-channel column tiles of the output
-  constexpr int QP = D + 4;      // row pitch of q: its 8-byte pieces meet no bank twice
+  constexpr int NB = HT / 8;     // its blocks of eight tokens
+  constexpr int NH = D / 64;     // 64-channel halves of a K row
+  constexpr int ND = D / 16;     // 16-channel row tiles of the output
   constexpr float kShift = 10.f;
+  constexpr float kFixed = 32512.f;  // 127 * 256: the largest element of a q row
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) __half qs[kRows * QP];
   __shared__ uint64_t full[R::STAGES], empty[R::STAGES];
   __shared__ Entry list[kListSize];
-  __shared__ float q_mul[kRows];
-  __shared__ float2 stat[kConsumers][kRows];
+  __shared__ float2 stat[kConsumers][ROWS];
   __shared__ long long warp_sum[kAttnThreads / 32];
   __shared__ long long s_before;  // cache blocks before the range's first sequence
   __shared__ int s_seq, s_abort;
@@ -394,7 +418,7 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
     if (length_of(a, s, BT) == 0)
       for (int i = threadIdx.x; i < q_heads * D; i += kAttnThreads) a.o[s * a.o_stride + i] = 0;
   if (idle) {
-    if (threadIdx.x == 0 && a.cut) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
   __syncthreads();
@@ -464,42 +488,69 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, t = lane & 3;
   const int half = warp & 1;
-  float* sums = reinterpret_cast<float*>(smem);  // [2][16][D]
+  float* sums = reinterpret_cast<float*>(smem);  // [2][ROWS][PITCH]
   int unit = 0;
   bool have_cut = false;
   while (unit < n_units) {
-    const int kvh = hg / a.row_groups, h0 = (hg - kvh * a.row_groups) * kRows;
-    const int rows = min(kRows, a.group - h0), head0 = kvh * a.group + h0;
+    const int kvh = hg / a.row_groups, h0 = (hg - kvh * a.row_groups) * ROWS;
+    const int rows = min(ROWS, a.group - h0), head0 = kvh * a.group + h0;
     const int n = min(pages - page, n_units - unit);  // this segment's units
     const bool begins = page == 0, ends = page + n == pages;
-    // q rows -> fp16 times a power of two
-    for (int r = warp; r < kRows; r += kConsumers) {
-      float x[D / 32], m = 0.f;
+    // q rows -> 16-bit fixed point, two limbs. Column g of tile c is head 8 c + g;
+    // the thread's channels are 64 h + 16 t + 0..15.
+    uint32_t qh[NC][NH][4], ql[NC][NH][4];
+    float mul[NC][2];  // of heads 8 c + 2 t, + 1
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        x[e] = r < rows ? act_to_float(a.q[seq * a.q_stride + (head0 + r) * D + e * 32 + lane],
-                                       a.f16) : 0.f;
-        m = max_nan(m, fabsf(x[e]));
-      }
+    for (int c = 0; c < NC; ++c) {
+      const bool there = 8 * c + g < rows;
+      const uint16_t* q = a.q + seq * a.q_stride + (head0 + (there ? 8 * c + g : 0)) * D + 16 * t;
+      float x[NH][16], m = 0.f;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      // 2^e with m 2^-e in [1, 2); rows of zeros and tiny rows as they are
-      const uint32_t ex = min(max(__float_as_uint(m) & 0x7f800000u, 0x01000000u), 0x7e000000u);
-      const float up = __uint_as_float(ex), down = __uint_as_float(0x7f000000u - ex);
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          const uint4 u = *reinterpret_cast<const uint4*>(q + 64 * h + e);
+          if (a.f16) unpack<H3_F16>(u, &x[h][e]);
+          else unpack<H3_BF16>(u, &x[h][e]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) m = max_nan(m, fabsf(x[h][e + k]));
+        }
+      m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const bool fine = m <= kMaxFinite;
+      // (a row below 1e-34 counts as zeros: its fixed-point factor would overflow)
+      const float inv = there && fine && m > 1e-34f ? kFixed / m : 0.f;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e)
-        qs[r * QP + e * 32 + lane] = __float2half_rn(fine ? x[e] * down : 0.f);
-      if (lane == 0) q_mul[r] = fine ? up * a.scale_log2 : __int_as_float(0x7fc00000);
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int v = fine ? __float2int_rn(x[h][4 * w + k] * inv) : 0;
+            hi[k] = (uint32_t)((v + 128) >> 8);
+            lo[k] = (uint32_t)v;  // its low byte, signed, is v - 256 hi
+          }
+          qh[c][h][w] = pack4(hi[0], hi[1], hi[2], hi[3]);
+          ql[c][h][w] = pack4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      const float f = fine ? m * (a.scale_log2 / kFixed) : __int_as_float(0x7fc00000);
+      mul[c][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+      mul[c][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }
-    consumers_sync();
-    float acc[ND][4];
+    // rows 16 d + g (+ 8) are channels, columns heads
+    float acc[NC][ND][4];
+    float m_run[NC][2], l_run[NC][2];
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+    for (int c = 0; c < NC; ++c) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[d][e] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
-    const float mul0 = q_mul[g], mul1 = q_mul[g + 8];
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[c][d][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) m_run[c][k] = -INFINITY, l_run[c][k] = 0.f;
+    }
+    float v_top = 0.f;  // the accumulator holds sums over V scale / v_top
     bool ok = true;
     // unit i belongs to the pair of warps i % 2
     for (int i = unit + ((unit ^ (warp >> 1)) & 1); i < unit + n; i += 2) {
@@ -516,201 +567,235 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
       }
       const uint8_t* kb = smem + R::SUMS + s * 2 * R::BLOCK;
       const uint8_t* vb = kb + R::BLOCK;
-      // column c of tile j is token HT / 4 * (c / 2) + 2 j + c % 2 of the half
-      float sc[NJ][4];
+      // row r of block b is token HT / 4 * (r / 2) + 2 b + r % 2 of the half
       const uint8_t* krow = kb + (half * HT + (HT / 4) * (g >> 1) + (g & 1)) * D + 16 * t;
-      const __half* qrow = qs + g * QP + 16 * t;
+      float sc[NC][NB / 2][4];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+      for (int b = 0; b < NB / 2; ++b) {
+        int hi[NC][4], lo[NC][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        constexpr int JB = NJ < 4 ? NJ : 4;  // independent products in flight
+          for (int e = 0; e < 4; ++e) hi[c][e] = lo[c][e] = 0;
 #pragma unroll
-        for (int j0 = 0; j0 < NJ; j0 += JB) {
-          uint32_t w[JB][4];
+        for (int h = 0; h < NH; ++h) {
+          const uint4 x = *reinterpret_cast<const uint4*>(krow + 4 * b * D + 64 * h);
+          const uint4 y = *reinterpret_cast<const uint4*>(krow + (4 * b + 2) * D + 64 * h);
+          const uint32_t k0[4] = {x.x, y.x, x.y, y.y}, k1[4] = {x.z, y.z, x.w, y.w};
 #pragma unroll
-          for (int j = 0; j < JB; ++j) {
-            const uint4 x = *reinterpret_cast<const uint4*>(krow + 2 * (j0 + j) * D + 64 * h);
-            w[j][0] = x.x, w[j][1] = x.y, w[j][2] = x.z, w[j][3] = x.w;
-          }
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            // the thread's four channels of rows g and g + 8
-            const uint2 lo = *reinterpret_cast<const uint2*>(qrow + 64 * h + 4 * m);
-            const uint2 hi = *reinterpret_cast<const uint2*>(qrow + 8 * QP + 64 * h + 4 * m);
-            const uint32_t qa[4] = {lo.x, hi.x, lo.y, hi.y};
-#pragma unroll
-            for (int j = 0; j < JB; ++j) {
-              uint32_t b0, b1;
-              codes_to_f16(w[j][m], b0, b1);
-              mma_f16(sc[j0 + j], qa, b0, b1);
-            }
+          for (int c = 0; c < NC; ++c) {
+            mma_s8(hi[c], k0, qh[c][h][0], qh[c][h][1]);
+            mma_s8(lo[c], k0, ql[c][h][0], ql[c][h][1]);
+            mma_s8(hi[c], k1, qh[c][h][2], qh[c][h][3]);
+            mma_s8(lo[c], k1, ql[c][h][2], ql[c][h][3]);
           }
         }
-      }
-      const float f0 = mul0 * en.ks, f1 = mul1 * en.ks;
-      const int base = en.page * BT + half * HT + (HT / 4) * t;  // the thread's first token
-      float mx0 = -INFINITY, mx1 = -INFINITY;
-      if ((en.page + 1) * BT > len) {
+        // |sum| <= 128 * 127 * (256 * 127 + 128) < 2^31
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[c][b][e] = (float)(hi[c][e] * 256 + lo[c][e]);
+      }
+      // scores in log2 units; tokens behind the end
+      const int base = en.page * BT + half * HT + (HT / 4) * (g >> 1) + (g & 1);
+      const bool cut = (en.page + 1) * BT > len;
+      float mx[NC][2];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const float f[2] = {mul[c][0] * en.ks, mul[c][1] * en.ks};
+        mx[c][0] = mx[c][1] = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < NB / 2; ++b)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sc[j][e] *= e < 2 ? f0 : f1;
-            if (base + 2 * j + (e & 1) >= len) sc[j][e] = -INFINITY;
+            sc[c][b][e] *= f[e & 1];
+            if (cut && base + 4 * b + (e & 2) >= len) sc[c][b][e] = -INFINITY;
+            mx[c][e & 1] = fmaxf(mx[c][e & 1], sc[c][b][e]);
           }
-      } else {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[j][e] *= e < 2 ? f0 : f1;
       }
+      bool grows = fabsf(en.vs) > v_top;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        mx0 = max3(mx0, sc[j][0], sc[j][1]);
-        mx1 = max3(mx1, sc[j][2], sc[j][3]);
-      }
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-      if (__any_sync(0xffffffffu, mx0 > m_run[0] || mx1 > m_run[1])) {
-        const float n0 = fmaxf(m_run[0], mx0), n1 = fmaxf(m_run[1], mx1);
-        const float a0 = n0 > m_run[0] ? exp2_mufu(m_run[0] - n0) : 1.f;
-        const float a1 = n1 > m_run[1] ? exp2_mufu(m_run[1] - n1) : 1.f;
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          acc[d][0] *= a0;
-          acc[d][1] *= a0;
-          acc[d][2] *= a1;
-          acc[d][3] *= a1;
+        for (int k = 0; k < 2; ++k) {
+          mx[c][k] = fmaxf(mx[c][k], __shfl_xor_sync(0xffffffffu, mx[c][k], 4));
+          mx[c][k] = fmaxf(mx[c][k], __shfl_xor_sync(0xffffffffu, mx[c][k], 8));
+          mx[c][k] = fmaxf(mx[c][k], __shfl_xor_sync(0xffffffffu, mx[c][k], 16));
+          grows |= mx[c][k] > m_run[c][k];
         }
-        l_run[0] *= a0;
-        l_run[1] *= a1;
-        m_run[0] = n0;
-        m_run[1] = n1;
-      }
-      // a row that has seen no token yet has maximum -inf: its weights are 0
-      const float s0 = kShift - (m_run[0] == -INFINITY ? 0.f : m_run[0]);
-      const float s1 = kShift - (m_run[1] == -INFINITY ? 0.f : m_run[1]);
-      uint32_t pa[NJ / 2][4];
+      if (__any_sync(0xffffffffu, grows)) {
+        // a new largest V scale with some room, so that few follow
+        const float top = fabsf(en.vs) > v_top ? 1.5f * fabsf(en.vs) : v_top;
+        const float vf = top > v_top ? v_top / top : 1.f;
+        v_top = top;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const float p0 = exp2_mufu(sc[j][0] + s0), p1 = exp2_mufu(sc[j][1] + s0);
-        const float p2 = exp2_mufu(sc[j][2] + s1), p3 = exp2_mufu(sc[j][3] + s1);
-        l_run[0] += p0 + p1;
-        l_run[1] += p2 + p3;
-        pa[j / 2][2 * (j & 1)] = pack_f16x2(p0, p1);
-        pa[j / 2][2 * (j & 1) + 1] = pack_f16x2(p2, p3);
+        for (int c = 0; c < NC; ++c) {
+          float f[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float to = fmaxf(m_run[c][k], mx[c][k]);
+            f[k] = to > m_run[c][k] ? exp2_mufu(m_run[c][k] - to) : 1.f;
+            l_run[c][k] *= f[k];
+            m_run[c][k] = to;
+          }
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[c][d][e] *= f[e & 1] * vf;
+        }
+      }
+      // weights, turned so that a thread has head g's tokens 2 t, 2 t + 1 of a block
+      const float ratio = en.vs == 0.f ? 0.f : en.vs / v_top;
+      uint32_t pb[NC][NB];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float sub[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)  // a head that has seen no token has maximum -inf: weights 0
+          sub[k] = kShift - (m_run[c][k] == -INFINITY ? 0.f : m_run[c][k]);
+#pragma unroll
+        for (int b = 0; b < NB / 2; ++b) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = exp2_mufu(sc[c][b][e] + sub[e & 1]);
+            l_run[c][e & 1] += p[e];
+          }
+          pb[c][2 * b] = transpose8(pack_f16x2(p[0] * ratio, p[1] * ratio));
+          pb[c][2 * b + 1] = transpose8(pack_f16x2(p[2] * ratio, p[3] * ratio));
+        }
       }
       const uint8_t* vrow = vb + g * BT + half * HT + (HT / 4) * t;
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
-        uint32_t w[NJ / 2];
-        if constexpr (NJ == 8) {
-          const uint4 x = *reinterpret_cast<const uint4*>(vrow + 8 * d * BT);
-          w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-        } else if constexpr (NJ == 4) {
-          const uint2 x = *reinterpret_cast<const uint2*>(vrow + 8 * d * BT);
-          w[0] = x.x, w[1] = x.y;
-        } else {
-          w[0] = *reinterpret_cast<const uint32_t*>(vrow + 8 * d * BT);
-        }
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t w[2][NB / 2];  // rows g and g + 8
 #pragma unroll
-        for (int k = 0; k < NJ / 2; ++k) {
-          uint32_t b0, b1;
-          codes_to_f16(w[k], b0, b1);
-          mma_f16(c, pa[k], b0, b1);
+        for (int r = 0; r < 2; ++r) {
+          const uint8_t* v = vrow + (16 * d + 8 * r) * BT;
+          if constexpr (NB == 8) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v);
+            w[r][0] = x.x, w[r][1] = x.y, w[r][2] = x.z, w[r][3] = x.w;
+          } else if constexpr (NB == 4) {
+            const uint2 x = *reinterpret_cast<const uint2*>(v);
+            w[r][0] = x.x, w[r][1] = x.y;
+          } else {
+            w[r][0] = *reinterpret_cast<const uint32_t*>(v);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[d][e] = fmaf(en.vs, c[e], acc[d][e]);
+        for (int k = 0; k < NB / 2; ++k) {
+          uint32_t va[4];
+          codes_to_f16(w[0][k], va[0], va[2]);
+          codes_to_f16(w[1][k], va[1], va[3]);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) mma_f16(acc[c][d], va, pb[c][2 * k], pb[c][2 * k + 1]);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
     // ---- the segment's end: the warps' results become one
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 1);
-      l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], 2);
-    }
-    if (t == 0) {
-      stat[warp][g] = make_float2(m_run[0], l_run[0]);
-      stat[warp][g + 8] = make_float2(m_run[1], l_run[1]);
-    }
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        l_run[c][k] += __shfl_xor_sync(0xffffffffu, l_run[c][k], 4);
+        l_run[c][k] += __shfl_xor_sync(0xffffffffu, l_run[c][k], 8);
+        l_run[c][k] += __shfl_xor_sync(0xffffffffu, l_run[c][k], 16);
+        if (g == 0) stat[warp][8 * c + 2 * t + k] = make_float2(m_run[c][k], l_run[c][k]);
+      }
     consumers_sync();
-    float m_all[2], f[2], l_all[2] = {0.f, 0.f};
+    float m_all[NC][2], l_all[NC][2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      m_all[r] = -INFINITY;
+    for (int c = 0; c < NC; ++c) {
+      float f[2];
 #pragma unroll
-      for (int w = 0; w < kConsumers; ++w) m_all[r] = fmaxf(m_all[r], stat[w][g + 8 * r].x);
+      for (int k = 0; k < 2; ++k) {
+        const int row = 8 * c + 2 * t + k;
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int w = 0; w < kConsumers; ++w) {
-        const float2 ml = stat[w][g + 8 * r];
-        // a NaN sum has to survive: its maximum may be -inf
-        l_all[r] = fmaf(ml.y, ml.x == m_all[r] ? 1.f : exp2_mufu(ml.x - m_all[r]), l_all[r]);
+        for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, stat[w][row].x);
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+          const float2 ml = stat[w][row];
+          // a NaN sum has to survive: its maximum may be -inf
+          l = fmaf(ml.y, ml.x == m ? 1.f : exp2_mufu(ml.x - m), l);
+        }
+        m_all[c][k] = m;
+        l_all[c][k] = l;
+        f[k] = (m_run[c][k] == m ? 1.f : exp2_mufu(m_run[c][k] - m)) * v_top;
       }
-      f[r] = m_run[r] == m_all[r] ? 1.f : exp2_mufu(m_run[r] - m_all[r]);
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[c][d][e] *= f[e & 1];
     }
+    auto each = [&](auto&& what) {  // (value, its place in a [ROWS][PITCH] array)
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+      for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[d][e] *= f[e >> 1];
-    auto put = [&](float* to) {
+        for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        float* p = to + g * D + 8 * d + 2 * t;
-        *reinterpret_cast<float2*>(p) = make_float2(acc[d][0], acc[d][1]);
-        *reinterpret_cast<float2*>(p + 8 * D) = make_float2(acc[d][2], acc[d][3]);
-      }
+          for (int e = 0; e < 4; ++e)
+            what(acc[c][d][e], (8 * c + 2 * t + (e & 1)) * PITCH + 16 * d + g + 4 * (e & 2));
     };
-    auto add = [&](const float* from) {
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const float* p = from + g * D + 8 * d + 2 * t;
-        const float2 x = *reinterpret_cast<const float2*>(p);
-        const float2 y = *reinterpret_cast<const float2*>(p + 8 * D);
-        acc[d][0] += x.x, acc[d][1] += x.y, acc[d][2] += y.x, acc[d][3] += y.y;
-      }
-    };
-    if (warp >= 2) put(sums + (warp - 2) * kRows * D);
+    if (warp >= 2) {
+      float* to = sums + (warp - 2) * ROWS * PITCH;
+      each([&](float& x, int at) { to[at] = x; });
+    }
     consumers_sync();
-    if (warp < 2) add(sums + warp * kRows * D);
-    if (warp == 1) put(sums + kRows * D);  // where this warp has just read
+    if (warp < 2) {
+      float* from = sums + warp * ROWS * PITCH;
+      each([&](float& x, int at) { x += from[at]; });
+      if (warp == 1) each([&](float& x, int at) { from[at] = x; });  // where it has just read
+    }
     consumers_sync();
+    const bool whole = begins && ends;
+    const size_t slot = ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * ROWS;
     if (warp == 0) {
-      add(sums + kRows * D);
-      if (begins && ends) {
+      const float* from = sums + ROWS * PITCH;
+      each([&](float& x, int at) { x += from[at]; });
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (g + 8 * r >= rows) continue;
-          const float inv = l_all[r] == 0.f ? 0.f : 1.f / l_all[r];
-          uint16_t* o = a.o + seq * a.o_stride + (head0 + g + 8 * r) * D + 2 * t;
+      for (int c = 0; c < NC; ++c) {
+        float f[2];
 #pragma unroll
-          for (int d = 0; d < ND; ++d)
-            *reinterpret_cast<uint32_t*>(o + 8 * d) =
-                (uint32_t)float_to_act(acc[d][2 * r] * inv, a.f16) |
-                (uint32_t)float_to_act(acc[d][2 * r + 1] * inv, a.f16) << 16;
+        for (int k = 0; k < 2; ++k) {
+          f[k] = !whole ? 1.f : l_all[c][k] == 0.f ? 0.f : 1.f / l_all[c][k];
+          if (!whole && g == 0)
+            a.stat[slot + 8 * c + 2 * t + k] = make_float2(m_all[c][k], l_all[c][k]);
         }
-      } else {
-        const size_t at = ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kRows;
-        put(a.part + at * D);
-        if (t == 0) {
-          a.stat[at + g] = make_float2(m_all[0], l_all[0]);
-          a.stat[at + g + 8] = make_float2(m_all[1], l_all[1]);
-        }
-        if (begins) {
-          // the pair's last unit, the range it is in, and so the number of parts
-          const long long last = u0 + unit + pages - 1;
-          const int to = (int)(((last + 1) * ranges - 1) / units);
-          if (lane == 0)
-            a.cut[blockIdx.x] = make_int4(seq, hg, to - (int)blockIdx.x + 1, 0);
-          have_cut = true;
-        }
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[c][d][e] *= f[e & 1];
+      }
+      each([&](float& x, int at) { sums[at] = x; });
+      if (!whole && begins) {
+        // the pair's last unit, the range it is in, and so the number of parts
+        const long long last = u0 + unit + pages - 1;
+        const int to = (int)(((last + 1) * ranges - 1) / units);
+        if (lane == 0) a.cut[blockIdx.x] = make_int4(seq, hg, to - (int)blockIdx.x + 1, 0);
+        have_cut = true;
+      }
+    }
+    consumers_sync();
+    // rows as they lie in memory
+    if (whole) {
+      for (int i = threadIdx.x; i < rows * (D / 8); i += 32 * kConsumers) {
+        const int r = i / (D / 8), d = i % (D / 8) * 8;
+        const float* x = sums + r * PITCH + d;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[k] = a.f16 ? pack_f16x2(x[2 * k], x[2 * k + 1]) : pack_bf16x2(x[2 * k], x[2 * k + 1]);
+        *reinterpret_cast<uint4*>(a.o + seq * a.o_stride + (head0 + r) * D + d) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+      for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kConsumers) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        *reinterpret_cast<float4*>(a.part + (slot + r) * D + d) =
+            *reinterpret_cast<const float4*>(sums + r * PITCH + d);
       }
     }
     unit += n;
@@ -718,66 +803,81 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
     if (!ok) break;
     if (unit < n_units) next_pair();
   }
-  if (threadIdx.x == 0 && !have_cut && a.cut) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0 && !have_cut) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
 }
 
 // Joins the parts of the pairs that were cut: a thread block per (range, row of
-// its last pair), a thread per channel.
+// its last pair), kJoinParts threads per channel, each taking every kJoinParts-th
+// part, so that the sums are fetched side by side.
+constexpr int kJoinParts = 4;
+
 template <int D>
-__global__ void __launch_bounds__(D) k_cache_join(const AttnArgs a) {
+__global__ void __launch_bounds__(D * kJoinParts) k_cache_join(const AttnArgs a) {
+  __shared__ float sums[kJoinParts][D], weights[kJoinParts];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the ranges' kernel is complete
   const int4 cut = a.cut[blockIdx.x];
-  const int n = cut.z, r = blockIdx.y, d = threadIdx.x;
-  const int kvh = cut.y / a.row_groups, h0 = (cut.y - kvh * a.row_groups) * kRows;
+  const int n = cut.z, r = blockIdx.y, d = threadIdx.x % D, p = threadIdx.x / D;
+  const int kvh = cut.y / a.row_groups, h0 = (cut.y - kvh * a.row_groups) * a.pass;
   if (n == 0 || h0 + r >= a.group) return;
   // part 1 of its own range, part 0 of the following ones
-  auto at = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kRows + r; };
+  auto at = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * a.pass + r; };
   float m = -INFINITY;
   for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, a.stat[at(i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float sum = 0.f, l = 0.f;
 #pragma unroll 8
-  for (int i = 0; i < n; ++i) {
+  for (int i = p; i < n; i += kJoinParts) {
     const float2 ml = a.stat[at(i)];
     const float f = ml.x == m ? 1.f : exp2_mufu(ml.x - m);
     sum = fmaf(a.part[at(i) * D + d], f, sum);
     l = fmaf(ml.y, f, l);
   }
+  sums[p][d] = sum;
+  if (d == 0) weights[p] = l;
+  __syncthreads();
+  if (p > 0) return;
+#pragma unroll
+  for (int i = 1; i < kJoinParts; ++i) sum += sums[i][d], l += weights[i];
   a.o[cut.x * a.o_stride + (kvh * a.group + h0 + r) * D + d] =
       float_to_act(l == 0.f ? 0.f : sum / l, a.f16);
 }
 
+// Query heads of a group that share a pass over the cache: 8, or 16 where more.
+inline int pass_of(int group) { return group > 8 ? 8 * kMaxCols : 8; }
+
 // Thread blocks of an attention call: as many as run at once, at most one per
 // kMinUnits units of tables that are full.
-template <int D, int BT>
+template <int D, int BT, int NC>
 int ranges_of(int n_seq, int heads, int width) {
   const long long units = (long long)n_seq * heads * width;
-  const long long most = (long long)num_sms() * Ring<D, BT>::PER_SM;
+  const long long most = (long long)num_sms() * Ring<D, BT, NC>::PER_SM;
   const long long n = (units + kMinUnits - 1) / kMinUnits;
   return (int)(n < most ? n : most);
 }
 
-size_t part_bytes(int ranges, int D) { return (size_t)ranges * 2 * kRows * D * 4; }
-size_t stat_bytes(int ranges) { return (size_t)ranges * 2 * kRows * 8; }
+template <int D, int BT, int NC>
+size_t workspace_of(int n_seq, int heads, int width) {
+  return (size_t)ranges_of<D, BT, NC>(n_seq, heads, width) *
+         (2 * 8 * NC * (D * 4 + 8) + sizeof(int4));
+}
 
-template <int D, int BT>
+template <int D, int BT, int NC>
 cudaError_t run_attention(AttnArgs& a, void* ws, cudaStream_t st) {
-  constexpr int BYTES = Ring<D, BT>::BYTES;
-  cudaError_t e = cudaFuncSetAttribute(k_cache_attention<D, BT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+  using R = Ring<D, BT, NC>;
+  cudaError_t e = cudaFuncSetAttribute(k_cache_attention<D, BT, NC>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, R::BYTES);
   if (e != cudaSuccess) return e;
-  const int ranges = ranges_of<D, BT>(a.n_seq, a.kv_heads * a.row_groups, a.width);
-  uint8_t* p = static_cast<uint8_t*>(ws);
-  a.part = reinterpret_cast<float*>(p);
-  a.stat = reinterpret_cast<float2*>(p + part_bytes(ranges, D));
-  a.cut = reinterpret_cast<int4*>(p + part_bytes(ranges, D) + stat_bytes(ranges));
-  k_cache_attention<D, BT><<<(unsigned)ranges, kAttnThreads, BYTES, st>>>(a);
+  const int ranges = ranges_of<D, BT, NC>(a.n_seq, a.kv_heads * a.row_groups, a.width);
+  a.part = static_cast<float*>(ws);
+  a.stat = reinterpret_cast<float2*>(a.part + (size_t)ranges * 2 * R::ROWS * D);
+  a.cut = reinterpret_cast<int4*>(a.stat + (size_t)ranges * 2 * R::ROWS);
+  k_cache_attention<D, BT, NC><<<(unsigned)ranges, kAttnThreads, R::BYTES, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // launched while the ranges run, to wait for them on the GPU
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ranges, (unsigned)(a.group < kRows ? a.group : kRows));
-  cfg.blockDim = dim3(D);
+  cfg.gridDim = dim3((unsigned)ranges, (unsigned)(a.group < a.pass ? a.group : a.pass));
+  cfg.blockDim = dim3(D * kJoinParts);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -786,6 +886,18 @@ cudaError_t run_attention(AttnArgs& a, void* ws, cudaStream_t st) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k_cache_join<D>, a);
 }
+
+// F<head_dim, block_tokens, column tiles>(...) for a cache and a group.
+#define H3_BY_CACHE(F, c, pass, ...)                                                       \
+  ((c).head_dim == 128                                                                     \
+       ? (pass) == 8 ? H3_BY_BLOCK(F, 128, 1, c, __VA_ARGS__)                              \
+                     : H3_BY_BLOCK(F, 128, 2, c, __VA_ARGS__)                              \
+       : (pass) == 8 ? H3_BY_BLOCK(F, 64, 1, c, __VA_ARGS__)                               \
+                     : H3_BY_BLOCK(F, 64, 2, c, __VA_ARGS__))
+#define H3_BY_BLOCK(F, D, NC, c, ...)                                                      \
+  ((c).block_tokens == 32   ? F<D, 32, NC>(__VA_ARGS__)                                    \
+   : (c).block_tokens == 64 ? F<D, 64, NC>(__VA_ARGS__)                                    \
+                            : F<D, 128, NC>(__VA_ARGS__))
 
 template <h3_type T, int D>
 cudaError_t run_store(const StoreArgs& a, int n_seq, int block_tokens, cudaStream_t st) {
@@ -834,14 +946,9 @@ cudaError_t launch_kv_cache_store(const h3_kv_cache& c, int n_seq, int max_new,
 }
 
 size_t cache_attention_workspace(const h3_kv_cache& c, int n_seq, int q_heads, int width) {
-  const int heads = c.kv_heads * ((q_heads / c.kv_heads + kRows - 1) / kRows);
-#define H3_RANGES(D)                                                      \
-  (c.block_tokens == 32 ? ranges_of<D, 32>(n_seq, heads, width)           \
-   : c.block_tokens == 64 ? ranges_of<D, 64>(n_seq, heads, width)         \
-                          : ranges_of<D, 128>(n_seq, heads, width))
-  const int ranges = c.head_dim == 128 ? H3_RANGES(128) : H3_RANGES(64);
-#undef H3_RANGES
-  return part_bytes(ranges, c.head_dim) + stat_bytes(ranges) + (size_t)ranges * sizeof(int4);
+  const int group = q_heads / c.kv_heads, pass = pass_of(group);
+  const int heads = c.kv_heads * ((group + pass - 1) / pass);
+  return H3_BY_CACHE(workspace_of, c, pass, n_seq, heads, width);
 }
 
 cudaError_t launch_cache_attention(const h3_kv_cache& c, int n_seq, int q_heads,
@@ -864,17 +971,13 @@ cudaError_t launch_cache_attention(const h3_kv_cache& c, int n_seq, int q_heads,
   a.n_blocks = c.n_blocks;
   a.kv_heads = c.kv_heads;
   a.group = q_heads / c.kv_heads;
-  a.row_groups = (a.group + kRows - 1) / kRows;
+  a.pass = pass_of(a.group);
+  a.row_groups = (a.group + a.pass - 1) / a.pass;
   a.width = width;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.f16 = f16;
   a.err = err;
-#define H3_RUN(D)                                                        \
-  (c.block_tokens == 32 ? run_attention<D, 32>(a, ws, st)                \
-   : c.block_tokens == 64 ? run_attention<D, 64>(a, ws, st)              \
-                          : run_attention<D, 128>(a, ws, st))
-  return c.head_dim == 128 ? H3_RUN(128) : H3_RUN(64);
-#undef H3_RUN
+  return H3_BY_CACHE(run_attention, c, a.pass, a, ws, st);
 }
 
 }  // namespace h3

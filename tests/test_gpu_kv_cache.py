@@ -281,6 +281,22 @@ def test_attention_splits(n_seq, length):
     _check_attention(lengths, 4, 2, 128, 64, BF, seed=length)
 
 
+@pytest.mark.parametrize("D,BT,QH", [(64, 32, 8), (128, 32, 20), (64, 64, 32), (128, 64, 8),
+                                     (64, 128, 40), (128, 128, 12)])
+def test_attention_many_blocks_per_range(D, BT, QH):
+    """Every range runs through its ring and its list several times and through
+    several sequences; repeated, since what could go wrong is a matter of timing."""
+    KH = 4
+    lengths = [(3 + 7 * i % 11) * 40 * BT + 13 * i for i in range(12)]
+    cache, q, o = _check_attention(lengths, QH, KH, D, BT, BF, seed=D + BT)
+    ws = torch.empty(h3.h3_cache_attention_workspace_size(cache.c, 12, QH, cache.width),
+                     dtype=torch.uint8, device=DEV)
+    for _ in range(30):
+        again = cache.attend(q, 1 / math.sqrt(D), ws=ws)
+        assert torch.equal(again, o)
+    assert h3.h3_text_error() == h3.H3_OK
+
+
 def test_attention_of_large_queries():
     """Scores up to about 60: their float32 error grows with them."""
     _check_attention([500, 40], 4, 2, 64, 64, BF, boost=8.0)
