@@ -2,12 +2,15 @@
 //
 // The code is the nearest integer to the exact quotient x / scale, ties to even.
 // x times the correctly rounded reciprocal is within 2^-24 of the quotient
-// relative to it, so its rounding r is the code or, next to a tie, its neighbour.
-// The rest x - r scale decides: it is a multiple of half a unit of the scale's
-// last place and at most about half the scale, so one fused multiply-add gives it
-// exactly, and r moves by one if the rest is more than half the scale, or equal
-// to it and r odd. (Near-ties are not rare: with x and the maximum in bfloat16
-// the quotient is 127 times a ratio of two 8-bit numbers.)
+// relative to it, so its floor r is the quotient's or, next to an integer, that
+// integer's neighbour; either way the code is r or r + 1. The rest x - r scale
+// decides: r + 1 if it is more than half the scale, or equal to that and r odd.
+// One fused multiply-add gives the rest exactly wherever the decision is close: it
+// is a multiple of the scale's last place and at most about the scale (for x
+// below the scale it is x itself, or the scale less |x|, which is exact from half
+// the scale on; where it is rounded, r is -1 and half the scale counts as more).
+// (Near-ties are not rare: with x and the maximum in bfloat16 the quotient is 127
+// times a ratio of two 8-bit numbers.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -19,7 +22,7 @@
 
 namespace h3 {
 
-constexpr float kCodeMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+constexpr float kCodeMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves an integer
 constexpr float kMaxFinite = 3.4028235e38f;
 
 struct RowScale {
@@ -70,24 +73,21 @@ __device__ __forceinline__ uint2 codes_of(const float* x, const RowScale& s) {
   const uint64_t unmagic = f2_pack(-kCodeMagic, -kCodeMagic);
   const uint64_t minus_scale = f2_pack(-s.scale, -s.scale);
   const uint32_t half = __float_as_uint(0.5f * s.scale);
-  float r[2 * N];
+  uint32_t u[2 * N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const uint64_t v = f2_pack(x[2 * i], x[2 * i + 1]);
-    const uint64_t rr = f2_fma(v, inv, magic);
-    float rest[2];
+    const uint64_t rr = f2_fma_down(v, inv, magic);
+    float rest[2], r[2];
     f2_unpack(f2_fma(f2_add(rr, unmagic), minus_scale, v), rest[0], rest[1]);
-    f2_unpack(rr, r[2 * i], r[2 * i + 1]);
+    f2_unpack(rr, r[0], r[1]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
+      const uint32_t w = __float_as_uint(r[k]);
       // above half the scale, or from half the scale on where r is odd
-      const float limit = __uint_as_float(half - (__float_as_uint(r[2 * i + k]) & 1u));
-      if (fabsf(rest[k]) > limit) r[2 * i + k] += copysignf(1.f, rest[k]);
+      u[2 * i + k] = w + (rest[k] > __uint_as_float(half - (w & 1u)) ? 1u : 0u);
     }
   }
-  uint32_t u[2 * N];
-#pragma unroll
-  for (int i = 0; i < 2 * N; ++i) u[i] = __float_as_uint(r[i]);
   uint2 c = make_uint2(pack4(u[0], u[1], u[2], u[3]), 0);
   if constexpr (!FOUR) c.y = pack4(u[4], u[5], u[6], u[7]);
   return c;

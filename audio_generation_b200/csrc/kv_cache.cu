@@ -43,6 +43,46 @@ struct StoreArgs {
   int* err;
 };
 
+// Scale of a block and kv head, and what happens to its codes.
+struct BlockScale {
+  RowScale s;
+  float old;
+  bool zero;   // every code is 0
+  bool again;  // earlier codes change
+};
+
+__device__ __forceinline__ BlockScale block_scale(float peak, float old, bool held,
+                                                  float* stored, bool writer) {
+  BlockScale b;
+  float scale = max_nan(peak / 127.f, old);
+  // an infinity or a NaN marks the whole block: scale NaN, codes 0
+  const bool bad = !(peak <= kMaxFinite) || !(old <= kMaxFinite);
+  if (bad) scale = __int_as_float(0x7fc00000);
+  if (writer) *stored = scale;
+  b.old = old;
+  b.zero = bad || scale == 0.f;
+  b.s = row_scale(b.zero ? 1.f : scale);
+  b.again = held && (bad || scale > old);
+  return b;
+}
+
+__device__ __forceinline__ uint32_t word_again(uint32_t x, const BlockScale& b) {
+  if (b.zero) return 0;
+  const float ratio = b.old * b.s.inv;
+  uint32_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    c[k] = code_again((int)(int8_t)(x >> (8 * k)), b.old, b.s.scale, ratio);
+  return pack4(c[0], c[1], c[2], c[3]);
+}
+
+template <h3_type T>
+__device__ __forceinline__ uint2 vec_codes(const uint4& u, const BlockScale& b) {
+  float f[8];
+  unpack<T>(u, f);
+  return codes_of(f, b.s);
+}
+
 template <h3_type T, int D, int BT>
 __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
   constexpr int RV = D / 8;                 // 16-byte vectors per token
@@ -71,23 +111,27 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
   if (lo >= hi) return;
   const int held = nth == 0 ? before % BT : 0;  // earlier tokens of the block
   const int slot0 = lo - page * BT, to = hi - page * BT;
+  const bool whole = slot0 == 0 && to == BT;
 
+  // the thread's groups: four slots from 4 word on, eight channels from 8 vec on
+  const int vec = t % RV, word0 = t / RV;
+  constexpr int WORDS = kStoreThreads / RV;  // word step between a thread's groups
   uint4 u[2][NG][4];
+  const long long row0 = (long long)first + page * BT - before;  // row of slot 0
 #pragma unroll
-  for (int w = 0; w < 2; ++w)
+  for (int w = 0; w < 2; ++w) {
+    const uint16_t* x = a.x[w] + (row0 + 4 * word0) * a.stride[w] + head * D + vec * 8;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int idx = t + i * kStoreThreads;
+    for (int i = 0; i < NG; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int slot = 4 * (idx / RV) + j;
+        const int slot = 4 * (word0 + i * WORDS) + j;
         u[w][i][j] = make_uint4(0, 0, 0, 0);
-        if (idx < GROUPS && slot >= slot0 && slot < to)
-          u[w][i][j] = __ldcs(reinterpret_cast<const uint4*>(
-              a.x[w] + (first + (page * BT + slot - before)) * a.stride[w] + head * D +
-              (idx % RV) * 8));
+        if (slot >= slot0 && slot < to)
+          u[w][i][j] = __ldcs(
+              reinterpret_cast<const uint4*>(x + (4 * i * WORDS + j) * a.stride[w]));
       }
-    }
+  }
   const int block = block_of(a.table, a.width, seq, page, a.n_blocks, a.err);
   if (block < 0) return;
   const size_t at = (size_t)block * a.kv_heads + head;
@@ -107,90 +151,84 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
     if ((t & 31) == 0) part[w][t >> 5] = m;
   }
   __syncthreads();  // also: every thread has read the old scales
+  BlockScale bs[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     float m = 0.f;
 #pragma unroll
     for (int k = 0; k < kStoreThreads / 32; ++k) m = max_nan(m, part[w][k]);
-    float scale = max_nan(m / 127.f, old[w]);
-    // an infinity or a NaN marks the whole block: scale NaN, codes 0
-    const bool bad = !(m <= kMaxFinite) || !(old[w] <= kMaxFinite);
-    if (bad) scale = __int_as_float(0x7fc00000);
-    if (t == 0) a.scales[w][at] = scale;
-    const bool zero = bad || scale == 0.f;
-    const RowScale s = row_scale(zero ? 1.f : scale);
-    const bool again = held > 0 && (bad || scale > old[w]);  // earlier codes change
-    const float ratio = old[w] * s.inv;
-    uint8_t* codes = a.codes[w] + at * (BT * D);
-    auto word_again = [&](uint32_t x) {
-      if (zero) return 0u;
-      uint32_t c[4];
+    bs[w] = block_scale(m, old[w], held > 0, a.scales[w] + at, t == 0);
+  }
+  uint8_t* kc = a.codes[0] + at * (BT * D);
+  uint8_t* vc = a.codes[1] + at * (BT * D);
+
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        c[k] = code_again((int)(int8_t)(x >> (8 * k)), old[w], scale, ratio);
-      return pack4(c[0], c[1], c[2], c[3]);
-    };
+  for (int i = 0; i < NG; ++i) {
+    const int word = word0 + i * WORDS;
+    if (word >= WR || 4 * word + 4 <= slot0 || 4 * word >= to) continue;
+    uint8_t* k = kc + 4 * word * D + vec * 8;
 #pragma unroll
-    for (int i = 0; i < NG; ++i) {
-      const int idx = t + i * kStoreThreads, word = idx / RV, vec = idx % RV;
-      if (idx >= GROUPS || 4 * word + 4 <= slot0 || 4 * word >= to) continue;
-      uint2 c[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float f[8];
-        unpack<T>(u[w][i][j], f);
-        c[j] = zero ? make_uint2(0, 0) : codes_of(f, s);
-      }
-      if (w == 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int slot = 4 * word + j;
-          if (slot >= slot0 && slot < to)
-            *reinterpret_cast<uint2*>(codes + slot * D + vec * 8) = c[j];
-        }
-      } else {
-        uint32_t* dst = turned + vec * 8 * WR + (word ^ (vec & (WR - 1)));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t c0 = h ? c[0].y : c[0].x, c1 = h ? c[1].y : c[1].x;
-          const uint32_t c2 = h ? c[2].y : c[2].x, c3 = h ? c[3].y : c[3].x;
-          const uint32_t p = __byte_perm(c0, c1, 0x5140), q = __byte_perm(c2, c3, 0x5140);
-          const uint32_t r = __byte_perm(c0, c1, 0x7362), x = __byte_perm(c2, c3, 0x7362);
-          dst[(4 * h) * WR] = __byte_perm(p, q, 0x5410);
-          dst[(4 * h + 1) * WR] = __byte_perm(p, q, 0x7632);
-          dst[(4 * h + 2) * WR] = __byte_perm(r, x, 0x5410);
-          dst[(4 * h + 3) * WR] = __byte_perm(r, x, 0x7632);
-        }
-      }
+    for (int j = 0; j < 4; ++j) {
+      uint2 c = vec_codes<T>(u[0][i][j], bs[0]);
+      if (bs[0].zero) c = make_uint2(0, 0);
+      const int slot = 4 * word + j;
+      if (whole || (slot >= slot0 && slot < to)) *reinterpret_cast<uint2*>(k + j * D) = c;
     }
-    if (w == 0) {
-      if (again)
-        for (int i = t; i < held * D / 4; i += kStoreThreads) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
-          *p = word_again(*p);
-        }
+    uint2 c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = vec_codes<T>(u[1][i][j], bs[1]);
+    uint32_t* dst = turned + vec * 8 * WR + (word ^ (vec & (WR - 1)));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t c0 = h ? c[0].y : c[0].x, c1 = h ? c[1].y : c[1].x;
+      const uint32_t c2 = h ? c[2].y : c[2].x, c3 = h ? c[3].y : c[3].x;
+      const uint32_t p = __byte_perm(c0, c1, 0x5140), q = __byte_perm(c2, c3, 0x5140);
+      const uint32_t r = __byte_perm(c0, c1, 0x7362), x = __byte_perm(c2, c3, 0x7362);
+      dst[(4 * h) * WR] = __byte_perm(p, q, 0x5410);
+      dst[(4 * h + 1) * WR] = __byte_perm(p, q, 0x7632);
+      dst[(4 * h + 2) * WR] = __byte_perm(r, x, 0x5410);
+      dst[(4 * h + 3) * WR] = __byte_perm(r, x, 0x7632);
+    }
+  }
+  if (bs[0].again)
+    for (int i = t; i < held * D / 4; i += kStoreThreads) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(kc) + i;
+      *p = word_again(*p, bs[0]);
+    }
+  __syncthreads();
+  const bool zero = bs[1].zero;
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < D * WR / 4; i += kStoreThreads) {
+      const int d = (i + t) / (WR / 4), q = (i + t) % (WR / 4) * 4;
+      if (D * WR / 4 % kStoreThreads != 0 && i + t >= D * WR / 4) break;
+      const uint32_t* row = turned + d * WR;
+      const int f = (d / 8) & (WR - 1);
+      uint4 c = make_uint4(row[q ^ f], row[(q + 1) ^ f], row[(q + 2) ^ f], row[(q + 3) ^ f]);
+      if (zero) c = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(vc + d * BT + 4 * q) = c;
+    }
+    return;
+  }
+  const bool again = bs[1].again;
+  const int w0 = (again ? 0 : slot0) / 4, words = (to + 3) / 4 - w0;
+  for (int i = t; i < D * words; i += kStoreThreads) {
+    const int d = i % D, word = w0 + i / D;
+    uint32_t c = turned[d * WR + (word ^ ((d / 8) & (WR - 1)))];
+    if (zero) c = 0;
+    uint8_t* p = vc + d * BT + 4 * word;
+    if (4 * word >= slot0 && 4 * word + 4 <= to) {
+      *reinterpret_cast<uint32_t*>(p) = c;
       continue;
     }
-    __syncthreads();
-    const int from = again ? 0 : slot0;
+    // the word also holds earlier or later tokens
+    const uint32_t early =
+        again && 4 * word < slot0 ? word_again(*reinterpret_cast<uint32_t*>(p), bs[1]) : 0;
 #pragma unroll
-    for (int i = t; i < D * WR; i += kStoreThreads) {
-      const int d = i / WR, word = i % WR;
-      if (4 * word + 4 <= from || 4 * word >= to) continue;
-      uint32_t* p = reinterpret_cast<uint32_t*>(codes + d * BT) + word;
-      uint32_t c = turned[d * WR + (word ^ ((d / 8) & (WR - 1)))];
-      if (4 * word < slot0 || 4 * word + 4 > to) {  // also earlier or later tokens' codes
-        const uint32_t was = *p;
-        const uint32_t early = again ? word_again(was) : was;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int slot = 4 * word + k;
-          const uint32_t mask = 0xffu << (8 * k);
-          if (slot < slot0) c = (c & ~mask) | (early & mask);
-          if (slot >= to) c = (c & ~mask) | (was & mask);
-        }
-      }
-      *p = c;
+    for (int k = 0; k < 4; ++k) {
+      const int slot = 4 * word + k;
+      if (slot >= slot0 && slot < to) p[k] = (uint8_t)(c >> (8 * k));
+      else if (again && slot < slot0) p[k] = (uint8_t)(early >> (8 * k));
     }
   }
 }
@@ -325,11 +363,6 @@ __device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t&
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint16_t float_to_act(float v, bool f16) {
-  return f16 ? __half_as_ushort(__float2half_rn(v))
-             : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
 // The tokens of a sequence, limited to what its table can name.
@@ -807,16 +840,17 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
 }
 
 // Joins the parts of the pairs that were cut: a thread block per (range, row of
-// its last pair), kJoinParts threads per channel, each taking every kJoinParts-th
-// part, so that the sums are fetched side by side.
-constexpr int kJoinParts = 4;
+// its last pair), kJoinParts threads per four channels, each taking every
+// kJoinParts-th part, so that the sums are fetched side by side.
+constexpr int kJoinParts = 8;
 
 template <int D>
-__global__ void __launch_bounds__(D * kJoinParts) k_cache_join(const AttnArgs a) {
-  __shared__ float sums[kJoinParts][D], weights[kJoinParts];
+__global__ void __launch_bounds__(D / 4 * kJoinParts) k_cache_join(const AttnArgs a) {
+  __shared__ float4 sums[kJoinParts][D / 4];
+  __shared__ float weights[kJoinParts];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the ranges' kernel is complete
   const int4 cut = a.cut[blockIdx.x];
-  const int n = cut.z, r = blockIdx.y, d = threadIdx.x % D, p = threadIdx.x / D;
+  const int n = cut.z, r = blockIdx.y, d = threadIdx.x % (D / 4), p = threadIdx.x / (D / 4);
   const int kvh = cut.y / a.row_groups, h0 = (cut.y - kvh * a.row_groups) * a.pass;
   if (n == 0 || h0 + r >= a.group) return;
   // part 1 of its own range, part 0 of the following ones
@@ -825,12 +859,17 @@ __global__ void __launch_bounds__(D * kJoinParts) k_cache_join(const AttnArgs a)
   for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, a.stat[at(i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float sum = 0.f, l = 0.f;
-#pragma unroll 8
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
   for (int i = p; i < n; i += kJoinParts) {
     const float2 ml = a.stat[at(i)];
+    const float4 x = *reinterpret_cast<const float4*>(a.part + at(i) * D + 4 * d);
     const float f = ml.x == m ? 1.f : exp2_mufu(ml.x - m);
-    sum = fmaf(a.part[at(i) * D + d], f, sum);
+    sum.x = fmaf(x.x, f, sum.x);
+    sum.y = fmaf(x.y, f, sum.y);
+    sum.z = fmaf(x.z, f, sum.z);
+    sum.w = fmaf(x.w, f, sum.w);
     l = fmaf(ml.y, f, l);
   }
   sums[p][d] = sum;
@@ -838,9 +877,18 @@ __global__ void __launch_bounds__(D * kJoinParts) k_cache_join(const AttnArgs a)
   __syncthreads();
   if (p > 0) return;
 #pragma unroll
-  for (int i = 1; i < kJoinParts; ++i) sum += sums[i][d], l += weights[i];
-  a.o[cut.x * a.o_stride + (kvh * a.group + h0 + r) * D + d] =
-      float_to_act(l == 0.f ? 0.f : sum / l, a.f16);
+  for (int i = 1; i < kJoinParts; ++i) {
+    const float4 x = sums[i][d];
+    sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+    l += weights[i];
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint2 o;
+  if (a.f16)
+    o = make_uint2(pack_f16x2(sum.x * inv, sum.y * inv), pack_f16x2(sum.z * inv, sum.w * inv));
+  else
+    o = make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
+  *reinterpret_cast<uint2*>(a.o + cut.x * a.o_stride + (kvh * a.group + h0 + r) * D + 4 * d) = o;
 }
 
 // Query heads of a group that share a pass over the cache: 8, or 16 where more.
@@ -877,7 +925,7 @@ cudaError_t run_attention(AttnArgs& a, void* ws, cudaStream_t st) {
   // launched while the ranges run, to wait for them on the GPU
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ranges, (unsigned)(a.group < a.pass ? a.group : a.pass));
-  cfg.blockDim = dim3(D * kJoinParts);
+  cfg.blockDim = dim3(D / 4 * kJoinParts);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
