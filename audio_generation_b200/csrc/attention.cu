@@ -82,20 +82,7 @@ constexpr float kExpC3 = 0.05508868396f, kExpC2 = 0.24260404706f, kExpC1 = 0.693
 constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23
 
 __device__ __forceinline__ void exp2_poly2(uint64_t x2, float& p0, float& p1) {
-  float x0, x1;
-  f2_unpack(x2, x0, x1);
-  const uint64_t xc = f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-  const uint64_t t = f2_add(xc, f2_pack(kRoundMagic, kRoundMagic));
-  const uint64_t jf = f2_add(t, f2_pack(-kRoundMagic, -kRoundMagic));     // j, exact
-  const uint64_t f = f2_fma(jf, f2_pack(-1.f, -1.f), xc);                  // x - j, exact
-  uint64_t p = f2_fma(f2_pack(kExpC3, kExpC3), f, f2_pack(kExpC2, kExpC2));
-  p = f2_fma(p, f, f2_pack(kExpC1, kExpC1));
-  p = f2_fma(p, f, f2_pack(kExpC0, kExpC0));
-  float q0, q1, t0, t1;
-  f2_unpack(p, q0, q1);
-  f2_unpack(t, t0, t1);
-  p0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
-  p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+  exp2_cubic2(x2, Cubic{kExpC3, kExpC2, kExpC1, kExpC0, kRoundMagic}, p0, p1);
 }
 
 // Which key pairs of a 64-key half take the FMA-pipe exp2 (bit e of the mask

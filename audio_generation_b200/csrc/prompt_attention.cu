@@ -19,7 +19,12 @@
 // Where G does not divide 128 the last rows of a tile are idle.
 //
 // Work items (two tiles each) come from the prompts object, longest key range
-// first, so that the long ones do not end the launch alone.
+// first. One CTA per SM takes them in turn (there and back over the list's
+// rounds, so that no CTA always gets the longer one), every role running on into
+// the next item: its first keys and its q are fetched and its first scores
+// computed while the item before is still being divided and stored. q has one
+// buffer, given back after the item's last score product; an O accumulator is
+// given back when its rows have been read.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -44,9 +49,16 @@ constexpr int TMEM_COLS = 512;
 constexpr float kLazyRescale = 8.0f;  // log2 units
 
 struct Bars {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2],
-      p_full[2], o_final[2], drain;
+  uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2],
+      p_full[2], o_final[2], o_free[2], drain;
 };
+
+// 2^f on the FMA pipe, f in [-1/2, 1/2]: the packed-sequence attention kernel's
+// cubic (relative error at most 7.7e-5), and which of 32 key pairs take it.
+constexpr float kExpC3 = 0.05508868396f, kExpC2 = 0.24260404706f, kExpC1 = 0.69327622652f,
+                kExpC0 = 0.99992895126f;
+constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23
+constexpr uint32_t kCubicPairs = 0x20820820u;  // every sixth
 
 // smem: Q0 Q1 | K0 K1 | V0 V1 | barriers
 template <int D>
@@ -54,11 +66,16 @@ constexpr int tile_bytes() { return D / 64 * HALF; }
 template <int D>
 constexpr int smem_bytes() { return 6 * tile_bytes<D>() + 256 + 1024; }
 
+struct Item {
+  int kvh, start, pos0, len, n0, n1;
+};
+
 struct Args {
   const uint16_t *q, *k, *v;
   uint16_t* o;
   int64_t q_stride, k_stride, v_stride, o_stride;
   const int4* items;  // {first row of the prompt, first position, length, 0}
+  int n_work;         // items * kv_heads
   int kv_heads, group, tile_pos;  // tile_pos = 128 / group positions per tile
   float scale_log2;
   int* err;
@@ -142,16 +159,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int item = blockIdx.x / a.kv_heads, kvh = blockIdx.x - item * a.kv_heads;
-  const int4 it = a.items[item];
-  const int start = it.x, pos0 = it.y, len = it.z, P = a.tile_pos;
-  // key tiles each query tile visits: up to its last existing position
-  const int n0 = (min(pos0 + P, len) - 1) / 128 + 1;
-  const int n1 = pos0 + P < len ? (min(pos0 + 2 * P, len) - 1) / 128 + 1 : 0;
-  const int n = max(n0, n1);
+  const int P = a.tile_pos;
+  // the w-th piece of work of this CTA; false past the last
+  auto piece = [&](int w, Item& x) {
+    const int i = (w & 1) ? (w + 1) * (int)gridDim.x - 1 - (int)blockIdx.x
+                          : w * (int)gridDim.x + (int)blockIdx.x;
+    if (i >= a.n_work) return false;
+    const int item = i / a.kv_heads;
+    const int4 it = __ldg(a.items + item);
+    x.kvh = i - item * a.kv_heads;
+    x.start = it.x;
+    x.pos0 = it.y;
+    x.len = it.z;
+    // key tiles each query tile visits: up to its last existing position
+    x.n0 = (min(x.pos0 + P, x.len) - 1) / 128 + 1;
+    x.n1 = x.pos0 + P < x.len ? (min(x.pos0 + 2 * P, x.len) - 1) / 128 + 1 : 0;
+    return true;
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->k_full[i], 1);
       mbar_init(&bars->k_empty[i], 1);
@@ -161,6 +189,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(&bars->p_half[i], 4);  // one arrival per softmax warp
       mbar_init(&bars->p_full[i], 4);
       mbar_init(&bars->o_final[i], 1);
+      mbar_init(&bars->o_free[i], 4);
     }
     mbar_init(&bars->drain, 1);
     *abort_flag = 0;
@@ -181,32 +210,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (warp == 8) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
-        const int tiles = n1 > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(&bars->q_full, tiles * (D / 64) * P * a.group * 128);
-        for (int i = 0; i < tiles; ++i)
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(smem + OFF_Q + i * TILE + h * HALF, &tq, &bars->q_full, 64 * h,
-                        kvh * a.group, start + pos0 + i * P);
-        int nk = 0, nv = 0;
+        int nk = 0, nv = 0, nq = 0;  // fills so far
         bool ok = true;
-        for (int j = 0; j < n && ok; ++j) {
-          const int st = j & 1;
-          const uint32_t ph = ((j >> 1) & 1) ^ 1;
-          if (!mbar_wait(&bars->k_empty[st], ph, wc)) { ok = false; break; }
-          mbar_arrive_expect_tx(&bars->k_full[st], TILE);
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(smem + OFF_K + st * TILE + h * HALF, &tk, &bars->k_full[st], 64 * h, kvh,
-                        start + j * 128);
-          ++nk;
-          if (!mbar_wait(&bars->v_empty[st], ph, wc)) { ok = false; break; }
-          mbar_arrive_expect_tx(&bars->v_full[st], TILE);
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(smem + OFF_V + st * TILE + h * HALF, &tv, &bars->v_full[st], 64 * h, kvh,
-                        start + j * 128);
-          ++nv;
+        Item x;
+        for (int w = 0; ok && piece(w, x); ++w) {
+          const int n = max(x.n0, x.n1);
+          for (int j = 0; j < n; ++j) {
+            int st = nk & 1;
+            if (!mbar_wait(&bars->k_empty[st], ((nk >> 1) & 1) ^ 1, wc)) { ok = false; break; }
+            mbar_arrive_expect_tx(&bars->k_full[st], TILE);
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(smem + OFF_K + st * TILE + h * HALF, &tk, &bars->k_full[st], 64 * h,
+                          x.kvh, x.start + j * 128);
+            ++nk;
+            if (j == 0) {
+              const int tiles = x.n1 > 0 ? 2 : 1;
+              if (!mbar_wait(&bars->q_empty, (nq & 1) ^ 1, wc)) { ok = false; break; }
+              mbar_arrive_expect_tx(&bars->q_full, tiles * (D / 64) * P * a.group * 128);
+              for (int i = 0; i < tiles; ++i)
+                for (int h = 0; h < D / 64; ++h)
+                  tma_load_3d(smem + OFF_Q + i * TILE + h * HALF, &tq, &bars->q_full, 64 * h,
+                              x.kvh * a.group, x.start + x.pos0 + i * P);
+              ++nq;
+            }
+            st = nv & 1;
+            if (!mbar_wait(&bars->v_empty[st], ((nv >> 1) & 1) ^ 1, wc)) { ok = false; break; }
+            mbar_arrive_expect_tx(&bars->v_full[st], TILE);
+            for (int h = 0; h < D / 64; ++h)
+              tma_load_3d(smem + OFF_V + st * TILE + h * HALF, &tv, &bars->v_full[st], 64 * h,
+                          x.kvh, x.start + j * 128);
+            ++nv;
+          }
         }
         if (!ok) {  // let issued copies land before the CTA retires
-          mbar_drain(&bars->q_full, 0);
+          if (nq > 0) mbar_drain(&bars->q_full, (nq - 1) & 1);
           for (int j = nk > 2 ? nk - 2 : 0; j < nk; ++j) mbar_drain(&bars->k_full[j & 1], (j >> 1) & 1);
           for (int j = nv > 2 ? nv - 2 : 0; j < nv; ++j) mbar_drain(&bars->v_full[j & 1], (j >> 1) & 1);
         }
@@ -222,55 +259,72 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto wait_all = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
       };
-      bool ok = wait_all(&bars->q_full, 0);
-      tc_fence_after();
-      // Tile 0 uses key tile j first where it visits it, tile 1 last; tile 1's
-      // range is at least tile 0's unless tile 1 is empty.
-      auto issue_s = [&](int i, int j) -> bool {
-        const int st = j & 1;
-        if (i == 0 || j >= n0) {
-          if (!wait_all(&bars->k_full[st], (j >> 1) & 1)) return false;
+      bool ok = true;
+      int kv = 0;                       // key tiles of the items before
+      int done[2] = {0, 0};             // score tiles of each query tile so far
+      int rounds[2] = {0, 0};           // items in which the query tile had work
+      Item x;
+      for (int w = 0; ok && piece(w, x); ++w) {
+        const int n0 = x.n0, n1 = x.n1, n = max(n0, n1);
+        if (!wait_all(&bars->q_full, w & 1)) { ok = false; break; }
+        tc_fence_after();
+        int left = n0 + n1;  // score products to issue
+        // Tile 0 uses key tile j first where it visits it, tile 1 last; tile 1's
+        // range is at least tile 0's unless tile 1 is empty.
+        auto issue_s = [&](int i, int j) -> bool {
+          const int c = kv + j, st = c & 1;
+          if (i == 0 || j >= n0) {
+            if (!wait_all(&bars->k_full[st], (c >> 1) & 1)) return false;
+            tc_fence_after();
+          }
+          const uint32_t kl = k_lo + st * (TILE >> 4);
+          const uint32_t ql = q_lo + i * (TILE >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+            umma_ss_w_elect(tmem + i * 128, ql + off, hi, kl + off, hi, idesc_s,
+                            kk > 0 ? 1u : 0u);
+          }
+          umma_commit_elect(&bars->s_full[i]);
+          if (i == 1 || j >= n1) umma_commit_elect(&bars->k_empty[st]);
+          if (--left == 0) umma_commit_elect(&bars->q_empty);
+          return true;
+        };
+        // O_i += P_i(j) V_j in two halves of the keys, each as soon as it is stored
+        auto issue_pv = [&](int i, int j) -> bool {
+          const int c = kv + j, st = c & 1, ph = (done[i] + j) & 1;
+          if (j == 0 && !wait_all(&bars->o_free[i], (rounds[i] & 1) ^ 1)) return false;
+          if (!wait_all(&bars->p_half[i], ph)) return false;
+          if ((i == 0 || j >= n0) && !wait_all(&bars->v_full[st], (c >> 1) & 1)) return false;
           tc_fence_after();
+          const uint32_t vl = v_lo + st * (TILE >> 4);
+          const uint32_t o = tmem + 256 + i * 128, p = tmem + i * 128;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts_w_elect(o, p + kk * 8, vl + kk * (2048 >> 4), hi, idesc_pv,
+                            (j > 0 || kk > 0) ? 1u : 0u);
+          if (!wait_all(&bars->p_full[i], ph)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk)
+            umma_ts_w_elect(o, p + kk * 8, vl + kk * (2048 >> 4), hi, idesc_pv, 1u);
+          if (i == 1 || j >= n1) umma_commit_elect(&bars->v_empty[st]);
+          if (j == (i == 0 ? n0 : n1) - 1) umma_commit_elect(&bars->o_final[i]);
+          return true;
+        };
+        ok = issue_s(0, 0);
+        if (ok && n1 > 0) ok = issue_s(1, 0);
+        for (int j = 0; j < n && ok; ++j) {
+          if (j < n0) ok = issue_pv(0, j);
+          if (ok && j + 1 < n0) ok = issue_s(0, j + 1);
+          if (ok && j < n1) ok = issue_pv(1, j);
+          if (ok && j + 1 < n1) ok = issue_s(1, j + 1);
         }
-        const uint32_t kl = k_lo + st * (TILE >> 4);
-        const uint32_t ql = q_lo + i * (TILE >> 4);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-          umma_ss_w_elect(tmem + i * 128, ql + off, hi, kl + off, hi, idesc_s, kk > 0 ? 1u : 0u);
-        }
-        umma_commit_elect(&bars->s_full[i]);
-        if (i == 1 || j >= n1) umma_commit_elect(&bars->k_empty[st]);
-        return true;
-      };
-      // O_i += P_i(j) V_j in two halves of the keys, each as soon as it is stored
-      auto issue_pv = [&](int i, int j) -> bool {
-        const int st = j & 1;
-        if (!wait_all(&bars->p_half[i], j & 1)) return false;
-        if ((i == 0 || j >= n0) && !wait_all(&bars->v_full[st], (j >> 1) & 1)) return false;
-        tc_fence_after();
-        const uint32_t vl = v_lo + st * (TILE >> 4);
-        const uint32_t o = tmem + 256 + i * 128, p = tmem + i * 128;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_ts_w_elect(o, p + kk * 8, vl + kk * (2048 >> 4), hi, idesc_pv,
-                          (j > 0 || kk > 0) ? 1u : 0u);
-        if (!wait_all(&bars->p_full[i], j & 1)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 4; kk < 8; ++kk)
-          umma_ts_w_elect(o, p + kk * 8, vl + kk * (2048 >> 4), hi, idesc_pv, 1u);
-        if (i == 1 || j >= n1) umma_commit_elect(&bars->v_empty[st]);
-        if (j == (i == 0 ? n0 : n1) - 1) umma_commit_elect(&bars->o_final[i]);
-        return true;
-      };
-      if (ok) ok = issue_s(0, 0);
-      if (ok && n1 > 0) ok = issue_s(1, 0);
-      for (int j = 0; j < n && ok; ++j) {
-        if (j < n0) ok = issue_pv(0, j);
-        if (ok && j + 1 < n0) ok = issue_s(0, j + 1);
-        if (ok && j < n1) ok = issue_pv(1, j);
-        if (ok && j + 1 < n1) ok = issue_s(1, j + 1);
+        kv += n;
+        done[0] += n0;
+        done[1] += n1;
+        ++rounds[0];
+        rounds[1] += n1 > 0;
       }
       umma_commit_elect(&bars->drain);  // every MMA issued is complete past this point
       mbar_drain(&bars->drain, 0);
@@ -282,16 +336,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row in the tile = TMEM lane
     const int rp = r / a.group;         // its position in the tile, its head in the group
-    const int tile0 = pos0 + i * P, pos = tile0 + rp;
-    const int my_n = i == 0 ? n0 : n1;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t s_col = lane_base + i * 128;
     const uint32_t o_col = lane_base + 256 + i * 128;
-    float m_run = -INFINITY, l_run = 0.f;
     const uint64_t scale2 = f2_pack(a.scale_log2, a.scale_log2);
     bool ok = true;
+    int done = 0, rounds = 0;  // score tiles, and items with work, so far
+    Item x;
+    for (int w = 0; ok && piece(w, x); ++w) {
+    const int my_n = i == 0 ? x.n0 : x.n1;
+    if (my_n == 0) continue;
+    const int tile0 = x.pos0 + i * P, pos = tile0 + rp;
+    float m_run = -INFINITY, l_run = 0.f;
     for (int j = 0; j < my_n; ++j) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[i], j & 1, wc))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[i], (done + j) & 1, wc))) {
         ok = false;
         break;
       }
@@ -354,9 +412,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int e = 0; e < 32; ++e) {
           const int key = 64 * h + 2 * e;
           const uint64_t x2 = f2_fma(f2_pack(sc[key], sc[key + 1]), scale2, negm2);
-          float x0, x1;
-          f2_unpack(x2, x0, x1);
-          const float p0 = exp2_mufu(x0), p1 = exp2_mufu(x1);
+          float p0, p1;
+          if ((kCubicPairs >> e) & 1u) {
+            exp2_cubic2(x2, Cubic{kExpC3, kExpC2, kExpC1, kExpC0, kRoundMagic}, p0, p1);
+          } else {
+            f2_unpack(x2, p0, p1);
+            p0 = exp2_mufu(p0);
+            p1 = exp2_mufu(p1);
+          }
           sum2[e & 3] = f2_add(sum2[e & 3], f2_pack(p0, p1));
           pk[e] = pack2<F16>(p0, p1);
         }
@@ -371,44 +434,49 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       f2_unpack(f2_add(sum2[2], sum2[3]), b0, b1);
       l_run += (a0 + a1) + (b0 + b1);
     }
-    if (ok && my_n > 0)
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_final[i], 0, wc));
-    if (ok && my_n > 0) {
-      tc_fence_after();
-      const int head = kvh * a.group + r - rp * a.group;
-      const bool row_ok = rp < P && pos < len;
-      const float inv_l = 1.f / l_run;
-      uint16_t* dst = a.o + (row_ok ? (start + pos) * a.o_stride + head * D : 0);
-      float worst = 0.f;  // NaN or infinite if any value of the row is
-      uint32_t rr[32];
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_final[i], rounds & 1, wc));
+    if (!ok) break;
+    done += my_n;
+    ++rounds;
+    tc_fence_after();
+    const int head = x.kvh * a.group + r - rp * a.group;
+    const bool row_ok = rp < P && pos < x.len;
+    const float inv_l = 1.f / l_run;
+    uint16_t* dst = a.o + (row_ok ? (x.start + pos) * a.o_stride + head * D : 0);
+    float worst = 0.f;  // NaN or infinite if any value of the row is
+    uint32_t rr[32];
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        tmem_ld32(o_col + 32 * c, rr);
-        tmem_wait_ld();
-        float v[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          v[e] = __uint_as_float(rr[e]) * inv_l;
-          worst = max_nan(worst, fabsf(v[e]));
-        }
-        if (row_ok) {
-          uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            d4[q] = make_uint4(pack2<F16>(v[8 * q], v[8 * q + 1]),
-                               pack2<F16>(v[8 * q + 2], v[8 * q + 3]),
-                               pack2<F16>(v[8 * q + 4], v[8 * q + 5]),
-                               pack2<F16>(v[8 * q + 6], v[8 * q + 7]));
-        }
+    for (int c = 0; c < D / 32; ++c) {
+      tmem_ld32(o_col + 32 * c, rr);
+      tmem_wait_ld();
+      if (c == D / 32 - 1) {  // the row is in registers: the accumulator may go
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->o_free[i]);
       }
-      tc_fence_before();
-      uint32_t again = __ballot_sync(0xffffffffu, row_ok && !(worst <= 3.4028235e38f));
-      while (again) {
-        const int src = __ffs(again) - 1;
-        again &= again - 1;
-        plain_row<D, F16>(a, start, __shfl_sync(0xffffffffu, pos, src),
-                          __shfl_sync(0xffffffffu, head, src));
+      float v[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        v[e] = __uint_as_float(rr[e]) * inv_l;
+        worst = max_nan(worst, fabsf(v[e]));
       }
+      if (row_ok) {
+        uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          d4[q] = make_uint4(pack2<F16>(v[8 * q], v[8 * q + 1]),
+                             pack2<F16>(v[8 * q + 2], v[8 * q + 3]),
+                             pack2<F16>(v[8 * q + 4], v[8 * q + 5]),
+                             pack2<F16>(v[8 * q + 6], v[8 * q + 7]));
+      }
+    }
+    uint32_t again = __ballot_sync(0xffffffffu, row_ok && !(worst <= 3.4028235e38f));
+    while (again) {
+      const int src = __ffs(again) - 1;
+      again &= again - 1;
+      plain_row<D, F16>(a, x.start, __shfl_sync(0xffffffffu, pos, src),
+                        __shfl_sync(0xffffffffu, head, src));
+    }
     }
   }
   __syncthreads();
@@ -439,8 +507,8 @@ cudaError_t run(const h3_prompts* p, const Args& a, cudaStream_t st) {
       !tmap_heads(&tk, a.k, F16, D, p->kv_heads, p->rows, a.k_stride, 1, 128) ||
       !tmap_heads(&tv, a.v, F16, D, p->kv_heads, p->rows, a.v_stride, 1, 128))
     return cudaErrorInvalidValue;
-  k_prompt_attention<D, F16><<<(unsigned)(p->n_items * p->kv_heads), NUM_THREADS, smem_bytes<D>(),
-                               st>>>(tq, tk, tv, a);
+  const int ctas = a.n_work < num_sms() ? a.n_work : num_sms();
+  k_prompt_attention<D, F16><<<(unsigned)ctas, NUM_THREADS, smem_bytes<D>(), st>>>(tq, tk, tv, a);
   return cudaGetLastError();
 }
 
@@ -491,6 +559,7 @@ cudaError_t launch_prompt_attention(const h3_prompts* p, bool f16, const void* q
   a.v_stride = v_stride;
   a.o_stride = o_stride;
   a.items = static_cast<const int4*>(p->items);
+  a.n_work = p->n_items * p->kv_heads;
   a.kv_heads = p->kv_heads;
   a.group = p->q_heads / p->kv_heads;
   a.tile_pos = 128 / a.group;

@@ -1,5 +1,6 @@
 // Arithmetic shared by the attention kernels' softmax: the MUFU exponential,
-// packed fp32 pairs, a three-way maximum and one that keeps NaN.
+// packed fp32 pairs, an exponential on the FMA pipe, a three-way maximum and one
+// that keeps NaN.
 #pragma once
 
 #include <stdint.h>
@@ -35,6 +36,30 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// 2^x for two values on the FMA pipe: x = j + f with j = round(x) (by adding
+// `magic` = 1.5 * 2^23, which leaves the integer in the low mantissa bits) and f
+// in [-1/2, 1/2], 2^f by a cubic, j added to the exponent. Inputs below -126 are
+// clamped.
+struct Cubic {
+  float c3, c2, c1, c0, magic;
+};
+__device__ __forceinline__ void exp2_cubic2(uint64_t x2, const Cubic& c, float& p0, float& p1) {
+  float x0, x1;
+  f2_unpack(x2, x0, x1);
+  const uint64_t xc = f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+  const uint64_t t = f2_add(xc, f2_pack(c.magic, c.magic));
+  const uint64_t jf = f2_add(t, f2_pack(-c.magic, -c.magic));  // j, exact
+  const uint64_t f = f2_fma(jf, f2_pack(-1.f, -1.f), xc);      // x - j, exact
+  uint64_t p = f2_fma(f2_pack(c.c3, c.c3), f, f2_pack(c.c2, c.c2));
+  p = f2_fma(p, f, f2_pack(c.c1, c.c1));
+  p = f2_fma(p, f, f2_pack(c.c0, c.c0));
+  float q0, q1, t0, t1;
+  f2_unpack(p, q0, q1);
+  f2_unpack(t, t0, t1);
+  p0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
+  p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
