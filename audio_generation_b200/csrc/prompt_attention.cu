@@ -21,10 +21,10 @@
 // Work items (two tiles each) come from the prompts object, longest key range
 // first. One CTA per SM takes them in turn (there and back over the list's
 // rounds, so that no CTA always gets the longer one), every role running on into
-// the next item: its first keys and its q are fetched and its first scores
-// computed while the item before is still being divided and stored. q has one
-// buffer, given back after the item's last score product; an O accumulator is
-// given back when its rows have been read.
+// the next item: its first keys and its q are fetched and a query tile's first
+// scores computed right after the tile's last product of the item before, while
+// that is still being divided and stored. A q tile is given back after the item's
+// last score product with it, an O accumulator when its rows have been read.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -49,7 +49,7 @@ constexpr int TMEM_COLS = 512;
 constexpr float kLazyRescale = 8.0f;  // log2 units
 
 struct Bars {
-  uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2],
+  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2],
       p_full[2], o_final[2], o_free[2], drain;
 };
 
@@ -178,9 +178,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   };
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->q_empty[i], 1);
       mbar_init(&bars->k_full[i], 1);
       mbar_init(&bars->k_empty[i], 1);
       mbar_init(&bars->v_full[i], 1);
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (warp == 8) {
       // ---------------------------------------------------------- producer
       if (lane == 0) {
-        int nk = 0, nv = 0, nq = 0;  // fills so far
+        int nk = 0, nv = 0, nq[2] = {0, 0};  // fills so far
         bool ok = true;
         Item x;
         for (int w = 0; ok && piece(w, x); ++w) {
@@ -223,16 +223,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               tma_load_3d(smem + OFF_K + st * TILE + h * HALF, &tk, &bars->k_full[st], 64 * h,
                           x.kvh, x.start + j * 128);
             ++nk;
-            if (j == 0) {
-              const int tiles = x.n1 > 0 ? 2 : 1;
-              if (!mbar_wait(&bars->q_empty, (nq & 1) ^ 1, wc)) { ok = false; break; }
-              mbar_arrive_expect_tx(&bars->q_full, tiles * (D / 64) * P * a.group * 128);
-              for (int i = 0; i < tiles; ++i)
-                for (int h = 0; h < D / 64; ++h)
-                  tma_load_3d(smem + OFF_Q + i * TILE + h * HALF, &tq, &bars->q_full, 64 * h,
-                              x.kvh * a.group, x.start + x.pos0 + i * P);
-              ++nq;
+            for (int i = 0; j == 0 && i < (x.n1 > 0 ? 2 : 1) && ok; ++i) {
+              if (!mbar_wait(&bars->q_empty[i], (nq[i] & 1) ^ 1, wc)) { ok = false; break; }
+              mbar_arrive_expect_tx(&bars->q_full[i], (D / 64) * P * a.group * 128);
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(smem + OFF_Q + i * TILE + h * HALF, &tq, &bars->q_full[i], 64 * h,
+                            x.kvh * a.group, x.start + x.pos0 + i * P);
+              ++nq[i];
             }
+            if (!ok) break;
             st = nv & 1;
             if (!mbar_wait(&bars->v_empty[st], ((nv >> 1) & 1) ^ 1, wc)) { ok = false; break; }
             mbar_arrive_expect_tx(&bars->v_full[st], TILE);
@@ -243,7 +242,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
         if (!ok) {  // let issued copies land before the CTA retires
-          if (nq > 0) mbar_drain(&bars->q_full, (nq - 1) & 1);
+          for (int i = 0; i < 2; ++i)
+            if (nq[i] > 0) mbar_drain(&bars->q_full[i], (nq[i] - 1) & 1);
           for (int j = nk > 2 ? nk - 2 : 0; j < nk; ++j) mbar_drain(&bars->k_full[j & 1], (j >> 1) & 1);
           for (int j = nv > 2 ? nv - 2 : 0; j < nv; ++j) mbar_drain(&bars->v_full[j & 1], (j >> 1) & 1);
         }
@@ -259,72 +259,92 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto wait_all = [&](uint64_t* bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
       };
-      bool ok = true;
-      int kv = 0;                       // key tiles of the items before
-      int done[2] = {0, 0};             // score tiles of each query tile so far
-      int rounds[2] = {0, 0};           // items in which the query tile had work
-      Item x;
-      for (int w = 0; ok && piece(w, x); ++w) {
-        const int n0 = x.n0, n1 = x.n1, n = max(n0, n1);
-        if (!wait_all(&bars->q_full, w & 1)) { ok = false; break; }
-        tc_fence_after();
-        int left = n0 + n1;  // score products to issue
-        // Tile 0 uses key tile j first where it visits it, tile 1 last; tile 1's
-        // range is at least tile 0's unless tile 1 is empty.
-        auto issue_s = [&](int i, int j) -> bool {
-          const int c = kv + j, st = c & 1;
-          if (i == 0 || j >= n0) {
-            if (!wait_all(&bars->k_full[st], (c >> 1) & 1)) return false;
-            tc_fence_after();
-          }
-          const uint32_t kl = k_lo + st * (TILE >> 4);
-          const uint32_t ql = q_lo + i * (TILE >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
-            umma_ss_w_elect(tmem + i * 128, ql + off, hi, kl + off, hi, idesc_s,
-                            kk > 0 ? 1u : 0u);
-          }
-          umma_commit_elect(&bars->s_full[i]);
-          if (i == 1 || j >= n1) umma_commit_elect(&bars->k_empty[st]);
-          if (--left == 0) umma_commit_elect(&bars->q_empty);
-          return true;
-        };
-        // O_i += P_i(j) V_j in two halves of the keys, each as soon as it is stored
-        auto issue_pv = [&](int i, int j) -> bool {
-          const int c = kv + j, st = c & 1, ph = (done[i] + j) & 1;
-          if (j == 0 && !wait_all(&bars->o_free[i], (rounds[i] & 1) ^ 1)) return false;
-          if (!wait_all(&bars->p_half[i], ph)) return false;
-          if ((i == 0 || j >= n0) && !wait_all(&bars->v_full[st], (c >> 1) & 1)) return false;
-          tc_fence_after();
-          const uint32_t vl = v_lo + st * (TILE >> 4);
-          const uint32_t o = tmem + 256 + i * 128, p = tmem + i * 128;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ts_w_elect(o, p + kk * 8, vl + kk * (2048 >> 4), hi, idesc_pv,
-                            (j > 0 || kk > 0) ? 1u : 0u);
-          if (!wait_all(&bars->p_full[i], ph)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 4; kk < 8; ++kk)
-            umma_ts_w_elect(o, p + kk * 8, vl + kk * (2048 >> 4), hi, idesc_pv, 1u);
-          if (i == 1 || j >= n1) umma_commit_elect(&bars->v_empty[st]);
-          if (j == (i == 0 ? n0 : n1) - 1) umma_commit_elect(&bars->o_final[i]);
-          return true;
-        };
-        ok = issue_s(0, 0);
-        if (ok && n1 > 0) ok = issue_s(1, 0);
-        for (int j = 0; j < n && ok; ++j) {
-          if (j < n0) ok = issue_pv(0, j);
-          if (ok && j + 1 < n0) ok = issue_s(0, j + 1);
-          if (ok && j < n1) ok = issue_pv(1, j);
-          if (ok && j + 1 < n1) ok = issue_s(1, j + 1);
+      // One step per key tile of each item in turn, the c-th of all. Tile 0 uses a
+      // step's key tile first where it visits it, tile 1 last: its range is the
+      // item's (n tiles) unless it is empty, and tile 0's is that or one less.
+      uint32_t p_ph[2] = {0, 0}, q_ph[2] = {0, 0}, o_ph[2] = {1, 1};  // parities to wait for
+      // S_i = Q_i K^T: the tile's first and last of the item, the key tile's last use
+      auto issue_s = [&](int i, int c, bool first, bool last, bool free) -> bool {
+        const int st = c & 1;
+        if (first) {
+          if (!wait_all(&bars->q_full[i], q_ph[i])) return false;
+          q_ph[i] ^= 1;
         }
-        kv += n;
-        done[0] += n0;
-        done[1] += n1;
-        ++rounds[0];
-        rounds[1] += n1 > 0;
+        if (!wait_all(&bars->k_full[st], (c >> 1) & 1)) return false;
+        tc_fence_after();
+        const uint32_t kl = k_lo + st * (TILE >> 4);
+        const uint32_t ql = q_lo + i * (TILE >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) >> 4;
+          umma_ss_w_elect(tmem + i * 128, ql + off, hi, kl + off, hi, idesc_s, kk > 0 ? 1u : 0u);
+        }
+        umma_commit_elect(&bars->s_full[i]);
+        if (free) umma_commit_elect(&bars->k_empty[st]);
+        if (last) umma_commit_elect(&bars->q_empty[i]);
+        return true;
+      };
+      // O_i += P_i V in two halves of the keys, each as soon as it is stored
+      auto issue_pv = [&](int i, int c, bool first, bool last, bool free) -> bool {
+        const int st = c & 1;
+        if (first) {
+          if (!wait_all(&bars->o_free[i], o_ph[i])) return false;
+          o_ph[i] ^= 1;
+        }
+        if (!wait_all(&bars->p_half[i], p_ph[i])) return false;
+        if (!wait_all(&bars->v_full[st], (c >> 1) & 1)) return false;
+        tc_fence_after();
+        const uint32_t vl = v_lo + st * (TILE >> 4);
+        const uint32_t o = tmem + 256 + i * 128, p = tmem + i * 128;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ts_w_elect(o, p + kk * 8, vl + kk * (2048 >> 4), hi, idesc_pv,
+                          (!first || kk > 0) ? 1u : 0u);
+        if (!wait_all(&bars->p_full[i], p_ph[i])) return false;
+        p_ph[i] ^= 1;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 4; kk < 8; ++kk)
+          umma_ts_w_elect(o, p + kk * 8, vl + kk * (2048 >> 4), hi, idesc_pv, 1u);
+        if (free) umma_commit_elect(&bars->v_empty[st]);
+        if (last) umma_commit_elect(&bars->o_final[i]);
+        return true;
+      };
+      bool ok = true;
+      Item x;
+      // (the shuffles only tell the compiler that the ranges are the same in every
+      // lane: its MMA operands then stay in uniform registers)
+      int z0 = 0, z1 = 0;  // the next item's ranges, 0 past the last
+      auto next = [&](int w) {
+        const bool have = piece(w, x);
+        z0 = __shfl_sync(0xffffffffu, have ? x.n0 : 0, 0);
+        z1 = __shfl_sync(0xffffffffu, have ? x.n1 : 0, 0);
+      };
+      next(0);
+      int n0 = 0, n1 = 0, c = -1;  // the item before the first
+      for (int w = 1; ok && (n0 > 0 || z0 > 0); ++w) {
+        // an item's last step and the next one's first scores
+        const int n = max(n0, n1);
+        if (n0 > 0 && n0 == n) ok = issue_pv(0, c, n == 1, true, n1 == 0);
+        if (ok && z0 > 0) ok = issue_s(0, c + 1, true, z0 == 1, z1 == 0);
+        if (ok && n1 > 0) ok = issue_pv(1, c, n == 1, true, true);
+        if (ok && z1 > 0) ok = issue_s(1, c + 1, true, z1 == 1, true);
+        if (!ok) break;
+        // the next item's steps but the last
+        n0 = z0;
+        n1 = z1;
+        next(w);
+        const int m = max(n0, n1);
+        ++c;
+        for (int j = 0; j + 1 < m; ++j, ++c) {
+          ok = issue_pv(0, c, j == 0, j + 1 == n0, n1 == 0);
+          if (ok && j + 1 < n0) ok = issue_s(0, c + 1, false, j + 2 == n0, n1 == 0);
+          if (n1 > 0) {
+            if (ok) ok = issue_pv(1, c, j == 0, false, true);
+            if (ok) ok = issue_s(1, c + 1, false, j + 2 == n1, true);
+          }
+          if (!ok) break;
+        }
       }
       umma_commit_elect(&bars->drain);  // every MMA issued is complete past this point
       mbar_drain(&bars->drain, 0);
@@ -442,7 +462,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int head = x.kvh * a.group + r - rp * a.group;
     const bool row_ok = rp < P && pos < x.len;
     const float inv_l = 1.f / l_run;
-    uint16_t* dst = a.o + (row_ok ? (x.start + pos) * a.o_stride + head * D : 0);
+    // A row's 64 bytes at a time; four lanes turn their pieces of 16 so that a
+    // store covers 64 bytes of eight rows instead of 16 of 32.
+    const long long mine = row_ok ? (x.start + pos) * a.o_stride + head * D : -1;
+    long long dst[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dst[k] = __shfl_sync(0xffffffffu, mine, (lane & 28) + k);
+    const bool odd = lane & 1, high = lane & 2;
     float worst = 0.f;  // NaN or infinite if any value of the row is
     uint32_t rr[32];
 #pragma unroll 1
@@ -454,21 +480,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->o_free[i]);
       }
-      float v[32];
+      uint32_t u[4][4];  // [piece][word]
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        v[e] = __uint_as_float(rr[e]) * inv_l;
-        worst = max_nan(worst, fabsf(v[e]));
+      for (int e = 0; e < 16; ++e) {
+        const float v0 = __uint_as_float(rr[2 * e]) * inv_l;
+        const float v1 = __uint_as_float(rr[2 * e + 1]) * inv_l;
+        worst = max_nan(worst, fabsf(v0));
+        worst = max_nan(worst, fabsf(v1));
+        u[e / 4][e % 4] = pack2<F16>(v0, v1);
       }
-      if (row_ok) {
-        uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          d4[q] = make_uint4(pack2<F16>(v[8 * q], v[8 * q + 1]),
-                             pack2<F16>(v[8 * q + 2], v[8 * q + 3]),
-                             pack2<F16>(v[8 * q + 4], v[8 * q + 5]),
-                             pack2<F16>(v[8 * q + 6], v[8 * q + 7]));
+      for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int h = 0; h < 4; h += 2) {  // lanes l and l ^ 1: pieces h, h + 1
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? u[h][k] : u[h + 1][k], 1);
+          if (odd) u[h][k] = got; else u[h + 1][k] = got;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // lanes l and l ^ 2: pieces h, h + 2
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? u[h][k] : u[h + 2][k], 2);
+          if (high) u[h][k] = got; else u[h + 2][k] = got;
+        }
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // piece lane % 4 of row k of the four
+        if (dst[k] >= 0)
+          *reinterpret_cast<uint4*>(a.o + dst[k] + 32 * c + 8 * (lane & 3)) =
+              make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
     }
     uint32_t again = __ballot_sync(0xffffffffu, row_ok && !(worst <= 3.4028235e38f));
     while (again) {
