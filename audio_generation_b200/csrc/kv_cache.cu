@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
   if (lane == 31) warp_sum[warp] = upto;
   if (warp == kConsumers) {
     if (lane < R::STAGES) {
-      mbar_init(&full[lane], 1);
+      mbar_init(&full[lane], 2);   // the copies issued, the list entry written
       mbar_init(&empty[lane], 2);  // the two warps of a pair
     }
     if (lane == 0) s_abort = 0;
@@ -481,8 +481,23 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
     while (i < n_units && ok) {
       const int n = min(min(32, pages - page), n_units - i);
       const int kvh = hg / a.row_groups;
+      auto issue = [&](int k, int block) {  // unit k's copies; nothing for no block
+        const int s = k % R::STAGES;
+        if (block < 0) {
+          mbar_arrive(&full[s]);
+          return;
+        }
+        const size_t at = ((size_t)block * a.kv_heads + kvh) * R::BLOCK;
+        uint8_t* dst = smem + R::SUMS + s * 2 * R::BLOCK;
+        mbar_arrive_expect_tx(&full[s], 2 * R::BLOCK);
+        bulk_load(dst, a.k_codes + at, R::BLOCK, &full[s]);
+        bulk_load(dst + R::BLOCK, a.v_codes + at, R::BLOCK, &full[s]);
+      };
+      // the first units' copies go out before anything else is known of them
+      const int early = i == 0 ? min(n, R::STAGES) : 0;
       if (lane < n) {
         const int b = block_of(a.table, a.width, seq, page + lane, a.n_blocks, a.err);
+        if (lane < early) issue(lane, b);
         const size_t at = (size_t)max(b, 0) * a.kv_heads + kvh;
         list[(i + lane) % kListSize] = Entry{b, page + lane, b < 0 ? 0.f : a.k_scales[at],
                                              b < 0 ? 0.f : a.v_scales[at]};
@@ -491,23 +506,17 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
       if (lane == 0) {
         for (int k = i; k < i + n; ++k) {
           const int s = k % R::STAGES;
-          if (!mbar_wait(&empty[s], ((k / R::STAGES) & 1) ^ 1, wc)) {
-            ok = false;
-            // let issued copies land before the block retires
-            for (int j = k > R::STAGES ? k - R::STAGES : 0; j < k; ++j)
-              mbar_drain(&full[j % R::STAGES], (j / R::STAGES) & 1);
-            break;
+          if (k >= i + early) {
+            if (!mbar_wait(&empty[s], ((k / R::STAGES) & 1) ^ 1, wc)) {
+              ok = false;
+              // let issued copies land before the block retires
+              for (int j = k > R::STAGES ? k - R::STAGES : 0; j < k; ++j)
+                mbar_drain(&full[j % R::STAGES], (j / R::STAGES) & 1);
+              break;
+            }
+            issue(k, list[k % kListSize].block);
           }
-          const int block = list[k % kListSize].block;
-          if (block < 0) {
-            mbar_arrive(&full[s]);  // nothing to load, nothing to attend
-            continue;
-          }
-          const size_t at = ((size_t)block * a.kv_heads + kvh) * R::BLOCK;
-          uint8_t* dst = smem + R::SUMS + s * 2 * R::BLOCK;
-          mbar_arrive_expect_tx(&full[s], 2 * R::BLOCK);
-          bulk_load(dst, a.k_codes + at, R::BLOCK, &full[s]);
-          bulk_load(dst + R::BLOCK, a.v_codes + at, R::BLOCK, &full[s]);
+          mbar_arrive(&full[s]);  // the entry is written
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -855,23 +864,33 @@ __global__ void __launch_bounds__(D / 4 * kJoinParts) k_cache_join(const AttnArg
   if (n == 0 || h0 + r >= a.group) return;
   // part 1 of its own range, part 0 of the following ones
   auto at = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * a.pass + r; };
+  auto part = [&](int i) { return *reinterpret_cast<const float4*>(a.part + at(i) * D + 4 * d); };
+  constexpr int kAhead = 4;  // fetched before the maximum is known
+  float4 x[kAhead];
+  float2 ml[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const int i = p + k * kJoinParts;
+    x[k] = i < n ? part(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    ml[k] = i < n ? a.stat[at(i)] : make_float2(-INFINITY, 0.f);
+  }
   float m = -INFINITY;
   for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, a.stat[at(i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-#pragma unroll 4
-  for (int i = p; i < n; i += kJoinParts) {
-    const float2 ml = a.stat[at(i)];
-    const float4 x = *reinterpret_cast<const float4*>(a.part + at(i) * D + 4 * d);
-    const float f = ml.x == m ? 1.f : exp2_mufu(ml.x - m);
-    sum.x = fmaf(x.x, f, sum.x);
-    sum.y = fmaf(x.y, f, sum.y);
-    sum.z = fmaf(x.z, f, sum.z);
-    sum.w = fmaf(x.w, f, sum.w);
-    l = fmaf(ml.y, f, l);
-  }
+  auto add = [&](const float4& v, const float2& st) {
+    const float f = st.x == m ? 1.f : exp2_mufu(st.x - m);
+    sum.x = fmaf(v.x, f, sum.x);
+    sum.y = fmaf(v.y, f, sum.y);
+    sum.z = fmaf(v.z, f, sum.z);
+    sum.w = fmaf(v.w, f, sum.w);
+    l = fmaf(st.y, f, l);
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) add(x[k], ml[k]);
+  for (int i = p + kAhead * kJoinParts; i < n; i += kJoinParts) add(part(i), a.stat[at(i)]);
   sums[p][d] = sum;
   if (d == 0) weights[p] = l;
   __syncthreads();

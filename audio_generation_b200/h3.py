@@ -621,10 +621,10 @@ def make_kv_cache(k_codes, v_codes, k_scales, v_scales) -> h3_kv_cache:
     """The cache descriptor of a pool's tensors, sizes from k_codes [n_blocks,
     kv_heads, block_tokens, head_dim] (the caller keeps the tensors)."""
     n_blocks, kv_heads, block_tokens, head_dim = k_codes.shape
-    if tuple(v_codes.shape) != (n_blocks, kv_heads, head_dim, block_tokens):
+    if v_codes.shape != (n_blocks, kv_heads, head_dim, block_tokens):
         raise H3Error(H3_ERR_SHAPE, "make_kv_cache")
-    return h3_kv_cache(n_blocks, block_tokens, kv_heads, head_dim, _ptr(k_codes), _ptr(v_codes),
-                       _ptr(k_scales), _ptr(v_scales))
+    return h3_kv_cache(n_blocks, block_tokens, kv_heads, head_dim, k_codes.data_ptr(),
+                       v_codes.data_ptr(), _ptr(k_scales), _ptr(v_scales))
 
 
 def h3_kv_cache_store(cache: h3_kv_cache, n_seq: int, max_new: int, block_table,
