@@ -32,31 +32,35 @@ __device__ __forceinline__ void store_codes(const uint4& u, const RowScale& s, v
     *reinterpret_cast<uint2*>(dst) = c;
 }
 
-template <int G>
+// The maximum over the block's threads, or over each warp's alone.
+template <bool BLOCK>
 __device__ __forceinline__ float group_max(float m) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if constexpr (G > 32) {
-    __shared__ float part[G / 32];
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  if constexpr (BLOCK) {
+    __shared__ float part[32];
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
-    m = part[threadIdx.x & (G / 32 - 1)];
+    m = lane < warps ? part[lane] : 0.f;
 #pragma unroll
-    for (int o = G / 64; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
   return m;
 }
 
-// G threads per row (a warp with eight rows per block, or the block), NV 16-byte
-// vectors of the row per thread in registers; NV = 0: any length, read twice.
+// A block per row (G threads; 0: as launched), or a warp (G = 32, eight rows per
+// block); NV 16-byte vectors of the row per thread in registers; NV = 0: any
+// length, read twice.
 template <h3_type T, int G, int NV>
-__global__ void __launch_bounds__(G == 32 ? 256 : G)
+__global__ void __launch_bounds__(G == 32 ? 256 : G == 0 ? 1024 : G)
     k_quantize_rows_int8(int rows, int K, const uint4* __restrict__ x, int64_t stride_vec,
                          uint8_t* __restrict__ codes, float* __restrict__ scales) {
   constexpr int VE = Vec<T>::N;
+  const int g = G == 0 ? blockDim.x : G;
   const int row = G == 32 ? blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
   if (G == 32 && row >= rows) return;
-  const int t = threadIdx.x & (G - 1);
+  const int t = G == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int nvec = K / VE;
   const uint4* xr = x + row * stride_vec;
   uint8_t* cr = codes + (size_t)row * K;
@@ -65,16 +69,16 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G)
   if constexpr (NV > 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (t + i * G < nvec) u[i] = __ldcs(xr + t + i * G);
+      if (t + i * g < nvec) u[i] = __ldcs(xr + t + i * g);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (t + i * G < nvec) peak.add(u[i]);
+      if (t + i * g < nvec) peak.add(u[i]);
   } else {
-    for (int i = t; i < nvec; i += G) peak.add(xr[i]);
+    for (int i = t; i < nvec; i += g) peak.add(xr[i]);
   }
-  const float m = group_max<G>(peak.value());
+  const float m = group_max<G != 32>(peak.value());
   if (!(m <= kMaxFinite)) {  // an infinity or a NaN in the row
-    for (int i = t; i < K / 4; i += G) reinterpret_cast<uint32_t*>(cr)[i] = 0;
+    for (int i = t; i < K / 4; i += g) reinterpret_cast<uint32_t*>(cr)[i] = 0;
     if (t == 0) scales[row] = __int_as_float(0x7fc00000);
     return;
   }
@@ -85,35 +89,38 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G)
   if constexpr (NV > 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (t + i * G < nvec) store_codes<T>(u[i], s, cr + (t + i * G) * VE);
+      if (t + i * g < nvec) store_codes<T>(u[i], s, cr + (t + i * g) * VE);
   } else {
-    for (int i = t; i < nvec; i += G) store_codes<T>(xr[i], s, cr + (size_t)i * VE);
+    for (int i = t; i < nvec; i += g) store_codes<T>(xr[i], s, cr + (size_t)i * VE);
   }
 }
 
-template <h3_type T, int G, int NV>
-cudaError_t run_quantize(int rows, int K, const void* x, int64_t stride_vec, void* codes,
-                         float* scales, cudaStream_t st) {
-  const int grid = G == 32 ? (rows + 7) / 8 : rows;
-  k_quantize_rows_int8<T, G, NV><<<grid, G == 32 ? 256 : G, 0, st>>>(
-      rows, K, static_cast<const uint4*>(x), stride_vec, static_cast<uint8_t*>(codes), scales);
-  return cudaGetLastError();
-}
-
-// A warp per row while the row fits a warp's registers, then a block of 256,
-// then of 1024, so that a row's loads are all in flight at once.
+// Short rows take a warp, longer ones a block of as many warps as hold them at
+// eight vectors a thread (four where there are few rows, so that a row's loads
+// are all in flight and little is done in turn), so that few threads idle. The
+// usual lengths have their block size built in: 14336 bf16 elements a row, 8192
+// rows, 57 us against 62 us with the block size read at run time (and with seven
+// warps instead of eight, which leave an SM fewer).
 template <h3_type T>
 cudaError_t quantize(int rows, int K, const void* x, int64_t stride_vec, void* codes,
                      float* scales, cudaStream_t st) {
   const int nvec = K / Vec<T>::N;
-#define H3_Q(G, NV) return run_quantize<T, G, NV>(rows, K, x, stride_vec, codes, scales, st)
-  if (nvec <= 64) H3_Q(32, 2);
-  if (nvec <= 256) H3_Q(32, 8);
-  if (nvec <= 1024) H3_Q(256, 4);
-  if (nvec <= 2048) H3_Q(256, 8);
-  if (nvec <= 8192) H3_Q(1024, 8);
-  H3_Q(1024, 0);
+  const uint4* xv = static_cast<const uint4*>(x);
+  uint8_t* c = static_cast<uint8_t*>(codes);
+#define H3_Q(G, NV, GRID, THREADS)                                                     \
+  k_quantize_rows_int8<T, G, NV><<<GRID, THREADS, 0, st>>>(rows, K, xv, stride_vec, c, scales)
+  const int few = (nvec + 127) / 128 * 32, many = (nvec + 255) / 256 * 32;
+  if (nvec <= 64) H3_Q(32, 2, (rows + 7) / 8, 256);
+  else if (nvec <= 256) H3_Q(32, 8, (rows + 7) / 8, 256);
+  else if (nvec <= 4096 && rows <= 4 * num_sms()) H3_Q(0, 4, rows, few);
+  else if (many == 64) H3_Q(64, 8, rows, 64);
+  else if (many == 96) H3_Q(96, 8, rows, 96);
+  else if (many == 128) H3_Q(128, 8, rows, 128);
+  else if (many == 224 || many == 256) H3_Q(256, 8, rows, 256);
+  else if (nvec <= 8192) H3_Q(0, 8, rows, many);
+  else H3_Q(0, 0, rows, 1024);
 #undef H3_Q
+  return cudaGetLastError();
 }
 
 // ------------------------------------------------------------- matrix product
@@ -141,6 +148,21 @@ __device__ __forceinline__ void store_one(const Out& o, size_t off, float v) {
     static_cast<__half*>(o.p)[off] = __float2half_rn(v);
   else
     static_cast<float*>(o.p)[off] = v;
+}
+
+// Four neighbouring values of one row, aligned to their size.
+__device__ __forceinline__ void store_4(const Out& o, size_t off, const float* v) {
+  if (o.type == H3_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(o.p) + off) =
+        make_float4(v[0], v[1], v[2], v[3]);
+  } else if (o.type == H3_BF16) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(o.p) + off) =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  } else {
+    const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(o.p) + off) = make_uint2(
+        *reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
 }
 
 // 32 neighbouring values of one row, 16-byte aligned.
@@ -355,11 +377,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-// Few rows (at most NT): bound by the bytes of the weights. The weights take
-// the MMA's 128-row side and the tokens its N side, so a CTA streams tiles of 128
-// weight rows through a ring that fills most of its SM's shared memory (the
-// bytes in flight are what carries the bandwidth), one CTA per SM, the ring
-// running on from tile to tile. With few tiles the CTAs of a cluster share the K
+// Few rows: bound by the bytes of the weights, or by how many SMs have work. The
+// weights take the MMA's 128-row side and NT tokens its N side, so a CTA streams
+// tiles of 128 weight rows through a ring that fills most of its SM's shared
+// memory (the bytes in flight are what carries the bandwidth), one CTA per SM,
+// the ring running on from tile to tile (token tiles first, so that a weight tile
+// stays in L2 for its others). With few tiles the CTAs of a cluster share the K
 // axis of one and add their integer sums through distributed shared memory,
 // each finishing a share of the tokens. Neighbouring lanes store neighbouring
 // columns of out. Warps as above; the accumulator is double-buffered.
@@ -370,9 +393,14 @@ constexpr int s_stages() { return 200 * 1024 / s_stage<NT>(); }
 template <int NT>
 constexpr int s_smem() { return s_stages<NT>() * s_stage<NT>() + 1024 + 512; }
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+constexpr int kMaxSplit = 8;  // CTAs that share a K axis
+
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -397,7 +425,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = split > 1 ? (int)cluster_ctarank() : 0;
-  const int tiles = (N + BM - 1) / BM;
+  const int m_tiles = (M + NT - 1) / NT;
+  const int tiles = (N + BM - 1) / BM * m_tiles;
   const int tile0 = (int)(blockIdx.x / split), step = (int)(gridDim.x / split);
   const int kb0 = (int)((long long)kb_n * rank / split);
   const int kb1 = (int)((long long)kb_n * (rank + 1) / split);
@@ -440,8 +469,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           uint8_t* sw = smem + s * STAGE;
           mbar_arrive_expect_tx(&full[s], STAGE);
-          tma_load_2d(sw, &tmW, &full[s], kb * BKB, t * BM);
-          tma_load_2d(sw + A_STAGE, &tmA, &full[s], kb * BKB, 0);
+          tma_load_2d(sw, &tmW, &full[s], kb * BKB, t / m_tiles * BM);
+          tma_load_2d(sw + A_STAGE, &tmA, &full[s], kb * BKB, t % m_tiles * NT);
         }
       }
       if (!ok) {  // let issued copies land before the CTA retires
@@ -486,7 +515,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t it = 0;
     for (int t = tile0; t < tiles; t += step, ++it) {
       const uint32_t acc = it & 1, aph = (it >> 1) & 1;
-      const int n = t * BM + r;
+      const int n = t / m_tiles * BM + r, m0 = t % m_tiles * NT;
+      const int rows = min(NT, M - m0);
       const float sw = n < N ? out.w_scale[n] : 0.f;
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], aph, wc))) break;
       tc_fence_after();
@@ -502,12 +532,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (split > 1) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (32 * c + i < M && 32 * c + i < NT) part[(32 * c + i) * BM + r] = v[i];
+            if (32 * c + i < rows) part[(32 * c + i) * BM + r] = v[i];
         } else if (n < N) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int m = 32 * c + i;
-            if (m < M)
+            const int m = m0 + 32 * c + i;
+            if (32 * c + i < rows)
               store_one(out, m * out.stride + n, (float)(int)v[i] * (out.a_scale[m] * sw));
           }
         }
@@ -520,16 +550,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (split > 1) {
     __syncwarp();
     cluster_sync();
-    const int r = (warp & 3) * 32 + lane, n = tile0 * BM + r;
+    const int n = tile0 / m_tiles * BM + 4 * lane;  // four columns of a token per thread
     if (warp >= 2 && n < N) {
-      const float sw = out.w_scale[n];
-      const int m0 = M * rank / split, m1 = M * (rank + 1) / split;
-      const uint32_t mine = smem_u32(smem) + r * 4;
-      for (int m = m0; m < m1; ++m) {
-        int sum = 0;
-        for (int q = 0; q < split; ++q)
-          sum += (int)ld_cluster_u32(mapa_shared(mine + m * BM * 4, q));
-        store_one(out, m * out.stride + n, (float)sum * (out.a_scale[m] * sw));
+      const int m0 = tile0 % m_tiles * NT, rows = min(NT, M - m0);
+      const int first = rows * rank / split, last = rows * (rank + 1) / split;
+      const bool vec = n + 4 <= N && out.stride % 4 == 0;
+      float sw[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sw[e] = n + e < N ? out.w_scale[n + e] : 0.f;
+      uint32_t from[kMaxSplit];
+#pragma unroll
+      for (int q = 0; q < kMaxSplit; ++q)
+        from[q] = mapa_shared(smem_u32(smem) + lane * 16, q < split ? q : 0);
+      for (int i = first + warp - 2; i < last; i += 4) {
+        uint4 v[kMaxSplit];
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q)
+          v[q] = q < split ? ld_cluster_v4(from[q] + i * BM * 4) : make_uint4(0, 0, 0, 0);
+        uint4 sum = v[0];
+#pragma unroll
+        for (int q = 1; q < kMaxSplit; ++q)
+          sum.x += v[q].x, sum.y += v[q].y, sum.z += v[q].z, sum.w += v[q].w;
+        const float sa = out.a_scale[m0 + i];
+        const float y[4] = {(float)(int)sum.x * (sa * sw[0]), (float)(int)sum.y * (sa * sw[1]),
+                            (float)(int)sum.z * (sa * sw[2]), (float)(int)sum.w * (sa * sw[3])};
+        const size_t at = (m0 + i) * out.stride + n;
+        if (vec) {
+          store_4(out, at, y);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < N) store_one(out, at + e, y[e]);
+        }
       }
     }
     cluster_sync();  // no CTA leaves while another reads its sums
@@ -574,53 +626,95 @@ cudaError_t run_pair(int M, int N, int K, const void* a, const void* w, const Ou
 
 // Clusters of `split` CTAs that the current device runs at once (asked once).
 template <int NT>
-int clusters_at_once(cudaLaunchConfig_t cfg, int split) {
-  static int known[64][9] = {};
+int clusters_at_once(int split) {
+  static int known[64][kMaxSplit + 1] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   if (known[dev][split] == 0) {
-    int n = 0;
+    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)split);
-    if (cudaOccupancyMaxActiveClusters(&n, k_int8_skinny<NT>, &cfg) != cudaSuccess) {
+    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.dynamicSmemBytes = s_smem<NT>();
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(k_int8_skinny<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             s_smem<NT>()) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, k_int8_skinny<NT>, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      n = 0;
+      return 0;
     }
     known[dev][split] = n > 0 ? n : -1;
   }
   return known[dev][split];
 }
 
+// How a launch of the few-row kernel looks, and about how many cycles it takes.
+struct Plan {
+  long long cycles;
+  int split, ctas;
+};
+
+// Cycles, from measurements at 1.9 GHz: a K step of a CTA costs its MMAs (2 NT) or
+// the fetch of its operands at 44 bytes a cycle, all weights together at least
+// 3440 bytes a cycle (HBM); 6000 go to launch, fill and last tile, and joining a
+// shared K axis costs 1500 and 8 per token. (5120 x 5120, one row: 8 us; 128 rows:
+// 15 us; 1024 x 5120, 512 rows: 9 us against 20 us by pairs of CTAs.)
 template <int NT>
-cudaError_t run_skinny(int M, int N, int K, const void* a, const void* w, const Out& out,
-                       int* err, cudaStream_t st) {
+Plan plan_skinny(int M, int N, int K) {
+  Plan p;
+  const int kb_n = (K + BKB - 1) / BKB, sms = num_sms();
+  const long long tiles = (long long)((N + BM - 1) / BM) * ((M + NT - 1) / NT);
+  // As many CTAs share a tile's K axis as leave every tile a cluster that runs at
+  // once, each with two K steps at least; with more tiles a CTA takes whole ones.
+  int split = tiles < sms ? (int)(sms / tiles) : 1;
+  if (split > kb_n / 2) split = kb_n / 2;
+  if (split > kMaxSplit) split = kMaxSplit;
+  while (split > 1 && clusters_at_once<NT>(split) < tiles) --split;
+  if (split < 1) split = 1;
+  p.split = split;
+  p.ctas = split > 1 ? (int)tiles * split : (int)(tiles < sms ? tiles : sms);
+  const long long step = 2 * NT > (A_STAGE + NT * BKB) / 44 ? 2 * NT : (A_STAGE + NT * BKB) / 44;
+  const long long run = (tiles * split + sms - 1) / sms * ((kb_n + split - 1) / split) * step;
+  const long long bytes = (long long)N * K / 3440;
+  p.cycles = (run > bytes ? run : bytes) + 6000 + (split > 1 ? 1500 + 8 * NT : 0);
+  return p;
+}
+
+// The same for the pair kernel: 700 cycles a K step and wave, 8000 around.
+long long pair_cycles(int M, int N, int K) {
+  const long long tiles =
+      (long long)((M + 2 * BM - 1) / (2 * BM)) * ((N + 255) / 256), pairs = num_sms() / 2;
+  const long long run = (tiles + pairs - 1) / pairs * ((K + BKB - 1) / BKB) * 700;
+  const long long bytes = (long long)N * K / 3440;
+  return (run > bytes ? run : bytes) + 8000;
+}
+
+template <int NT>
+cudaError_t run_skinny(const Plan& p, int M, int N, int K, const void* a, const void* w,
+                       const Out& out, int* err, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(k_int8_skinny<NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, s_smem<NT>());
   if (e != cudaSuccess) return e;
   CUtensorMap ta, tw;
   if (!tmap_codes(&ta, a, M, K, NT) || !tmap_codes(&tw, w, N, K, BM)) return cudaErrorInvalidValue;
-  const int tiles = (N + BM - 1) / BM, kb_n = (K + BKB - 1) / BKB;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.ctas);
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = s_smem<NT>();
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  // As many CTAs share a tile's K axis as leave every tile a cluster that runs at
-  // once, each with two K steps at least; with more tiles a CTA takes whole ones.
-  int split = num_sms() / tiles;
-  if (split > kb_n / 2) split = kb_n / 2;
-  if (split > 8) split = 8;
-  for (;; --split) {
-    if (split < 1) split = 1;
-    at[0].val.clusterDim.x = (unsigned)split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    if (split == 1 || clusters_at_once<NT>(cfg, split) >= tiles) break;
-  }
-  const int ctas = split > 1 ? tiles * split : (tiles < num_sms() ? tiles : num_sms());
-  cfg.gridDim = dim3((unsigned)ctas);
-  return cudaLaunchKernelEx(&cfg, k_int8_skinny<NT>, tw, ta, M, N, kb_n, split, out, err);
+  return cudaLaunchKernelEx(&cfg, k_int8_skinny<NT>, tw, ta, M, N, (K + BKB - 1) / BKB, p.split,
+                            out, err);
 }
 
 }  // namespace
@@ -640,10 +734,19 @@ cudaError_t launch_matmul_int8(int M, int N, int K, const void* a, const float* 
                                const void* w, const float* w_scale, h3_type out_type, void* out,
                                int64_t out_stride, int* err, cudaStream_t st) {
   const Out o{out, out_stride, (int)out_type, a_scale, w_scale};
-  if (M <= 16) return run_skinny<16>(M, N, K, a, w, o, err, st);
-  if (M <= 32) return run_skinny<32>(M, N, K, a, w, o, err, st);
-  if (M <= 64) return run_skinny<64>(M, N, K, a, w, o, err, st);
-  if (M <= 128) return run_skinny<128>(M, N, K, a, w, o, err, st);
+  // The narrowest token tile that holds all rows, or tiles of 128 of them; pairs
+  // of CTAs where they are estimated to be faster.
+#define H3_FEW(NT)                                                              \
+  {                                                                             \
+    const Plan p = plan_skinny<NT>(M, N, K);                                    \
+    if (M <= 128 || p.cycles < pair_cycles(M, N, K))                            \
+      return run_skinny<NT>(p, M, N, K, a, w, o, err, st);                      \
+  }
+  if (M <= 16) H3_FEW(16)
+  else if (M <= 32) H3_FEW(32)
+  else if (M <= 64) H3_FEW(64)
+  else if (M <= 2048) H3_FEW(128)
+#undef H3_FEW
   return run_pair<256>(M, N, K, a, w, o, err, st);
 }
 

@@ -29,7 +29,9 @@ def _formula(x):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,K", [(1, 16), (3, 512), (9, 528), (5, 2048), (1, 5120), (7, 14336),
-                                    (2, 32784), (2, 65552), (1, 131056), (0, 64)])
+                                    (2, 32784), (2, 65552), (1, 131056), (0, 64), (700, 1024),
+                                    (700, 4096), (650, 5120), (601, 14336), (599, 20480),
+                                    (595, 65536)])
 def test_codes_and_scales_bit_for_bit(dtype, rows, K):
     """Every group size and register count of the kernel, and its two-pass form."""
     x = (torch.randn(rows, K, generator=gen(K + rows), device=DEV) * 3).to(dtype)
@@ -105,7 +107,9 @@ def _product(M, N, K, dtype, seed=0, stride=None, a=None, w=None):
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 16), (1, 128, 128), (2, 129, 144), (15, 1000, 1040), (16, 14336, 5120), (17, 255, 2064),
     (32, 640, 14336), (33, 32003, 256), (64, 5376, 1024), (65, 100, 4096), (128, 384, 2560),
-    (129, 256, 128), (256, 257, 528), (333, 1003, 5376), (700, 1, 64), (1025, 2048, 1040)])
+    (129, 256, 128), (256, 257, 528), (333, 1003, 5376), (700, 1, 64), (1025, 2048, 1040),
+    (130, 1500, 5120), (513, 300, 5120), (1030, 129, 2064), (2048, 640, 1296), (2049, 3000, 272),
+    (300, 19000, 512)])
 def test_product(M, N, K, dtype):
     _product(M, N, K, dtype)
 
