@@ -25,11 +25,10 @@ template <h3_type T>
 __device__ __forceinline__ void store_codes(const uint4& u, const RowScale& s, void* dst) {
   float v[Vec<T>::N];
   unpack<T>(u, v);
-  const uint2 c = codes_of<T == H3_F32>(v, s);
   if constexpr (T == H3_F32)
-    *reinterpret_cast<uint32_t*>(dst) = c.x;
+    *reinterpret_cast<uint32_t*>(dst) = codes_of_4(v, s);
   else
-    *reinterpret_cast<uint2*>(dst) = c;
+    *reinterpret_cast<uint2*>(dst) = codes_of_8(v, s);
 }
 
 // The maximum over the block's threads, or over each warp's alone.
@@ -84,7 +83,7 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G == 0 ? 1024 : G)
   }
   float scale = m / 127.f;
   if (scale == 0.f) scale = 1.f;  // zeros, or a maximum below the smallest scale
-  const RowScale s = row_scale(scale);
+  const RowScale s = row_scale<T>(scale);
   if (t == 0) scales[row] = s.scale;
   if constexpr (NV > 0) {
 #pragma unroll

@@ -51,6 +51,7 @@ struct BlockScale {
   bool again;  // earlier codes change
 };
 
+template <h3_type T>
 __device__ __forceinline__ BlockScale block_scale(float peak, float old, bool held,
                                                   float* stored, bool writer) {
   BlockScale b;
@@ -61,7 +62,7 @@ __device__ __forceinline__ BlockScale block_scale(float peak, float old, bool he
   if (writer) *stored = scale;
   b.old = old;
   b.zero = bad || scale == 0.f;
-  b.s = row_scale(b.zero ? 1.f : scale);
+  b.s = row_scale<T>(b.zero ? 1.f : scale);
   b.again = held && (bad || scale > old);
   return b;
 }
@@ -80,11 +81,12 @@ template <h3_type T>
 __device__ __forceinline__ uint2 vec_codes(const uint4& u, const BlockScale& b) {
   float f[8];
   unpack<T>(u, f);
-  return codes_of(f, b.s);
+  return codes_of_8(f, b.s);
 }
 
 template <h3_type T, int D, int BT>
-__global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
+__global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
+    k_kv_store(const StoreArgs a) {
   constexpr int RV = D / 8;                 // 16-byte vectors per token
   constexpr int WR = BT / 4;                // words of four slots per channel
   constexpr int GROUPS = WR * RV;           // (word, vector) pairs
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv_store(const StoreArgs a) {
     float m = 0.f;
 #pragma unroll
     for (int k = 0; k < kStoreThreads / 32; ++k) m = max_nan(m, part[w][k]);
-    bs[w] = block_scale(m, old[w], held > 0, a.scales[w] + at, t == 0);
+    bs[w] = block_scale<T>(m, old[w], held > 0, a.scales[w] + at, t == 0);
   }
   uint8_t* kc = a.codes[0] + at * (BT * D);
   uint8_t* vc = a.codes[1] + at * (BT * D);

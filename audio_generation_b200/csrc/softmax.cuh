@@ -62,6 +62,12 @@ __device__ __forceinline__ void exp2_cubic2(uint64_t x2, const Cubic& c, float& 
   p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
 }
 
+__device__ __forceinline__ float fma_01(float a, float b, float c) {  // limited to [0, 1]
+  float d;
+  asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
