@@ -244,10 +244,13 @@ __global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
 // order, cut into equal ranges, one per thread block, as many as run at once:
 // lengths may differ as they like, every thread block streams the same number
 // of bytes, and its ring of stages runs on from one sequence to the next. A pair
-// (sequence, head group) that lies in one range is finished there; the parts of
-// one that is cut go to the workspace and a second kernel joins them. At most
-// the first and the last pair of a range are cut, so the workspace does not grow
-// with the sequences.
+// (sequence, head group) counts kPairUnits more than it has, since beginning and
+// ending one costs a thread block about as much as three units (40 sequences of
+// 500 to 24000 tokens, 40 over 8 heads: the last thread block ends after 84 us
+// without this, most after 66). A pair that lies in one range is finished there;
+// the parts of one that is cut go to the workspace and a second kernel joins
+// them. At most the first and the last pair of a range are cut, so the workspace
+// does not grow with the sequences.
 //
 // A thread block has one producer warp, which streams cache blocks into shared-
 // memory stages with bulk copies, and four consumer warps: two pairs take the
@@ -273,7 +276,8 @@ __global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
 constexpr int kAttnThreads = 160, kConsumers = 4;
 constexpr int kMaxCols = 2;     // column tiles of eight heads a warp takes at most
 constexpr int kListSize = 64;   // entries of the producer's list, two batches of 32
-constexpr int kMinUnits = 2;    // cache blocks a thread block takes at least
+constexpr int kMinUnits = 2;    // cache blocks a thread block takes at least, about
+constexpr int kPairUnits = 3;
 
 template <int D, int BT, int NC>  // NC column tiles: ROWS = 8 NC query heads per pass
 struct Ring {
@@ -376,6 +380,13 @@ __device__ __forceinline__ int length_of(const AttnArgs& a, int seq, int block_t
   return len < 0 ? 0 : (int)most;
 }
 
+// Division of values that hardly ever need 64 bits (which take a hundred
+// instructions).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
 }
@@ -396,18 +407,25 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
   __shared__ Entry list[kListSize];
   __shared__ float2 stat[kConsumers][ROWS];
   __shared__ long long warp_sum[kAttnThreads / 32];
-  __shared__ long long s_before;  // cache blocks before the range's first sequence
-  __shared__ int s_seq, s_abort;
+  __shared__ int4 s_begin;       // the range's first unit: {sequence, head group, page, 0}
+  __shared__ long long s_cut[2];  // its ends among all units
+  __shared__ long long s_pair_at; // where its first pair begins in the weights
+  __shared__ int s_abort;
 
   asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may be set up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int heads = a.kv_heads * a.row_groups, q_heads = a.kv_heads * a.group;
 
   // ---- this thread block's range of units: a scan over the sequences' lengths
+  auto pages_of = [&](int s) { return (length_of(a, s, BT) + BT - 1) / BT; };
+  constexpr int kCount = 40;  // cache blocks in the low bits, sequences that have any above
   const int per = (a.n_seq + kAttnThreads - 1) / kAttnThreads;
   const int seq0 = min(a.n_seq, (int)threadIdx.x * per), seq1 = min(a.n_seq, seq0 + per);
   long long mine = 0;
-  for (int s = seq0; s < seq1; ++s) mine += (length_of(a, s, BT) + BT - 1) / BT;
+  for (int s = seq0; s < seq1; ++s) {
+    const int n = pages_of(s);
+    if (n > 0) mine += (1ll << kCount) + n;
+  }
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -430,44 +448,58 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
-  before += upto - mine;  // cache blocks of the sequences before seq0
-  const long long units = total * heads;
+  before += upto - mine;  // of the sequences before seq0
+  auto units_in = [&](long long sum) { return (sum & ((1ll << kCount) - 1)) * heads; };
+  auto weight_of = [&](long long sum) {
+    return units_in(sum) + (sum >> kCount) * kPairUnits * heads;
+  };
+  const long long units = units_in(total), weight = weight_of(total);
   long long ranges = (units + kMinUnits - 1) / kMinUnits;
   if (ranges > gridDim.x) ranges = gridDim.x;
   const bool idle = (long long)blockIdx.x >= ranges;
-  const long long u0 = idle ? 0 : units * blockIdx.x / ranges;
-  const long long u1 = idle ? 0 : units * (blockIdx.x + 1) / ranges;
-  if (!idle && u0 >= before * heads && u0 < (before + mine) * heads) {
-    int s = seq0;
-    long long at = before;
-    for (;; ++s) {
-      const int pages = (length_of(a, s, BT) + BT - 1) / BT;
-      if (u0 < (at + pages) * heads) break;
-      at += pages;
+  if (!idle) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const long long at = quotient(weight * (blockIdx.x + e), ranges);
+      if (at == weight && threadIdx.x == 0) s_cut[e] = units;
+      if (at < weight_of(before) || at >= weight_of(before + mine)) continue;
+      // this thread's sequences hold the cut
+      long long sum = before;
+      for (int s = seq0;; ++s) {
+        const int n = pages_of(s);
+        if (n == 0) continue;
+        const long long in = at - weight_of(sum);
+        if (in < (long long)heads * (n + kPairUnits)) {
+          const int h = (int)quotient(in, n + kPairUnits);
+          const int p = max(0, (int)(in - (long long)h * (n + kPairUnits)) - kPairUnits);
+          s_cut[e] = units_in(sum) + (long long)h * n + p;
+          if (e == 0) {
+            s_begin = make_int4(s, h, p, 0);
+            s_pair_at = weight_of(sum) + (long long)h * (n + kPairUnits);
+          }
+          break;
+        }
+        sum += (1ll << kCount) + n;
+      }
     }
-    s_seq = s;
-    s_before = at;
   }
   // sequences with nothing cached get zeros
   for (int s = blockIdx.x; s < a.n_seq; s += gridDim.x)
     if (length_of(a, s, BT) == 0)
       for (int i = threadIdx.x; i < q_heads * D; i += kAttnThreads) a.o[s * a.o_stride + i] = 0;
-  if (idle) {
+  __syncthreads();
+  const long long u0 = idle ? 0 : s_cut[0], u1 = idle ? 0 : s_cut[1];
+  if (u0 == u1) {
     if (threadIdx.x == 0) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
     return;
   }
-  __syncthreads();
-  int seq = s_seq;
+  int seq = s_begin.x, hg = s_begin.y, page = s_begin.z;
   int len = length_of(a, seq, BT), pages = (len + BT - 1) / BT;
-  int hg, page;
-  {
-    const long long in = u0 - s_before * heads;
-    hg = (int)(in / pages);
-    page = (int)(in - (long long)hg * pages);
-  }
+  long long pair_at = s_pair_at;
   const int n_units = (int)(u1 - u0);  // at most 2^31: a range is a fraction of the pool
   // on to the next (sequence, head group)
   auto next_pair = [&]() {
+    pair_at += pages + kPairUnits;
     page = 0;
     if (++hg < heads) return;
     hg = 0;
@@ -815,9 +847,9 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
       }
       each([&](float& x, int at) { sums[at] = x; });
       if (!whole && begins) {
-        // the pair's last unit, the range it is in, and so the number of parts
-        const long long last = u0 + unit + pages - 1;
-        const int to = (int)(((last + 1) * ranges - 1) / units);
+        // the range that holds the pair's end, and so the number of parts
+        const long long end = pair_at + pages + kPairUnits;
+        const int to = (int)quotient(end * ranges - 1, weight);
         if (lane == 0) a.cut[blockIdx.x] = make_int4(seq, hg, to - (int)blockIdx.x + 1, 0);
         have_cut = true;
       }
