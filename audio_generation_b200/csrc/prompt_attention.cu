@@ -557,7 +557,7 @@ h3_status build_prompts(h3_prompts* p, const int32_t* offsets, int n_prompts) {
   long long count = 0;
   for (int i = 0; i < n_prompts; ++i)
     count += ((long long)offsets[i + 1] - offsets[i] + 2 * P - 1) / (2 * P);
-  if (count * p->kv_heads > 0x7fffffffLL) return H3_ERR_SHAPE;
+  if (count * p->kv_heads > 0x7fff0000LL) return H3_ERR_SHAPE;  // rounds of the grid fit an int
   p->n_items = (int)count;
   if (count == 0) return H3_OK;
   std::vector<int4> items;

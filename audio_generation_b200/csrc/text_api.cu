@@ -36,6 +36,9 @@ inline bool row_stride_ok(int64_t stride, int64_t width) {
   return stride >= width && stride % 8 == 0 && stride < (1ll << 38);
 }
 
+// Positive and finite, in log2 units too.
+inline bool scale_ok(float scale) { return scale > 0.f && isfinite(scale * 1.4426950408889634f); }
+
 inline bool known_type(h3_type t) { return t == H3_BF16 || t == H3_F16 || t == H3_F32; }
 
 h3_status check_cache(const h3_kv_cache* c) {
@@ -158,7 +161,7 @@ h3_status h3_prompt_attention(h3_prompts_t p, h3_type type, const void* q, int64
                               const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                               float scale, void* o, int64_t o_stride, h3_stream_t stream) {
   if (!p || (type != H3_BF16 && type != H3_F16)) return H3_ERR_ARG;
-  if (!(scale > 0.f) || !isfinite(scale)) return H3_ERR_ARG;
+  if (!scale_ok(scale)) return H3_ERR_ARG;
   const int64_t qw = (int64_t)p->q_heads * p->head_dim, kw = (int64_t)p->kv_heads * p->head_dim;
   if (!row_stride_ok(q_stride, qw) || !row_stride_ok(o_stride, qw) ||
       !row_stride_ok(k_stride, kw) || !row_stride_ok(v_stride, kw))
@@ -218,8 +221,7 @@ h3_status h3_cache_attention(const h3_kv_cache* cache, int n_seq, int q_heads,
                              int64_t o_stride, void* ws, size_t ws_bytes, h3_stream_t stream) {
   h3_status rc = check_cache(cache);
   if (rc != H3_OK) return rc;
-  if (n_seq < 0 || q_heads <= 0 || (type != H3_BF16 && type != H3_F16) || !(scale > 0.f) ||
-      !isfinite(scale))
+  if (n_seq < 0 || q_heads <= 0 || (type != H3_BF16 && type != H3_F16) || !scale_ok(scale))
     return H3_ERR_ARG;
   if ((rc = check_table(cache, table_width)) != H3_OK) return rc;
   const int64_t w = (int64_t)q_heads * cache->head_dim;

@@ -558,17 +558,38 @@ def _type(t) -> int:
     return code
 
 
+def _current_device() -> int:
+    """The current device's index, -1 before CUDA has been used."""
+    import torch
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+
+
+def _dev_ptr(t, device: int, where: str) -> Optional[int]:
+    """Address of a tensor that has to be on the current device (an int or None
+    as it is): a host tensor's address, or another device's, is refused here,
+    where the kernel would fault on it."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.get_device() != device:
+        raise H3Error(H3_ERR_ARG, f"{where}: tensor on {t.device}, current device {device}")
+    return t.data_ptr()
+
+
 def h3_quantize_int8_rows(dtype, rows: int, K: int, x, x_stride: int, codes, scales,
                           stream=None) -> None:
-    _check(lib().h3_quantize_int8_rows(_type(dtype), rows, K, _ptr(x), x_stride, _ptr(codes),
-                                       _ptr(scales), _stream(stream)), "h3_quantize_int8_rows")
+    d, w = _current_device(), "h3_quantize_int8_rows"
+    _check(lib().h3_quantize_int8_rows(_type(dtype), rows, K, _dev_ptr(x, d, w), x_stride,
+                                       _dev_ptr(codes, d, w), _dev_ptr(scales, d, w),
+                                       _stream(stream)), w)
 
 
 def h3_matmul_int8(M: int, N: int, K: int, a_codes, a_scales, w_codes, w_scales, out_dtype, out,
                    out_stride: int, stream=None) -> None:
-    _check(lib().h3_matmul_int8(M, N, K, _ptr(a_codes), _ptr(a_scales), _ptr(w_codes),
-                                _ptr(w_scales), _type(out_dtype), _ptr(out), out_stride,
-                                _stream(stream)), "h3_matmul_int8")
+    d, w = _current_device(), "h3_matmul_int8"
+    _check(lib().h3_matmul_int8(M, N, K, _dev_ptr(a_codes, d, w), _dev_ptr(a_scales, d, w),
+                                _dev_ptr(w_codes, d, w), _dev_ptr(w_scales, d, w),
+                                _type(out_dtype), _dev_ptr(out, d, w), out_stride,
+                                _stream(stream)), w)
 
 
 def h3_text_error() -> int:
@@ -612,9 +633,10 @@ def h3_prompts_destroy(prompts: Prompts) -> None:
 
 def h3_prompt_attention(prompts: Prompts, dtype, q, q_stride: int, k, k_stride: int, v,
                         v_stride: int, scale: float, o, o_stride: int, stream=None) -> None:
-    _check(lib().h3_prompt_attention(prompts.handle, _type(dtype), _ptr(q), q_stride, _ptr(k),
-                                     k_stride, _ptr(v), v_stride, scale, _ptr(o), o_stride,
-                                     _stream(stream)), "h3_prompt_attention")
+    d, w = _current_device(), "h3_prompt_attention"
+    _check(lib().h3_prompt_attention(prompts.handle, _type(dtype), _dev_ptr(q, d, w), q_stride,
+                                     _dev_ptr(k, d, w), k_stride, _dev_ptr(v, d, w), v_stride,
+                                     scale, _dev_ptr(o, d, w), o_stride, _stream(stream)), w)
 
 
 def make_kv_cache(k_codes, v_codes, k_scales, v_scales) -> h3_kv_cache:
@@ -623,8 +645,9 @@ def make_kv_cache(k_codes, v_codes, k_scales, v_scales) -> h3_kv_cache:
     n_blocks, kv_heads, block_tokens, head_dim = k_codes.shape
     if v_codes.shape != (n_blocks, kv_heads, head_dim, block_tokens):
         raise H3Error(H3_ERR_SHAPE, "make_kv_cache")
-    return h3_kv_cache(n_blocks, block_tokens, kv_heads, head_dim, k_codes.data_ptr(),
-                       v_codes.data_ptr(), _ptr(k_scales), _ptr(v_scales))
+    d, w = _current_device(), "make_kv_cache"
+    return h3_kv_cache(n_blocks, block_tokens, kv_heads, head_dim, _dev_ptr(k_codes, d, w),
+                       _dev_ptr(v_codes, d, w), _dev_ptr(k_scales, d, w), _dev_ptr(v_scales, d, w))
 
 
 def h3_kv_cache_store(cache: h3_kv_cache, n_seq: int, max_new: int, block_table,
@@ -632,11 +655,13 @@ def h3_kv_cache_store(cache: h3_kv_cache, n_seq: int, max_new: int, block_table,
                       v_stride: int, rows: Optional[int] = None, stream=None) -> None:
     """rows: the rows of k and v (from k's first dimension by default)."""
     if rows is None:
-        rows = int(k.shape[0])
-    _check(lib().h3_kv_cache_store(ctypes.byref(cache), n_seq, max_new, _ptr(block_table),
-                                   table_width, _ptr(lengths), _ptr(offsets), _type(dtype), rows,
-                                   _ptr(k), k_stride, _ptr(v), v_stride, _stream(stream)),
-           "h3_kv_cache_store")
+        rows = k.shape[0]
+    d, w = _current_device(), "h3_kv_cache_store"
+    _check(lib().h3_kv_cache_store(ctypes.byref(cache), n_seq, max_new,
+                                   _dev_ptr(block_table, d, w), table_width,
+                                   _dev_ptr(lengths, d, w), _dev_ptr(offsets, d, w), _type(dtype),
+                                   rows, _dev_ptr(k, d, w), k_stride, _dev_ptr(v, d, w), v_stride,
+                                   _stream(stream)), w)
 
 
 def h3_cache_attention_workspace_size(cache: h3_kv_cache, n_seq: int, q_heads: int,
@@ -648,7 +673,9 @@ def h3_cache_attention_workspace_size(cache: h3_kv_cache, n_seq: int, q_heads: i
 def h3_cache_attention(cache: h3_kv_cache, n_seq: int, q_heads: int, block_table,
                        table_width: int, lengths, dtype, q, q_stride: int, scale: float, o,
                        o_stride: int, ws, ws_bytes: int, stream=None) -> None:
-    _check(lib().h3_cache_attention(ctypes.byref(cache), n_seq, q_heads, _ptr(block_table),
-                                    table_width, _ptr(lengths), _type(dtype), _ptr(q), q_stride,
-                                    scale, _ptr(o), o_stride, _ptr(ws), ws_bytes,
-                                    _stream(stream)), "h3_cache_attention")
+    d, w = _current_device(), "h3_cache_attention"
+    _check(lib().h3_cache_attention(ctypes.byref(cache), n_seq, q_heads,
+                                    _dev_ptr(block_table, d, w), table_width,
+                                    _dev_ptr(lengths, d, w), _type(dtype), _dev_ptr(q, d, w),
+                                    q_stride, scale, _dev_ptr(o, d, w), o_stride,
+                                    _dev_ptr(ws, d, w), ws_bytes, _stream(stream)), w)

@@ -20,13 +20,15 @@
  *  - Ownership: the caller owns every buffer. Pointers named in structs and
  *    arguments are DEVICE pointers unless the name ends in `_host`. The library
  *    allocates device memory only in h3_layout_prepare (small per-layout tables,
- *    released by h3_layout_destroy).
+ *    released by h3_layout_destroy) and h3_prompts_prepare (a work list, released
+ *    by h3_prompts_destroy).
  *  - Types: "bf16" buffers hold IEEE bfloat16 values (2 bytes each); "f32"
  *    buffers hold float; index buffers hold int32_t.
  *  - Matrices are row-major [out, in] (K-major for the tensor cores).
  *  - Streams: `stream` is a cudaStream_t passed as void* (NULL = legacy
- *    default stream). Every call except h3_layout_prepare, h3_layout_error and
- *    h3_layout_export only enqueues work and returns; argument, shape and
+ *    default stream). Every call except h3_layout_prepare, h3_layout_error,
+ *    h3_layout_export and the ones that take no stream only enqueues work and
+ *    returns; argument, shape and
  *    alignment errors are returned synchronously before anything is launched.
  *  - Alignment: every device pointer must be 16-byte aligned.
  *  - Shapes: head_dim == 128; hidden % 256 == 0 and <= 6144; heads even;
@@ -633,14 +635,14 @@ typedef struct {
  * holds earlier tokens and that is larger; code = value / scale rounded to
  * nearest, ties to even (the exact quotient decides). If the scale of a block
  * with earlier tokens grows, their codes are rounded again to the same values
- * under the new scale. A block of zeros has scale 0. An infinity or a NaN marks its block and kv head:
- * scale NaN, codes 0 (attention over it gives NaN). max_new: the largest number
- * of new tokens of one sequence; `rows`: the rows of k and v. A sequence whose
- * lengths or offsets are negative, whose new tokens are more than max_new, leave
- * `rows` or do not fit table_width blocks is not stored, nor is a token whose
- * table entry names no block: both record an error (h3_text_error,
- * H3_ERR_LAYOUT). A block that is written must be in one sequence's table only.
- * Enqueues. */
+ * under the new scale. A block of zeros has scale 0. An infinity or a NaN marks
+ * its block and kv head: scale NaN, codes 0 (attention over it gives NaN).
+ * max_new: the largest number of new tokens of one sequence; `rows`: the rows of
+ * k and v. A sequence whose lengths or offsets are negative, whose new tokens are
+ * more than max_new, leave `rows` or do not fit table_width blocks is not stored,
+ * nor is a token whose table entry names no block: both record an error
+ * (h3_text_error, H3_ERR_LAYOUT). A block that is written must be in one
+ * sequence's table only, and there once. Enqueues. */
 H3_API h3_status h3_kv_cache_store(const h3_kv_cache* cache, int n_seq, int max_new,
                                    const int32_t* block_table, int table_width,
                                    const int32_t* lengths, const int32_t* offsets, h3_type type,

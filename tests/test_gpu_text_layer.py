@@ -206,3 +206,34 @@ print("captured")
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
                        timeout=120)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_host_tensors_are_refused():
+    """Addresses that a kernel would fault on do not reach one: in every place of
+    every call of the binding."""
+    g = dict(device=DEV)
+    bf = torch.zeros(4, 4, 64, dtype=BF, **g)
+    codes, scales = torch.zeros(4, 256, dtype=torch.int8, **g), torch.ones(4, **g)
+    kc, vc = torch.zeros(2, 2, 32, 64, dtype=torch.int8, **g), torch.zeros(2, 2, 64, 32,
+                                                                          dtype=torch.int8, **g)
+    ks = torch.zeros(2, 2, **g)
+    i32 = torch.zeros(4, dtype=torch.int32, **g)
+    p = h3.h3_prompts_prepare([0, 4], 4, 2, 64)
+    cache = h3.make_kv_cache(kc, vc, ks, ks)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, **g)
+    calls = [
+        (h3.h3_quantize_int8_rows, [BF, 4, 256, bf, 256, codes, scales]),
+        (h3.h3_matmul_int8, [4, 4, 256, codes, scales, codes, scales, BF, bf, 4]),
+        (h3.h3_prompt_attention, [p, BF, bf, 256, bf, 128, bf, 128, 0.1, bf.clone(), 256]),
+        (h3.make_kv_cache, [kc, vc, ks, ks]),
+        (h3.h3_kv_cache_store, [cache, 1, 4, i32, 1, i32, i32, BF, bf, 128, bf, 128]),
+        (h3.h3_cache_attention, [cache, 1, 4, i32, 1, i32, BF, bf, 256, 0.1, bf.clone(), 256, ws,
+                                 1 << 20])]
+    for fn, args in calls:
+        for i, a in enumerate(args):
+            if not isinstance(a, torch.Tensor):
+                continue
+            with pytest.raises(h3.H3Error) as e:
+                fn(*args[:i], a.cpu(), *args[i + 1:])
+            assert e.value.status == h3.H3_ERR_ARG
+    torch.cuda.synchronize()

@@ -152,6 +152,19 @@ def test_cache_attention_workspace_size():
     # ranges per SM whatever the number of sequences
     assert 0 < size(c, 1, 8, 1) < size(c, 2, 8, 40) < size(c, 40, 8, 375)
     assert size(c, 40, 8, 375) == size(c, 4000, 8, 375) <= 3 * 148 * (2 * 16 * (128 * 4 + 8) + 16)
-    with pytest.raises(h3.H3Error):
+    with pytest.raises(h3.H3Error) as e:
         import torch
         h3.make_kv_cache(torch.zeros(1, 1, 32, 64), torch.zeros(1, 1, 32, 64), None, None)
+    assert e.value.status == h3.H3_ERR_SHAPE
+
+
+def test_binding_refuses_values_of_the_wrong_device():
+    """Where CUDA is in use a host tensor is refused by the binding; where it is not
+    (device -1 on both sides) the address goes to the library's own checks."""
+    import torch
+    x = torch.zeros(64)
+    with pytest.raises(h3.H3Error) as e:
+        h3._dev_ptr(x, 0, "somewhere")
+    assert e.value.status == h3.H3_ERR_ARG and "somewhere" in str(e.value)
+    assert h3._dev_ptr(x, -1, "x") == x.data_ptr()
+    assert h3._dev_ptr(None, 0, "x") is None and h3._dev_ptr(4096, 0, "x") == 4096
