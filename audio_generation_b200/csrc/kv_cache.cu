@@ -723,8 +723,10 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
       // weights, turned so that a thread has head g's tokens 2 t, 2 t + 1 of a block
       const float ratio = en.vs == 0.f ? 0.f : en.vs / v_top;
       uint32_t pb[NC][NB];
+      float zeros[NC][2];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
+        zeros[c][0] = zeros[c][1] = 0.f;
         float sub[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k)  // a head that has seen no token has maximum -inf: weights 0
@@ -733,12 +735,34 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
         for (int b = 0; b < NB / 2; ++b) {
           float p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = exp2_mufu(sc[c][b][e] + sub[e & 1]);
-            l_run[c][e & 1] += p[e];
+          for (int e = 0; e < 4; ++e) p[e] = exp2_mufu(sc[c][b][e] + sub[e & 1]);
+          if (ratio == 0.f) {  // a block of zeros: its weights count, its values do not
+#pragma unroll
+            for (int e = 0; e < 4; ++e) zeros[c][e & 1] += p[e];
           }
           pb[c][2 * b] = transpose8(pack_f16x2(p[0] * ratio, p[1] * ratio));
           pb[c][2 * b + 1] = transpose8(pack_f16x2(p[2] * ratio, p[3] * ratio));
+        }
+      }
+      // The weights' sum from the rounded weights, as one more row of values that are
+      // all 1: what rounding moves in the sums it then moves in their divisor too.
+      const float back = ratio == 0.f ? 0.f : 1.f / ratio;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < NB / 2; ++k) mma_f16(sum, ones, pb[c][2 * k], pb[c][2 * k + 1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          l_run[c][k] = fmaf(sum[k], back, l_run[c][k]);
+          if (ratio == 0.f) {
+            float z = zeros[c][k];
+            z += __shfl_xor_sync(0xffffffffu, z, 4);
+            z += __shfl_xor_sync(0xffffffffu, z, 8);
+            z += __shfl_xor_sync(0xffffffffu, z, 16);
+            l_run[c][k] += z;
+          }
         }
       }
       const uint8_t* vrow = vb + g * BT + half * HT + (HT / 4) * t;
@@ -775,9 +799,6 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        l_run[c][k] += __shfl_xor_sync(0xffffffffu, l_run[c][k], 4);
-        l_run[c][k] += __shfl_xor_sync(0xffffffffu, l_run[c][k], 8);
-        l_run[c][k] += __shfl_xor_sync(0xffffffffu, l_run[c][k], 16);
         if (g == 0) stat[warp][8 * c + 2 * t + k] = make_float2(m_run[c][k], l_run[c][k]);
       }
     consumers_sync();
