@@ -30,7 +30,9 @@ __device__ __forceinline__ int block_of(const int32_t* table, int width, int seq
 // eight channels of four neighbouring slots, so that V's codes turn in
 // registers to words of four tokens; these pass through shared memory (with the
 // word's place XORed by the channel, against bank conflicts), so that global
-// stores run along the tokens.
+// stores run along the tokens. 18400 tokens of 8 heads x 128 (113 MB in and out):
+// 34.5 us, bound by instructions (60 % of the issue slots); one token of each of 48
+// sequences: 4.5 us.
 constexpr int kStoreThreads = 256;
 
 struct StoreArgs {
@@ -272,7 +274,8 @@ __global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
 // 16-byte pieces of a K row as four k-quads, since the order of the channels in a
 // product is free, and the tokens are assigned to rows so that its V operand is
 // one contiguous piece of a transposed V row; the weights turn between the two
-// layouts by 8 x 8 transposes across the warp.
+// layouts by 8 x 8 transposes across the warp. 40 sequences of 500 to 24000 tokens,
+// 40 heads over 8 x 128 (423 MB): 77 us, 5.5 TB/s; one of 4001 tokens: 10.5 us.
 constexpr int kAttnThreads = 160, kConsumers = 4;
 constexpr int kMaxCols = 2;     // column tiles of eight heads a warp takes at most
 constexpr int kListSize = 64;   // entries of the producer's list, two batches of 32

@@ -574,8 +574,11 @@ h3_status build_prompts(h3_prompts* p, const int32_t* offsets, int n_prompts) {
     return H3_ERR_CUDA;
   }
   if (cudaMalloc(&p->items, count * sizeof(int4)) != cudaSuccess) return H3_ERR_CUDA;
+  // the copy may still be under way when cudaMemcpy returns, and a stream that
+  // does not follow the default one would not wait for it
   if (cudaMemcpy(p->items, items.data(), count * sizeof(int4), cudaMemcpyHostToDevice) !=
-      cudaSuccess) {
+          cudaSuccess ||
+      cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
     cudaFree(p->items);
     p->items = nullptr;
     return H3_ERR_CUDA;

@@ -85,7 +85,9 @@ h3_status h3_text_error(void) {
   int v = 0;
   if (cudaDeviceSynchronize() != cudaSuccess) return H3_ERR_CUDA;
   if (cudaMemcpy(&v, p, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return H3_ERR_CUDA;
-  if (v != 0 && cudaMemset(p, 0, 4) != cudaSuccess) return H3_ERR_CUDA;
+  // cleared for good before the caller launches anything more, on any stream
+  if (v != 0 && (cudaMemset(p, 0, 4) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess))
+    return H3_ERR_CUDA;
   return v == 0 ? H3_OK : v == H3_DEVERR_LAYOUT ? H3_ERR_LAYOUT : H3_ERR_TIMEOUT;
 }
 

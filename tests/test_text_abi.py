@@ -2,6 +2,8 @@
 host, before any device work (the pointers here are never dereferenced)."""
 
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -168,3 +170,15 @@ def test_binding_refuses_values_of_the_wrong_device():
     assert e.value.status == h3.H3_ERR_ARG and "somewhere" in str(e.value)
     assert h3._dev_ptr(x, -1, "x") == x.data_ptr()
     assert h3._dev_ptr(None, 0, "x") is None and h3._dev_ptr(4096, 0, "x") == 4096
+
+
+def test_prompt_attention_has_the_checked_cubic():
+    """The part of the exponentials on the FMA pipe: the same coefficients as in the
+    packed-sequence kernel, whose error bound is checked against float64."""
+    csrc = os.path.join(os.path.dirname(h3.__file__), "csrc")
+    values = []
+    for name in ("attention.cu", "prompt_attention.cu"):
+        src = open(os.path.join(csrc, name)).read()
+        values.append([re.search(r"\b%s\s*=\s*([\d.]+)f" % c, src).group(1)
+                       for c in ("kExpC3", "kExpC2", "kExpC1", "kExpC0", "kRoundMagic")])
+    assert values[0] == values[1]
