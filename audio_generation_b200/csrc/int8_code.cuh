@@ -145,6 +145,19 @@ __device__ __forceinline__ uint32_t code_again(int code, float from, float to, f
   return __float_as_uint(r);
 }
 
+// Two neighbouring 16-bit elements as floats.
+template <h3_type T>
+__device__ __forceinline__ void unpack_pair(uint32_t w, float& lo, float& hi) {
+  if constexpr (T == H3_BF16) {
+    lo = bf16lo(w);
+    hi = bf16hi(w);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    lo = f.x;
+    hi = f.y;
+  }
+}
+
 // 16 bytes of a row as floats: 8 elements of 2 bytes, or 4 of 4.
 template <h3_type T>
 struct Vec {
@@ -155,21 +168,19 @@ __device__ __forceinline__ void unpack(const uint4& u, float* v) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (T == H3_BF16) {
-      v[2 * i] = bf16lo(w[i]);
-      v[2 * i + 1] = bf16hi(w[i]);
-    } else if constexpr (T == H3_F16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-    } else {
-      v[i] = __uint_as_float(w[i]);
-    }
+    if constexpr (T == H3_F32) v[i] = __uint_as_float(w[i]);
+    else unpack_pair<T>(w[i], v[2 * i], v[2 * i + 1]);
   }
 }
 
+// The warp's largest magnitude, a NaN winning: the bits of floats >= 0 and of
+// positive NaNs are ordered as integers are (one instruction for the warp).
+__device__ __forceinline__ float warp_peak(float m) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7fffffffu));
+}
+
 // max(m, |elements|) of 16 bytes of a row, a NaN winning: 16-bit types by pairs in
-// their own type, where maxima are exact.
+// their own type, where maxima are exact (m with any sign until its value is taken).
 template <h3_type T>
 struct AbsMax;
 template <>
@@ -187,23 +198,21 @@ template <>
 struct AbsMax<H3_BF16> {
   uint32_t m = 0;
   __device__ __forceinline__ void one(uint32_t w) {
-    w &= 0x7fff7fffu;
-    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
   }
   __device__ __forceinline__ void add(const uint4& u) { one(u.x), one(u.y), one(u.z), one(u.w); }
-  __device__ __forceinline__ float value() const { return max_nan(bf16lo(m), bf16hi(m)); }
+  __device__ __forceinline__ float value() const { return max_nan(fabsf(bf16lo(m)), fabsf(bf16hi(m))); }
 };
 template <>
 struct AbsMax<H3_F16> {
   uint32_t m = 0;
   __device__ __forceinline__ void one(uint32_t w) {
-    w &= 0x7fff7fffu;
-    asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
+    asm("max.NaN.xorsign.abs.f16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
   }
   __device__ __forceinline__ void add(const uint4& u) { one(u.x), one(u.y), one(u.z), one(u.w); }
   __device__ __forceinline__ float value() const {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
-    return max_nan(f.x, f.y);
+    return max_nan(fabsf(f.x), fabsf(f.y));
   }
 };
 

@@ -34,16 +34,13 @@ __device__ __forceinline__ void store_codes(const uint4& u, const RowScale& s, v
 // The maximum over the block's threads, or over each warp's alone.
 template <bool BLOCK>
 __device__ __forceinline__ float group_max(float m) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = warp_peak(m);
   if constexpr (BLOCK) {
     __shared__ float part[32];
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
-    m = lane < warps ? part[lane] : 0.f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    m = warp_peak(lane < warps ? part[lane] : 0.f);
   }
   return m;
 }
@@ -98,8 +95,8 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G == 0 ? 1024 : G)
 // eight vectors a thread (four where there are few rows, so that a row's loads
 // are all in flight and little is done in turn), so that few threads idle. The
 // usual lengths have their block size built in: 14336 bf16 elements a row, 8192
-// rows, 57 us (now 54.5, 6.5 TB/s) against 62 us with the block size read at run time (and with seven
-// warps instead of eight, which leave an SM fewer).
+// rows, 57 us against 62 us with the block size read at run time (and with seven
+// warps instead of eight, which leave an SM fewer); now 53.3 us, 6.6 TB/s.
 template <h3_type T>
 cudaError_t quantize(int rows, int K, const void* x, int64_t stride_vec, void* codes,
                      float* scales, cudaStream_t st) {

@@ -30,9 +30,12 @@ __device__ __forceinline__ int block_of(const int32_t* table, int width, int seq
 // eight channels of four neighbouring slots, so that V's codes turn in
 // registers to words of four tokens; these pass through shared memory (with the
 // word's place XORed by the channel, against bank conflicts), so that global
-// stores run along the tokens. 18400 tokens of 8 heads x 128 (113 MB in and out):
-// 34.5 us, bound by instructions (60 % of the issue slots); one token of each of 48
-// sequences: 4.5 us.
+// stores run along the tokens. Where most pairs of a sequence and a block up to
+// max_new would be empty, a thread block finds its pair by a scan over the
+// sequences. 18400 tokens of 8 heads x 128 in 16 sequences (113 MB in and out):
+// 31 us (34 without the scan), six waves of one chain each (sequence, values, scale,
+// codes); two thread blocks per SM 37 us, four, whose registers spill, 35 us. One
+// token of each of 48 sequences: 4.3 us.
 constexpr int kStoreThreads = 256;
 
 struct StoreArgs {
@@ -41,9 +44,72 @@ struct StoreArgs {
   int64_t stride[2];
   uint8_t* codes[2];
   float* scales[2];
-  int n_blocks, kv_heads, width, max_new, rows, pages;
+  int n_blocks, kv_heads, width, max_new, rows, n_seq, pages;
+  bool search;
   int* err;
 };
+
+// The new tokens of a sequence and the cache blocks they touch.
+struct Arrival {
+  int before, first, count;
+};
+
+// False for lengths or offsets that make no sense: nothing of the sequence is stored.
+template <int BT>
+__device__ __forceinline__ bool arrival(const StoreArgs& a, int seq, Arrival& r) {
+  r.before = a.lengths[seq];
+  r.first = a.offsets[seq];
+  r.count = a.offsets[seq + 1] - r.first;
+  return r.count == 0 ||
+         !(r.before < 0 || r.first < 0 || r.count < 0 || r.count > a.max_new ||
+           r.first > a.rows - r.count || (long long)r.before + r.count > (long long)a.width * BT);
+}
+
+template <int BT>
+__device__ __forceinline__ int blocks_touched(const Arrival& r) {
+  return r.count == 0 ? 0 : (r.before + r.count - 1) / BT - r.before / BT + 1;
+}
+
+// The unit-th cache block of all that the sequences touch, in their order: a scan
+// over the sequences by the thread block. False past the last.
+template <int BT>
+__device__ __forceinline__ bool find_unit(const StoreArgs& a, int unit, int* sums, int* found,
+                                          Arrival* which) {
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int each = (a.n_seq + kStoreThreads - 1) / kStoreThreads;
+  const int begin = min(t * each, a.n_seq), end = min(begin + each, a.n_seq);
+  int mine = 0;
+  for (int s = begin; s < end; ++s) {
+    Arrival r;
+    if (arrival<BT>(a, s, r)) mine += blocks_touched<BT>(r);
+    else if (blockIdx.x == 0) atomicExch(a.err, H3_DEVERR_LAYOUT);
+  }
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) sums[warp] = upto;
+  if (t == 0) found[0] = -1;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += sums[w];
+  int at = upto - mine;
+  if (unit >= at && unit < upto)
+    for (int s = begin; s < end; ++s) {
+      Arrival r;
+      const int n = arrival<BT>(a, s, r) ? blocks_touched<BT>(r) : 0;
+      if (unit < at + n) {
+        found[0] = s;
+        found[1] = unit - at;
+        *which = r;
+        break;
+      }
+      at += n;
+    }
+  __syncthreads();
+  return found[0] >= 0;
+}
 
 // Scale of a block and kv head, and what happens to its codes.
 struct BlockScale {
@@ -87,29 +153,15 @@ __device__ __forceinline__ uint2 vec_codes(const uint4& u, const BlockScale& b) 
 }
 
 template <h3_type T, int D, int BT>
-__global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
-    k_kv_store(const StoreArgs a) {
+__device__ __forceinline__ void store_block(const StoreArgs& a, int seq, int nth, int head,
+                                            const Arrival& r, uint32_t* turned,
+                                            float (*part)[kStoreThreads / 32]) {
   constexpr int RV = D / 8;                 // 16-byte vectors per token
   constexpr int WR = BT / 4;                // words of four slots per channel
   constexpr int GROUPS = WR * RV;           // (word, vector) pairs
   constexpr int NG = (GROUPS + kStoreThreads - 1) / kStoreThreads;
-  __shared__ uint32_t turned[D * WR];
-  __shared__ float part[2][kStoreThreads / 32];
-  int id = blockIdx.x;
-  const int head = id % a.kv_heads;
-  id /= a.kv_heads;
-  const int nth = id % a.pages, seq = id / a.pages;
   const int t = threadIdx.x;
-
-  const int before = a.lengths[seq], first = a.offsets[seq];
-  const int count = a.offsets[seq + 1] - first;
-  if (count == 0) return;
-  // lengths or offsets that make no sense: nothing of the sequence is stored
-  if (before < 0 || first < 0 || count < 0 || count > a.max_new || first > a.rows - count ||
-      (long long)before + count > (long long)a.width * BT) {
-    if (t == 0) atomicExch(a.err, H3_DEVERR_LAYOUT);
-    return;
-  }
+  const int before = r.before, first = r.first, count = r.count;
   const int page = before / BT + nth;
   const int lo = max(before, page * BT), hi = min(before + count, (page + 1) * BT);
   if (lo >= hi) return;
@@ -149,18 +201,14 @@ __global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
     for (int i = 0; i < NG; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) peak.add(u[w][i][j]);
-    float m = peak.value();
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float m = warp_peak(peak.value());
     if ((t & 31) == 0) part[w][t >> 5] = m;
   }
   __syncthreads();  // also: every thread has read the old scales
   BlockScale bs[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    float m = 0.f;
-#pragma unroll
-    for (int k = 0; k < kStoreThreads / 32; ++k) m = max_nan(m, part[w][k]);
+    const float m = warp_peak(part[w][t % (kStoreThreads / 32)]);
     bs[w] = block_scale<T>(m, old[w], held > 0, a.scales[w] + at, t == 0);
   }
   uint8_t* kc = a.codes[0] + at * (BT * D);
@@ -178,20 +226,19 @@ __global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
       const int slot = 4 * word + j;
       if (whole || (slot >= slot0 && slot < to)) *reinterpret_cast<uint2*>(k + j * D) = c;
     }
-    uint2 c[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = vec_codes<T>(u[1][i][j], bs[1]);
+    // two channels of the four slots at a time, in the order of the words
     uint32_t* dst = turned + vec * 8 * WR + (word ^ (vec & (WR - 1)));
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t c0 = h ? c[0].y : c[0].x, c1 = h ? c[1].y : c[1].x;
-      const uint32_t c2 = h ? c[2].y : c[2].x, c3 = h ? c[3].y : c[3].x;
-      const uint32_t p = __byte_perm(c0, c1, 0x5140), q = __byte_perm(c2, c3, 0x5140);
-      const uint32_t r = __byte_perm(c0, c1, 0x7362), x = __byte_perm(c2, c3, 0x7362);
-      dst[(4 * h) * WR] = __byte_perm(p, q, 0x5410);
-      dst[(4 * h + 1) * WR] = __byte_perm(p, q, 0x7632);
-      dst[(4 * h + 2) * WR] = __byte_perm(r, x, 0x5410);
-      dst[(4 * h + 3) * WR] = __byte_perm(r, x, 0x7632);
+    for (int h = 0; h < 4; ++h) {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4& x = u[1][i][j];
+        unpack_pair<T>(h == 0 ? x.x : h == 1 ? x.y : h == 2 ? x.z : x.w, f[j], f[4 + j]);
+      }
+      const uint2 c = codes_of_8(f, bs[1].s);
+      dst[2 * h * WR] = c.x;
+      dst[(2 * h + 1) * WR] = c.y;
     }
   }
   if (bs[0].again)
@@ -235,6 +282,34 @@ __global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
       else if (again && slot < slot0) p[k] = (uint8_t)(early >> (8 * k));
     }
   }
+}
+
+template <h3_type T, int D, int BT>
+__global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
+    k_kv_store(const StoreArgs a) {
+  __shared__ uint32_t turned[D * BT / 4];
+  __shared__ float part[2][kStoreThreads / 32];
+  __shared__ int sums[kStoreThreads / 32], found[2];
+  __shared__ Arrival which;
+  const int head = blockIdx.x % a.kv_heads;
+  const int unit = blockIdx.x / a.kv_heads;
+  int seq, nth;
+  Arrival r;
+  if (a.search) {
+    if (!find_unit<BT>(a, unit, sums, found, &which)) return;
+    seq = found[0];
+    nth = found[1];
+    r = which;
+  } else {
+    seq = unit / a.pages;
+    nth = unit % a.pages;
+    if (!arrival<BT>(a, seq, r)) {
+      if (threadIdx.x == 0) atomicExch(a.err, H3_DEVERR_LAYOUT);
+      return;
+    }
+    if (r.count == 0) return;
+  }
+  store_block<T, D, BT>(a, seq, nth, head, r, turned, part);
 }
 
 // ------------------------------------------------------------- attention
@@ -1025,10 +1100,16 @@ cudaError_t run_attention(AttnArgs& a, void* ws, cudaStream_t st) {
                             : F<D, 128, NC>(__VA_ARGS__))
 
 template <h3_type T, int D>
-cudaError_t run_store(const StoreArgs& a, int n_seq, int block_tokens, cudaStream_t st) {
-  const long long blocks = (long long)n_seq * a.pages * a.kv_heads;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const unsigned grid = (unsigned)blocks;
+cudaError_t run_store(StoreArgs a, int block_tokens, cudaStream_t st) {
+  // Where the sequences bring very different numbers of tokens, most pairs of a
+  // sequence and a block up to max_new would be empty: with as many rows as there
+  // are, only rows / block_tokens + 2 n_seq of them can hold one.
+  long long units = (long long)a.n_seq * a.pages;
+  if (units * a.kv_heads > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const long long most = a.rows / block_tokens + 2LL * a.n_seq;
+  a.search = most < units;
+  if (a.search) units = most;
+  const unsigned grid = (unsigned)(units * a.kv_heads);
   if (block_tokens == 32) k_kv_store<T, D, 32><<<grid, kStoreThreads, 0, st>>>(a);
   else if (block_tokens == 64) k_kv_store<T, D, 64><<<grid, kStoreThreads, 0, st>>>(a);
   else k_kv_store<T, D, 128><<<grid, kStoreThreads, 0, st>>>(a);
@@ -1059,15 +1140,16 @@ cudaError_t launch_kv_cache_store(const h3_kv_cache& c, int n_seq, int max_new,
   a.width = width;
   a.max_new = max_new;
   a.rows = rows;
+  a.n_seq = n_seq;
   // max_new tokens that begin anywhere inside a block
   a.pages = (max_new + c.block_tokens - 2) / c.block_tokens + 1;
   if (a.pages > width) a.pages = width;
   a.err = err;
   if (c.head_dim == 128)
-    return f16 ? run_store<H3_F16, 128>(a, n_seq, c.block_tokens, st)
-               : run_store<H3_BF16, 128>(a, n_seq, c.block_tokens, st);
-  return f16 ? run_store<H3_F16, 64>(a, n_seq, c.block_tokens, st)
-             : run_store<H3_BF16, 64>(a, n_seq, c.block_tokens, st);
+    return f16 ? run_store<H3_F16, 128>(a, c.block_tokens, st)
+               : run_store<H3_BF16, 128>(a, c.block_tokens, st);
+  return f16 ? run_store<H3_F16, 64>(a, c.block_tokens, st)
+             : run_store<H3_BF16, 64>(a, c.block_tokens, st);
 }
 
 size_t cache_attention_workspace(const h3_kv_cache& c, int n_seq, int q_heads, int width) {

@@ -641,7 +641,8 @@ typedef struct {
  * k and v. A sequence whose lengths or offsets are negative, whose new tokens are
  * more than max_new, leave `rows` or do not fit table_width blocks is not stored,
  * nor is a token whose table entry names no block: both record an error
- * (h3_text_error, H3_ERR_LAYOUT). A block that is written must be in one
+ * (h3_text_error, H3_ERR_LAYOUT; where offsets decrease, parts of other sequences
+ * may be left out as well). A block that is written must be in one
  * sequence's table only, and there once. Enqueues. */
 H3_API h3_status h3_kv_cache_store(const h3_kv_cache* cache, int n_seq, int max_new,
                                    const int32_t* block_table, int table_width,

@@ -125,6 +125,34 @@ def test_store(D, BT, dtype):
     _check_store(cache, counts, *_new(counts, 3, D, dtype))
 
 
+@pytest.mark.parametrize("n_seq", [3, 40, 257, 700])
+def test_store_of_very_different_counts(n_seq):
+    """Far fewer blocks than sequences times the largest number of tokens: nothing,
+    one or a few tokens next to prompts of several blocks, at any place of a block;
+    the rows of k and v go on behind the last sequence."""
+    BT, D = 32, 64
+    counts = [(0, 1, 2, 33)[i % 4] if i % 97 else 300 + i for i in range(n_seq)]
+    lengths = [(0, 31, 32, 45)[(i // 4) % 4] for i in range(n_seq)]
+    cache = Cache(lengths, 1, D, BT, spare=max(counts))
+    k, v = _new(counts + [9], 1, D, BF)
+    _check_store(cache, counts, k, v)
+
+
+def test_store_reports_a_bad_sequence_among_very_different_counts():
+    BT, D = 32, 64
+    counts, lengths = [300, 1, 0, 40, 2], [5, 31, 7, 64, 0]
+    cache = Cache(lengths, 2, D, BT, spare=300)
+    k, v = _new(counts, 2, D, BF)
+    want, scales = cache.kc, cache.ks
+    for s in (0, 1, 2, 4):  # sequence 3 is left out
+        part = [c if i == s else 0 for i, c in enumerate(counts)]
+        row = sum(counts[:s])
+        want, scales = _store_formula(cache, want, scales, part, k[row:row + counts[s]], False)
+    cache.store(counts, k, v, lengths=_i32(lengths[:3] + [-1] + lengths[4:]))
+    assert h3.h3_text_error() == h3.H3_ERR_LAYOUT
+    assert torch.equal(cache.kc, want) and torch.equal(cache.ks, scales)
+
+
 def test_store_token_by_token_grows_the_scale():
     """Forty single tokens, some far larger than all before: the earlier codes are
     rounded again, exactly once per growth."""
