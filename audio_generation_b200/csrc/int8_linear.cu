@@ -4,6 +4,7 @@
 // with the sum in 32-bit integers on tcgen05 (kind::i8). The integer sum is
 // exact whatever its order, so K may be split freely.
 #include <cuda_fp16.h>
+#include <limits.h>
 
 #include "host_util.cuh"
 #include "int8_code.cuh"
@@ -128,7 +129,7 @@ constexpr int A_STAGE = BM * BKB;  // 16 KB
 
 struct Out {
   void* p;
-  int64_t stride;
+  int64_t stride_m, stride_n;  // elements between rows, and between columns
   int type;
   const float* a_scale;
   const float* w_scale;
@@ -197,7 +198,7 @@ constexpr int PNST = 6;
 template <int BN>
 constexpr int p_stage() { return A_STAGE + BN / 2 * BKB; }
 template <int BN>
-constexpr int p_smem() { return PNST * p_stage<BN>() + 1024 + 256; }
+constexpr int p_smem() { return PNST * p_stage<BN>() + 1024 + 256 + 4 * (BN + 32 * 33) * 4; }
 
 template <int BN>
 __device__ __forceinline__ void pair_tile(int t, int tiles_m, int tiles_n, int group_n, int& m0,
@@ -324,43 +325,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   } else {
     const int quarter = warp & 3;
     const uint32_t tempty0 = at(&tempty[0], 0), tempty1 = at(&tempty[1], 0);
-    const bool vec = out.stride % (out.type == H3_F32 ? 4 : 8) == 0;
+    const bool vec = out.stride_m % (out.type == H3_F32 ? 4 : 8) == 0;
+    // the tile's column scales, and 32 x 32 values to turn
+    float* scales = reinterpret_cast<float*>(smem + PNST * STAGE + 256) + (warp - 2) * BN;
+    float* turn = reinterpret_cast<float*>(smem + PNST * STAGE + 256) + 4 * BN + (warp - 2) * 32 * 33;
     uint32_t it = 0;
     for (int t = pair; t < T; t += n_pairs, ++it) {
       const uint32_t acc = it & 1, aph = (it >> 1) & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], aph, wc))) break;
-      tc_fence_after();
       int m0, n0;
       pair_tile<BN>(t, tiles_m, tiles_n, group_n, m0, n0);
-      const int m = m0 + BM * rank + quarter * 32 + lane;
+      m0 += BM * rank + quarter * 32;
+      const int m = m0 + lane;
       const bool row_ok = m < M;
-      const float sa = row_ok ? out.a_scale[m] : 0.f;
+      const float sa = row_ok ? __ldg(out.a_scale + m) : 0.f;
+#pragma unroll
+      for (int k = 4 * lane; k < BN; k += 128) {
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float* src = out.w_scale + n0 + k;
+        if (n0 + k + 4 <= N) {
+          w = __ldg(reinterpret_cast<const float4*>(src));
+        } else {
+          if (n0 + k < N) w.x = __ldg(src);
+          if (n0 + k + 1 < N) w.y = __ldg(src + 1);
+          if (n0 + k + 2 < N) w.z = __ldg(src + 2);
+        }
+        *reinterpret_cast<float4*>(scales + k) = w;
+      }
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], aph, wc))) break;
+      tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN;
 #pragma unroll 1
       for (int c = 0; c < BN / 32; ++c) {
+        const int n = n0 + 32 * c;
+        if (n >= N || m0 >= M) break;
         uint32_t r[32];
         tmem_ld32(taddr + 32 * c, r);
         tmem_wait_ld();
-        const int n = n0 + 32 * c;
-        if (n + 32 <= N && vec) {
-          float v[32];
-          const float4* w4 = reinterpret_cast<const float4*>(out.w_scale + n);
+        float v[32];
+        const float4* w4 = reinterpret_cast<const float4*>(scales + 32 * c);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 w = __ldg(w4 + q);
-            v[4 * q] = (float)(int)r[4 * q] * (sa * w.x);
-            v[4 * q + 1] = (float)(int)r[4 * q + 1] * (sa * w.y);
-            v[4 * q + 2] = (float)(int)r[4 * q + 2] * (sa * w.z);
-            v[4 * q + 3] = (float)(int)r[4 * q + 3] * (sa * w.w);
-          }
-          if (row_ok) store_32(out, m * out.stride + n, v);
-        } else if (row_ok) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (n + i < N)
-              store_one(out, m * out.stride + n + i,
-                        (float)(int)r[i] * (sa * __ldg(out.w_scale + n + i)));
+        for (int q = 0; q < 8; ++q) {
+          const float4 w = w4[q];
+          v[4 * q] = (float)(int)r[4 * q] * (sa * w.x);
+          v[4 * q + 1] = (float)(int)r[4 * q + 1] * (sa * w.y);
+          v[4 * q + 2] = (float)(int)r[4 * q + 2] * (sa * w.z);
+          v[4 * q + 3] = (float)(int)r[4 * q + 3] * (sa * w.w);
         }
+        if (n + 32 <= N && vec) {
+          if (row_ok) store_32(out, m * out.stride_m + n, v);
+          continue;
+        }
+        // Rows that do not start 16-byte aligned, or a row's last columns: turned, so
+        // that neighbouring lanes store neighbouring columns (4517 x 275 x 224: NNN us
+        // against 50 us with a lane per row).
+#pragma unroll
+        for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v[i];
+        __syncwarp();
+        if (n + lane < N) {
+          const int rows = min(32, M - m0);
+#pragma unroll 8
+          for (int i = 0; i < rows; ++i)
+            store_one(out, (m0 + i) * out.stride_m + n + lane, turn[i * 33 + lane]);
+        }
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -518,7 +546,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t acc = it & 1, aph = (it >> 1) & 1;
       const int n = t / m_tiles * BM + r, m0 = t % m_tiles * NT;
       const int rows = min(NT, M - m0);
-      const float sw = n < N ? out.w_scale[n] : 0.f;
+      const float sw = n < N ? __ldg(out.w_scale + n) : 0.f;
+      float sa_next = lane < rows ? __ldg(out.a_scale + m0 + lane) : 0.f;
       if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], aph, wc))) break;
       tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * ACC;
@@ -527,6 +556,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t* part = reinterpret_cast<uint32_t*>(smem);
 #pragma unroll 1
       for (int c = 0; c < (NT + 31) / 32; ++c) {
+        const float sa = sa_next;  // of token 32 c + lane
+        sa_next = 32 * c + 32 + lane < rows ? __ldg(out.a_scale + m0 + 32 * c + 32 + lane) : 0.f;
         uint32_t v[32];
         tmem_ld32(taddr + 32 * c, v);
         tmem_wait_ld();
@@ -534,12 +565,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (32 * c + i < rows) part[(32 * c + i) * BM + r] = v[i];
-        } else if (n < N) {
+        } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const int m = m0 + 32 * c + i;
-            if (32 * c + i < rows)
-              store_one(out, m * out.stride + n, (float)(int)v[i] * (out.a_scale[m] * sw));
+            const float s = __shfl_sync(0xffffffffu, sa, i) * sw;
+            if (32 * c + i < rows && n < N)
+              store_one(out, (m0 + 32 * c + i) * out.stride_m + n * out.stride_n,
+                        (float)(int)v[i] * s);
           }
         }
       }
@@ -555,10 +587,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (warp >= 2 && n < N) {
       const int m0 = tile0 % m_tiles * NT, rows = min(NT, M - m0);
       const int first = rows * rank / split, last = rows * (rank + 1) / split;
-      const bool vec = n + 4 <= N && out.stride % 4 == 0;
+      const bool vec = n + 4 <= N && out.stride_n == 1 && out.stride_m % 4 == 0;
       float sw[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sw[e] = n + e < N ? out.w_scale[n + e] : 0.f;
+      for (int e = 0; e < 4; ++e) sw[e] = n + e < N ? __ldg(out.w_scale + n + e) : 0.f;
       uint32_t from[kMaxSplit];
 #pragma unroll
       for (int q = 0; q < kMaxSplit; ++q)
@@ -572,16 +604,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int q = 1; q < kMaxSplit; ++q)
           sum.x += v[q].x, sum.y += v[q].y, sum.z += v[q].z, sum.w += v[q].w;
-        const float sa = out.a_scale[m0 + i];
+        const float sa = __ldg(out.a_scale + m0 + i);
         const float y[4] = {(float)(int)sum.x * (sa * sw[0]), (float)(int)sum.y * (sa * sw[1]),
                             (float)(int)sum.z * (sa * sw[2]), (float)(int)sum.w * (sa * sw[3])};
-        const size_t at = (m0 + i) * out.stride + n;
+        const size_t at = (m0 + i) * out.stride_m + n * out.stride_n;
         if (vec) {
           store_4(out, at, y);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (n + e < N) store_one(out, at + e, y[e]);
+            if (n + e < N) store_one(out, at + e * out.stride_n, y[e]);
         }
       }
     }
@@ -718,6 +750,21 @@ cudaError_t run_skinny(const Plan& p, int M, int N, int K, const void* a, const 
                             out, err);
 }
 
+// By the number of tokens.
+Plan plan_any(int M, int N, int K) {
+  return M <= 16   ? plan_skinny<16>(M, N, K)
+         : M <= 32 ? plan_skinny<32>(M, N, K)
+         : M <= 64 ? plan_skinny<64>(M, N, K)
+                   : plan_skinny<128>(M, N, K);
+}
+cudaError_t run_any(const Plan& p, int M, int N, int K, const void* a, const void* w,
+                    const Out& out, int* err, cudaStream_t st) {
+  return M <= 16   ? run_skinny<16>(p, M, N, K, a, w, out, err, st)
+         : M <= 32 ? run_skinny<32>(p, M, N, K, a, w, out, err, st)
+         : M <= 64 ? run_skinny<64>(p, M, N, K, a, w, out, err, st)
+                   : run_skinny<128>(p, M, N, K, a, w, out, err, st);
+}
+
 }  // namespace
 
 cudaError_t launch_quantize_rows_int8(h3_type type, int rows, int K, const void* x,
@@ -734,20 +781,22 @@ cudaError_t launch_quantize_rows_int8(h3_type type, int rows, int K, const void*
 cudaError_t launch_matmul_int8(int M, int N, int K, const void* a, const float* a_scale,
                                const void* w, const float* w_scale, h3_type out_type, void* out,
                                int64_t out_stride, int* err, cudaStream_t st) {
-  const Out o{out, out_stride, (int)out_type, a_scale, w_scale};
-  // The narrowest token tile that holds all rows, or tiles of 128 of them; pairs
-  // of CTAs where they are estimated to be faster.
-#define H3_FEW(NT)                                                              \
-  {                                                                             \
-    const Plan p = plan_skinny<NT>(M, N, K);                                    \
-    if (M <= 128 || p.cycles < pair_cycles(M, N, K))                            \
-      return run_skinny<NT>(p, M, N, K, a, w, o, err, st);                      \
+  const Out o{out, out_stride, 1, (int)out_type, a_scale, w_scale};
+  // The few-row kernel with a's rows as tokens (up to 2048 of them), or, where out
+  // is narrower than long, with w's rows as tokens and out turned; the narrowest
+  // token tile that holds all tokens, or tiles of 128 of them. Pairs of CTAs where
+  // they are estimated to be faster. (2290 x 10 x 9040: NNN us turned, 30 us by
+  // pairs, of which there are only nine.)
+  const bool few = M <= 2048, turn = N <= 128 && N < M;
+  Plan p{}, q{};
+  if (few) p = plan_any(M, N, K);
+  if (turn) q = plan_any(N, M, K);
+  const long long pairs = M <= 128 ? LLONG_MAX : pair_cycles(M, N, K);
+  if (turn && q.cycles < pairs && (!few || q.cycles < p.cycles)) {
+    const Out t{out, 1, out_stride, (int)out_type, w_scale, a_scale};
+    return run_any(q, N, M, K, w, a, t, err, st);
   }
-  if (M <= 16) H3_FEW(16)
-  else if (M <= 32) H3_FEW(32)
-  else if (M <= 64) H3_FEW(64)
-  else if (M <= 2048) H3_FEW(128)
-#undef H3_FEW
+  if (few && p.cycles < pairs) return run_any(p, M, N, K, a, w, o, err, st);
   return run_pair<256>(M, N, K, a, w, o, err, st);
 }
 

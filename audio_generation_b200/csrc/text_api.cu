@@ -107,7 +107,8 @@ h3_status h3_matmul_int8(int M, int N, int K, const void* a_codes, const float* 
                          int64_t out_stride, h3_stream_t stream) {
   if (!known_type(out_type) || M < 0 || N < 0 || K <= 0) return H3_ERR_ARG;
   // |sum| <= 128 * 128 * K must stay below 2^31; rows of codes start 16-byte aligned
-  if (K % 16 != 0 || K > 131056 || out_stride < N) return H3_ERR_SHAPE;
+  if (K % 16 != 0 || K > 131056 || out_stride < N || M > 1 << 30 || N > 1 << 30)
+    return H3_ERR_SHAPE;
   if (M == 0 || N == 0) return H3_OK;
   if (!a_codes || !a_scales || !w_codes || !w_scales || !out) return H3_ERR_ARG;
   if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) ||

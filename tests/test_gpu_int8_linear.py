@@ -114,6 +114,20 @@ def test_product(M, N, K, dtype):
     _product(M, N, K, dtype)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [
+    (300, 1, 64), (2290, 10, 9040), (1000, 3, 14320), (4097, 17, 272), (129, 128, 528),
+    (5000, 100, 144), (20001, 33, 48), (127, 9, 4096), (4517, 275, 224), (2392, 382, 16),
+    (2051, 3001, 160)])
+def test_product_of_many_rows_and_few_or_odd_columns(M, N, K, dtype):
+    _product(M, N, K, dtype)
+
+
+@pytest.mark.parametrize("stride", [10, 11, 16, 32])
+def test_narrow_rows_of_out_apart(stride):
+    _product(777, 10, 1040, torch.bfloat16, stride=stride)
+
+
 @pytest.mark.parametrize("M", [5, 300])
 @pytest.mark.parametrize("stride", [1001, 1008, 1537])
 def test_rows_of_out_apart(M, stride):

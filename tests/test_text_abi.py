@@ -37,6 +37,8 @@ def _matmul(M=4, N=8, K=64, a=P, sa=P, w=P, sw=P, type=h3.H3_F16, out=P, stride=
     (dict(type=7), h3.H3_ERR_ARG), (dict(a=None), h3.H3_ERR_ARG), (dict(sa=None), h3.H3_ERR_ARG),
     (dict(w=None), h3.H3_ERR_ARG), (dict(sw=None), h3.H3_ERR_ARG), (dict(out=None), h3.H3_ERR_ARG),
     (dict(K=24), h3.H3_ERR_SHAPE), (dict(K=131072), h3.H3_ERR_SHAPE),
+    (dict(M=2 ** 30 + 1), h3.H3_ERR_SHAPE),
+    (dict(N=2 ** 30 + 1, stride=2 ** 31), h3.H3_ERR_SHAPE),
     (dict(stride=7), h3.H3_ERR_SHAPE), (dict(a=ODD), h3.H3_ERR_ALIGN),
     (dict(sa=ODD), h3.H3_ERR_ALIGN), (dict(w=ODD), h3.H3_ERR_ALIGN),
     (dict(sw=ODD), h3.H3_ERR_ALIGN), (dict(out=ODD), h3.H3_ERR_ALIGN),
