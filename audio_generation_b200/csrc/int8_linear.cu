@@ -162,26 +162,54 @@ __device__ __forceinline__ void store_4(const Out& o, size_t off, const float* v
   }
 }
 
-// 32 neighbouring values of one row, 16-byte aligned.
-__device__ __forceinline__ void store_32(const Out& o, size_t off, const float* v) {
-  if (o.type == H3_F32) {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(o.p) + off);
+template <h3_type T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (T == H3_BF16) return pack_bf16x2(lo, hi);
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A warp's 32 x 32 values, row i from turn + kTurn i, to `rows` rows of out from off
+// on, `cols` columns each: whole and aligned rows in pieces of 16 bytes, a row's
+// pieces by neighbouring lanes; else neighbouring lanes store neighbouring columns.
+constexpr int kTurn = 36;
+template <h3_type T>
+__device__ __forceinline__ void store_turned(const Out& o, int64_t off, const float* turn,
+                                             int rows, int cols, bool vec, int lane) {
+  if (vec && cols >= 32) {
+    constexpr int PER = T == H3_F32 ? 4 : 8;  // values of a piece
+    constexpr int LANES = 32 / PER;           // lanes of a row
+    const int i0 = lane / LANES, q = lane % LANES * PER;
+    const float* src = turn + i0 * kTurn + q;
+    off += i0 * o.stride_m + q;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) d[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-  } else {
-    uint32_t w[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      if (o.type == H3_BF16) {
-        w[q] = pack_bf16x2(v[2 * q], v[2 * q + 1]);
+    for (int i = 0; i < 32; i += 32 / LANES) {
+      const float4 x = *reinterpret_cast<const float4*>(src + i * kTurn);
+      uint4 w;
+      if constexpr (T == H3_F32) {
+        w = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z),
+                       __float_as_uint(x.w));
       } else {
-        const __half2 h = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
-        w[q] = *reinterpret_cast<const uint32_t*>(&h);
+        const float4 y = *reinterpret_cast<const float4*>(src + i * kTurn + 4);
+        w = make_uint4(pack16<T>(x.x, x.y), pack16<T>(x.z, x.w),
+                       pack16<T>(y.x, y.y), pack16<T>(y.z, y.w));
       }
+      if (i0 + i < rows)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(o.p) +
+                                  (off + i * o.stride_m) * (T == H3_F32 ? 4 : 2)) = w;
     }
-    uint4* d = reinterpret_cast<uint4*>(static_cast<uint16_t*>(o.p) + off);
+    return;
+  }
+  if (lane >= cols) return;
+  off += lane;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) d[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  for (int i = 0; i < 32; ++i) {
+    const float x = turn[i * kTurn + lane];
+    if (i < rows) {
+      if constexpr (T == H3_F32) static_cast<float*>(o.p)[off] = x;
+      else static_cast<uint16_t*>(o.p)[off] = (uint16_t)pack16<T>(x, 0.f);
+    }
+    off += o.stride_m;
   }
 }
 
@@ -198,7 +226,7 @@ constexpr int PNST = 6;
 template <int BN>
 constexpr int p_stage() { return A_STAGE + BN / 2 * BKB; }
 template <int BN>
-constexpr int p_smem() { return PNST * p_stage<BN>() + 1024 + 256 + 4 * (BN + 32 * 33) * 4; }
+constexpr int p_smem() { return PNST * p_stage<BN>() + 1024 + 256 + 4 * (BN + 32 * kTurn) * 4; }
 
 template <int BN>
 __device__ __forceinline__ void pair_tile(int t, int tiles_m, int tiles_n, int group_n, int& m0,
@@ -328,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const bool vec = out.stride_m % (out.type == H3_F32 ? 4 : 8) == 0;
     // the tile's column scales, and 32 x 32 values to turn
     float* scales = reinterpret_cast<float*>(smem + PNST * STAGE + 256) + (warp - 2) * BN;
-    float* turn = reinterpret_cast<float*>(smem + PNST * STAGE + 256) + 4 * BN + (warp - 2) * 32 * 33;
+    float* turn = reinterpret_cast<float*>(smem + PNST * STAGE + 256) + 4 * BN + (warp - 2) * 32 * kTurn;
     uint32_t it = 0;
     for (int t = pair; t < T; t += n_pairs, ++it) {
       const uint32_t acc = it & 1, aph = (it >> 1) & 1;
@@ -372,22 +400,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           v[4 * q + 2] = (float)(int)r[4 * q + 2] * (sa * w.z);
           v[4 * q + 3] = (float)(int)r[4 * q + 3] * (sa * w.w);
         }
-        if (n + 32 <= N && vec) {
-          if (row_ok) store_32(out, m * out.stride_m + n, v);
-          continue;
-        }
-        // Rows that do not start 16-byte aligned, or a row's last columns: turned, so
-        // that neighbouring lanes store neighbouring columns (4517 x 275 x 224: NNN us
-        // against 50 us with a lane per row).
+        // (A lane per row would store 16 bytes of 32 rows at a time: 63 us for 2031 x
+        // 18992 x 256 to float32, against 43 us; 50 us against 11 for 4517 x 275 x 224.)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) turn[lane * 33 + i] = v[i];
+        for (int q = 0; q < 8; ++q)
+          *reinterpret_cast<float4*>(turn + lane * kTurn + 4 * q) =
+              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         __syncwarp();
-        if (n + lane < N) {
-          const int rows = min(32, M - m0);
-#pragma unroll 8
-          for (int i = 0; i < rows; ++i)
-            store_one(out, (m0 + i) * out.stride_m + n + lane, turn[i * 33 + lane]);
-        }
+        const int rows = min(32, M - m0), cols = min(32, N - n);
+        const int64_t off = m0 * out.stride_m + n;
+        if (out.type == H3_F32) store_turned<H3_F32>(out, off, turn, rows, cols, vec, lane);
+        else if (out.type == H3_BF16) store_turned<H3_BF16>(out, off, turn, rows, cols, vec, lane);
+        else store_turned<H3_F16>(out, off, turn, rows, cols, vec, lane);
         __syncwarp();
       }
       tc_fence_before();
@@ -413,8 +437,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 // axis of one and add their integer sums through distributed shared memory,
 // each finishing a share of the tokens. Neighbouring lanes store neighbouring
 // columns of out. Warps as above; the accumulator is double-buffered.
-// 1 x 14336 x 5120: 15.1 us (73 MB: 4.9 TB/s, 3 to 4 us of it launch, fill and
-// tail); 48 x 32003 x 5120 with float32 out: 31.7 us (170 MB: 5.4 TB/s).
+// 1 x 14336 x 5120: 14.8 us (73 MB: 5.0 TB/s, 3 to 4 us of it launch, fill and
+// tail); 48 x 32003 x 5120 with float32 out: 31.2 us (170 MB: 5.5 TB/s).
 template <int NT>
 constexpr int s_stage() { return A_STAGE + NT * BKB; }
 template <int NT>
@@ -785,7 +809,7 @@ cudaError_t launch_matmul_int8(int M, int N, int K, const void* a, const float* 
   // The few-row kernel with a's rows as tokens (up to 2048 of them), or, where out
   // is narrower than long, with w's rows as tokens and out turned; the narrowest
   // token tile that holds all tokens, or tiles of 128 of them. Pairs of CTAs where
-  // they are estimated to be faster. (2290 x 10 x 9040: NNN us turned, 30 us by
+  // they are estimated to be faster. (2290 x 10 x 9040: 7.6 us turned, 30 us by
   // pairs, of which there are only nine.)
   const bool few = M <= 2048, turn = N <= 128 && N < M;
   Plan p{}, q{};
