@@ -4,6 +4,8 @@
 // and the attention of one query token per sequence reads it.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "int8_code.cuh"
 #include "internal.cuh"
 #include "sm100.cuh"
@@ -315,7 +317,10 @@ __global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
 // ------------------------------------------------------------- attention
 // o[s, h] = softmax_j(scale q[s, h] . k[j]) v[j] over the sequence's cached
 // tokens. Bound by the bytes of the cache (2 D per token and kv head), so the
-// query heads of a group (16 at a time) share one pass over it.
+// query heads of a group share one pass over it, eight at a time: the columns of an
+// MMA. (16 at a time halve the bytes of larger groups, but double a thread's
+// registers and work per byte: 24 sequences of 6000 tokens, 24 heads over 1 x 128,
+// 45 us against 24.)
 //
 // The work is the list of all (sequence, head group, cache block) units in that
 // order, cut into equal ranges, one per thread block, as many as run at once:
@@ -342,34 +347,33 @@ __global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
 // rate.) Scores: s^T = K q^T on 8-bit integers (m16n8k32), q as two 8-bit limbs of
 // a 16-bit fixed-point row (an error of at most 2^-16 of the row's largest
 // element), the sums exact. Values: o^T += V^T w^T on fp16 (m16n8k16), where the
-// codes become fp16 exactly and the weights are fp16, times 2^10 so that they
-// stay normal numbers down to 2^-24 of the largest, and times the block's V scale
+// codes become fp16 exactly and the weights are fp16, times 2^15 so that they
+// stay normal numbers down to 2^-29 of the largest, and times the block's V scale
 // over the largest one met so far, so that the sums of all blocks share one
 // accumulator. The K scale is applied to the scores in float32. A thread reads
 // 16-byte pieces of a K row as four k-quads, since the order of the channels in a
 // product is free, and the tokens are assigned to rows so that its V operand is
 // one contiguous piece of a transposed V row; the weights turn between the two
 // layouts by 8 x 8 transposes across the warp. 40 sequences of 500 to 24000 tokens,
-// 40 heads over 8 x 128 (423 MB): 77 us, 5.5 TB/s; one of 4001 tokens: 10.5 us.
+// 40 heads over 8 x 128 (423 MB): 75 us, 5.6 TB/s; one of 4001 tokens: 10.6 us.
 constexpr int kAttnThreads = 160, kConsumers = 4;
-constexpr int kMaxCols = 2;     // column tiles of eight heads a warp takes at most
+constexpr int kRows = 8;        // query heads that share a pass over the cache
 constexpr int kListSize = 64;   // entries of the producer's list, two batches of 32
-constexpr int kMinUnits = 2;    // cache blocks a thread block takes at least, about
+constexpr int kMinUnits = 2;    // cache blocks a thread block takes at least, about, but for whole pairs
 constexpr int kPairUnits = 3;
 
-template <int D, int BT, int NC>  // NC column tiles: ROWS = 8 NC query heads per pass
+template <int D, int BT>
 struct Ring {
-  static constexpr int ROWS = 8 * NC;
   static constexpr int BLOCK = BT * D;  // bytes of K (or V) codes
   // thread blocks per SM: three where the accumulators leave the registers for it
-  static constexpr int PER_SM = BLOCK >= 16384 || D * NC == 256 ? 2 : 3;
+  static constexpr int PER_SM = BLOCK >= 16384 ? 2 : 3;
   static constexpr int FIT = (PER_SM == 2 ? 98304 : 65536) / (2 * BLOCK);
   // Even, so that a stage always serves the same pair of warps: a warp that waits
   // for a stage's next fill has then seen its last one, and cannot take an older
   // phase of the same parity for the one it waits for.
   static constexpr int STAGES = FIT < 16 ? FIT / 2 * 2 : 16;
   static constexpr int PITCH = D + 4;   // floats; the accumulators' stores meet no bank twice
-  static constexpr int SUMS = 2 * ROWS * PITCH * 4;  // two warps' accumulators
+  static constexpr int SUMS = 2 * kRows * PITCH * 4;  // two warps' accumulators
   static constexpr int BYTES = STAGES * 2 * BLOCK + SUMS;
   static_assert(STAGES <= kListSize - 32, "a list entry outlives its stage");
   static_assert(SUMS % 128 == 0, "stage alignment");
@@ -388,12 +392,12 @@ struct AttnArgs {
   uint16_t* o;
   int64_t q_stride, o_stride;
   // workspace, per thread block: two parts (0: a pair begun earlier, 1: a pair
-  // that goes on) of `pass` rows of sums and of (maximum, sum of weights), and
+  // that goes on) of kRows rows of sums and of (maximum, sum of weights), and
   // which pair part 1 belongs to, with the number of its parts
-  float* part;    // [blocks][2][pass][D]
-  float2* stat;   // [blocks][2][pass]
+  float* part;    // [blocks][2][kRows][D]
+  float2* stat;   // [blocks][2][kRows]
   int4* cut;      // [blocks] {sequence, head group, parts, 0}
-  int n_seq, n_blocks, kv_heads, group, row_groups, pass, width;
+  int n_seq, n_blocks, kv_heads, group, row_groups, width;
   float scale_log2;
   bool f16;
   int* err;
@@ -469,21 +473,23 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
-template <int D, int BT, int NC>
-__global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
+template <int D, int BT>
+__global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
     k_cache_attention(const AttnArgs a) {
-  using R = Ring<D, BT, NC>;
-  constexpr int ROWS = R::ROWS, PITCH = R::PITCH;
+  using R = Ring<D, BT>;
+  constexpr int PITCH = R::PITCH;
   constexpr int HT = BT / 2;     // tokens of a warp per cache block
   constexpr int NB = HT / 8;     // its blocks of eight tokens
   constexpr int NH = D / 64;     // 64-channel halves of a K row
   constexpr int ND = D / 16;     // 16-channel row tiles of the output
-  constexpr float kShift = 10.f;
+  // Weights are at most 2^15: normal numbers of fp16 down to 2^-29 of that, and with
+  // the smaller V scale of a block still to 2^-21 where their sum comes from them.
+  constexpr float kShift = 15.f, kSmallRatio = 1.f / 256;
   constexpr float kFixed = 32512.f;  // 127 * 256: the largest element of a q row
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[R::STAGES], empty[R::STAGES];
   __shared__ Entry list[kListSize];
-  __shared__ float2 stat[kConsumers][ROWS];
+  __shared__ float2 stat[kConsumers][kRows];
   __shared__ long long warp_sum[kAttnThreads / 32];
   __shared__ int4 s_begin;       // the range's first unit: {sequence, head group, page, 0}
   __shared__ long long s_cut[2];  // its ends among all units
@@ -532,7 +538,7 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
     return units_in(sum) + (sum >> kCount) * kPairUnits * heads;
   };
   const long long units = units_in(total), weight = weight_of(total);
-  long long ranges = (units + kMinUnits - 1) / kMinUnits;
+  long long ranges = max((units + kMinUnits - 1) / kMinUnits, (total >> kCount) * heads);
   if (ranges > gridDim.x) ranges = gridDim.x;
   const bool idle = (long long)blockIdx.x >= ranges;
   if (!idle) {
@@ -642,22 +648,21 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, t = lane & 3;
   const int half = warp & 1;
-  float* sums = reinterpret_cast<float*>(smem);  // [2][ROWS][PITCH]
+  float* sums = reinterpret_cast<float*>(smem);  // [2][kRows][PITCH]
   int unit = 0;
   bool have_cut = false;
   while (unit < n_units) {
-    const int kvh = hg / a.row_groups, h0 = (hg - kvh * a.row_groups) * ROWS;
-    const int rows = min(ROWS, a.group - h0), head0 = kvh * a.group + h0;
+    const int kvh = hg / a.row_groups, h0 = (hg - kvh * a.row_groups) * kRows;
+    const int rows = min(kRows, a.group - h0), head0 = kvh * a.group + h0;
     const int n = min(pages - page, n_units - unit);  // this segment's units
     const bool begins = page == 0, ends = page + n == pages;
-    // q rows -> 16-bit fixed point, two limbs. Column g of tile c is head 8 c + g;
-    // the thread's channels are 64 h + 16 t + 0..15.
-    uint32_t qh[NC][NH][4], ql[NC][NH][4];
-    float mul[NC][2];  // of heads 8 c + 2 t, + 1
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const bool there = 8 * c + g < rows;
-      const uint16_t* q = a.q + seq * a.q_stride + (head0 + (there ? 8 * c + g : 0)) * D + 16 * t;
+    // q rows -> 16-bit fixed point, two limbs. Column g is head g of the group's
+    // part; the thread's channels are 64 h + 16 t + 0..15.
+    uint32_t qh[NH][4], ql[NH][4];
+    float mul[2];  // of heads 2 t, + 1
+    {
+      const bool there = g < rows;
+      const uint16_t* q = a.q + seq * a.q_stride + (head0 + (there ? g : 0)) * D + 16 * t;
       float x[NH][16], m = 0.f;
 #pragma unroll
       for (int h = 0; h < NH; ++h)
@@ -685,25 +690,20 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
             hi[k] = (uint32_t)((v + 128) >> 8);
             lo[k] = (uint32_t)v;  // its low byte, signed, is v - 256 hi
           }
-          qh[c][h][w] = pack4(hi[0], hi[1], hi[2], hi[3]);
-          ql[c][h][w] = pack4(lo[0], lo[1], lo[2], lo[3]);
+          qh[h][w] = pack4(hi[0], hi[1], hi[2], hi[3]);
+          ql[h][w] = pack4(lo[0], lo[1], lo[2], lo[3]);
         }
       const float f = fine ? m * (a.scale_log2 / kFixed) : __int_as_float(0x7fc00000);
-      mul[c][0] = __shfl_sync(0xffffffffu, f, 8 * t);
-      mul[c][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+      mul[0] = __shfl_sync(0xffffffffu, f, 8 * t);
+      mul[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }
     // rows 16 d + g (+ 8) are channels, columns heads
-    float acc[NC][ND][4];
-    float m_run[NC][2], l_run[NC][2];
+    float acc[ND][4];
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[c][d][e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) m_run[c][k] = -INFINITY, l_run[c][k] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) acc[d][e] = 0.f;
     float v_top = 0.f;  // the accumulator holds sums over V scale / v_top
     bool ok = true;
     // unit i belongs to the pair of warps i % 2
@@ -723,125 +723,104 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
       const uint8_t* vb = kb + R::BLOCK;
       // row r of block b is token HT / 4 * (r / 2) + 2 b + r % 2 of the half
       const uint8_t* krow = kb + (half * HT + (HT / 4) * (g >> 1) + (g & 1)) * D + 16 * t;
-      float sc[NC][NB / 2][4];
+      float sc[NB / 2][4];
 #pragma unroll
       for (int b = 0; b < NB / 2; ++b) {
-        int hi[NC][4], lo[NC][4];
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) hi[c][e] = lo[c][e] = 0;
+        int hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           const uint4 x = *reinterpret_cast<const uint4*>(krow + 4 * b * D + 64 * h);
           const uint4 y = *reinterpret_cast<const uint4*>(krow + (4 * b + 2) * D + 64 * h);
           const uint32_t k0[4] = {x.x, y.x, x.y, y.y}, k1[4] = {x.z, y.z, x.w, y.w};
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            mma_s8(hi[c], k0, qh[c][h][0], qh[c][h][1]);
-            mma_s8(lo[c], k0, ql[c][h][0], ql[c][h][1]);
-            mma_s8(hi[c], k1, qh[c][h][2], qh[c][h][3]);
-            mma_s8(lo[c], k1, ql[c][h][2], ql[c][h][3]);
-          }
+          mma_s8(hi, k0, qh[h][0], qh[h][1]);
+          mma_s8(lo, k0, ql[h][0], ql[h][1]);
+          mma_s8(hi, k1, qh[h][2], qh[h][3]);
+          mma_s8(lo, k1, ql[h][2], ql[h][3]);
         }
         // |sum| <= 128 * 127 * (256 * 127 + 128) < 2^31
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[c][b][e] = (float)(hi[c][e] * 256 + lo[c][e]);
+        for (int e = 0; e < 4; ++e) sc[b][e] = (float)(hi[e] * 256 + lo[e]);
       }
       // scores in log2 units; tokens behind the end
       const int base = en.page * BT + half * HT + (HT / 4) * (g >> 1) + (g & 1);
       const bool cut = (en.page + 1) * BT > len;
-      float mx[NC][2];
+      const float f[2] = {mul[0] * en.ks, mul[1] * en.ks};
+      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const float f[2] = {mul[c][0] * en.ks, mul[c][1] * en.ks};
-        mx[c][0] = mx[c][1] = -INFINITY;
+      for (int b = 0; b < NB / 2; ++b)
 #pragma unroll
-        for (int b = 0; b < NB / 2; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            sc[c][b][e] *= f[e & 1];
-            if (cut && base + 4 * b + (e & 2) >= len) sc[c][b][e] = -INFINITY;
-            mx[c][e & 1] = fmaxf(mx[c][e & 1], sc[c][b][e]);
-          }
-      }
+        for (int e = 0; e < 4; ++e) {
+          sc[b][e] *= f[e & 1];
+          if (cut && base + 4 * b + (e & 2) >= len) sc[b][e] = -INFINITY;
+          mx[e & 1] = fmaxf(mx[e & 1], sc[b][e]);
+        }
       bool grows = fabsf(en.vs) > v_top;
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mx[c][k] = fmaxf(mx[c][k], __shfl_xor_sync(0xffffffffu, mx[c][k], 4));
-          mx[c][k] = fmaxf(mx[c][k], __shfl_xor_sync(0xffffffffu, mx[c][k], 8));
-          mx[c][k] = fmaxf(mx[c][k], __shfl_xor_sync(0xffffffffu, mx[c][k], 16));
-          grows |= mx[c][k] > m_run[c][k];
-        }
+      for (int k = 0; k < 2; ++k) {
+        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 4));
+        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 8));
+        mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 16));
+        grows |= mx[k] > m_run[k];
+      }
       if (__any_sync(0xffffffffu, grows)) {
         // a new largest V scale with some room, so that few follow
         const float top = fabsf(en.vs) > v_top ? 1.5f * fabsf(en.vs) : v_top;
         const float vf = top > v_top ? v_top / top : 1.f;
         v_top = top;
+        float by[2];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          float f[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float to = fmaxf(m_run[c][k], mx[c][k]);
-            f[k] = to > m_run[c][k] ? exp2_mufu(m_run[c][k] - to) : 1.f;
-            l_run[c][k] *= f[k];
-            m_run[c][k] = to;
-          }
-#pragma unroll
-          for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[c][d][e] *= f[e & 1] * vf;
+        for (int k = 0; k < 2; ++k) {
+          const float to = fmaxf(m_run[k], mx[k]);
+          by[k] = to > m_run[k] ? exp2_mufu(m_run[k] - to) : 1.f;
+          l_run[k] *= by[k];
+          m_run[k] = to;
         }
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[d][e] *= by[e & 1] * vf;
       }
       // weights, turned so that a thread has head g's tokens 2 t, 2 t + 1 of a block
       const float ratio = en.vs == 0.f ? 0.f : en.vs / v_top;
-      uint32_t pb[NC][NB];
-      float zeros[NC][2];
+      // so small a share of the largest V scale that weights leave fp16's normal
+      // numbers: their sum is then taken from the unrounded ones
+      const bool small = ratio < kSmallRatio;
+      uint32_t pb[NB];
+      float unrounded[2] = {0.f, 0.f}, sub[2];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        zeros[c][0] = zeros[c][1] = 0.f;
-        float sub[2];
+      for (int k = 0; k < 2; ++k)  // a head that has seen no token has maximum -inf: weights 0
+        sub[k] = kShift - (m_run[k] == -INFINITY ? 0.f : m_run[k]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)  // a head that has seen no token has maximum -inf: weights 0
-          sub[k] = kShift - (m_run[c][k] == -INFINITY ? 0.f : m_run[c][k]);
+      for (int b = 0; b < NB / 2; ++b) {
+        float p[4];
 #pragma unroll
-        for (int b = 0; b < NB / 2; ++b) {
-          float p[4];
+        for (int e = 0; e < 4; ++e) p[e] = exp2_mufu(sc[b][e] + sub[e & 1]);
+        if (small) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = exp2_mufu(sc[c][b][e] + sub[e & 1]);
-          if (ratio == 0.f) {  // a block of zeros: its weights count, its values do not
-#pragma unroll
-            for (int e = 0; e < 4; ++e) zeros[c][e & 1] += p[e];
-          }
-          pb[c][2 * b] = transpose8(pack_f16x2(p[0] * ratio, p[1] * ratio));
-          pb[c][2 * b + 1] = transpose8(pack_f16x2(p[2] * ratio, p[3] * ratio));
+          for (int e = 0; e < 4; ++e) unrounded[e & 1] += p[e];
         }
+        pb[2 * b] = transpose8(pack_f16x2(p[0] * ratio, p[1] * ratio));
+        pb[2 * b + 1] = transpose8(pack_f16x2(p[2] * ratio, p[3] * ratio));
       }
       // The weights' sum from the rounded weights, as one more row of values that are
       // all 1: what rounding moves in the sums it then moves in their divisor too.
-      const float back = ratio == 0.f ? 0.f : 1.f / ratio;
+      if (small) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
+        for (int k = 0; k < 2; ++k) {
+          float z = unrounded[k];
+          z += __shfl_xor_sync(0xffffffffu, z, 4);
+          z += __shfl_xor_sync(0xffffffffu, z, 8);
+          z += __shfl_xor_sync(0xffffffffu, z, 16);
+          l_run[k] += z;
+        }
+      } else {
         const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < NB / 2; ++k) mma_f16(sum, ones, pb[c][2 * k], pb[c][2 * k + 1]);
+        for (int k = 0; k < NB / 2; ++k) mma_f16(sum, ones, pb[2 * k], pb[2 * k + 1]);
+        const float back = 1.f / ratio;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          l_run[c][k] = fmaf(sum[k], back, l_run[c][k]);
-          if (ratio == 0.f) {
-            float z = zeros[c][k];
-            z += __shfl_xor_sync(0xffffffffu, z, 4);
-            z += __shfl_xor_sync(0xffffffffu, z, 8);
-            z += __shfl_xor_sync(0xffffffffu, z, 16);
-            l_run[c][k] += z;
-          }
-        }
+        for (int k = 0; k < 2; ++k) l_run[k] = fmaf(sum[k], back, l_run[k]);
       }
       const uint8_t* vrow = vb + g * BT + half * HT + (HT / 4) * t;
 #pragma unroll
@@ -865,85 +844,70 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
           uint32_t va[4];
           codes_to_f16(w[0][k], va[0], va[2]);
           codes_to_f16(w[1][k], va[1], va[3]);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) mma_f16(acc[c][d], va, pb[c][2 * k], pb[c][2 * k + 1]);
+          mma_f16(acc[d], va, pb[2 * k], pb[2 * k + 1]);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
     // ---- the segment's end: the warps' results become one
+    if (g == 0) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (g == 0) stat[warp][8 * c + 2 * t + k] = make_float2(m_run[c][k], l_run[c][k]);
-      }
+      for (int k = 0; k < 2; ++k) stat[warp][2 * t + k] = make_float2(m_run[k], l_run[k]);
+    }
     consumers_sync();
-    float m_all[NC][2], l_all[NC][2];
+    float m_all[2], l_all[2], by[2];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float f[2];
+    for (int k = 0; k < 2; ++k) {
+      float m = -INFINITY, l = 0.f;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int row = 8 * c + 2 * t + k;
-        float m = -INFINITY, l = 0.f;
+      for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, stat[w][2 * t + k].x);
 #pragma unroll
-        for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, stat[w][row].x);
-#pragma unroll
-        for (int w = 0; w < kConsumers; ++w) {
-          const float2 ml = stat[w][row];
-          // a NaN sum has to survive: its maximum may be -inf
-          l = fmaf(ml.y, ml.x == m ? 1.f : exp2_mufu(ml.x - m), l);
-        }
-        m_all[c][k] = m;
-        l_all[c][k] = l;
-        f[k] = (m_run[c][k] == m ? 1.f : exp2_mufu(m_run[c][k] - m)) * v_top;
+      for (int w = 0; w < kConsumers; ++w) {
+        const float2 ml = stat[w][2 * t + k];
+        // a NaN sum has to survive: its maximum may be -inf
+        l = fmaf(ml.y, ml.x == m ? 1.f : exp2_mufu(ml.x - m), l);
       }
+      m_all[k] = m;
+      l_all[k] = l;
+      by[k] = (m_run[k] == m ? 1.f : exp2_mufu(m_run[k] - m)) * v_top;
+    }
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[d][e] *= by[e & 1];
+    auto each = [&](auto&& what) {  // (value, its place in a [kRows][PITCH] array)
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[c][d][e] *= f[e & 1];
-    }
-    auto each = [&](auto&& what) {  // (value, its place in a [ROWS][PITCH] array)
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            what(acc[c][d][e], (8 * c + 2 * t + (e & 1)) * PITCH + 16 * d + g + 4 * (e & 2));
+        for (int e = 0; e < 4; ++e)
+          what(acc[d][e], (2 * t + (e & 1)) * PITCH + 16 * d + g + 4 * (e & 2));
     };
     if (warp >= 2) {
-      float* to = sums + (warp - 2) * ROWS * PITCH;
+      float* to = sums + (warp - 2) * kRows * PITCH;
       each([&](float& x, int at) { to[at] = x; });
     }
     consumers_sync();
     if (warp < 2) {
-      float* from = sums + warp * ROWS * PITCH;
+      float* from = sums + warp * kRows * PITCH;
       each([&](float& x, int at) { x += from[at]; });
       if (warp == 1) each([&](float& x, int at) { from[at] = x; });  // where it has just read
     }
     consumers_sync();
     const bool whole = begins && ends;
-    const size_t slot = ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * ROWS;
+    const size_t slot = ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kRows;
     if (warp == 0) {
-      const float* from = sums + ROWS * PITCH;
+      const float* from = sums + kRows * PITCH;
       each([&](float& x, int at) { x += from[at]; });
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        float f[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          f[k] = !whole ? 1.f : l_all[c][k] == 0.f ? 0.f : 1.f / l_all[c][k];
-          if (!whole && g == 0)
-            a.stat[slot + 8 * c + 2 * t + k] = make_float2(m_all[c][k], l_all[c][k]);
-        }
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[c][d][e] *= f[e & 1];
+      for (int k = 0; k < 2; ++k) {
+        by[k] = !whole ? 1.f : l_all[k] == 0.f ? 0.f : 1.f / l_all[k];
+        if (!whole && g == 0) a.stat[slot + 2 * t + k] = make_float2(m_all[k], l_all[k]);
       }
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[d][e] *= by[e & 1];
       each([&](float& x, int at) { sums[at] = x; });
       if (!whole && begins) {
         // the range that holds the pair's end, and so the number of parts
@@ -981,123 +945,140 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT, NC>::PER_SM)
   if (threadIdx.x == 0 && !have_cut) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
 }
 
-// Joins the parts of the pairs that were cut: a thread block per (range, row of
-// its last pair), kJoinParts threads per four channels, each taking every
-// kJoinParts-th part, so that the sums are fetched side by side.
-constexpr int kJoinParts = 8;
+// Joins the parts of the pairs that were cut: a thread block per range, for its
+// last pair. A warp takes a row, its lanes side by side along the channels; where
+// pairs are few, and so have many parts, eight warps share a row's parts and a
+// thread block has one row (one sequence of 4001 tokens: 10.5 us against 12.5; 48 of
+// 1000 tokens, eight rows per thread block: 27 us against 31). The first parts are
+// fetched before it is known whether there is anything to join (they lie in the
+// workspace anyway).
+constexpr int kJoinWarps = 8;
 
-template <int D>
-__global__ void __launch_bounds__(D / 4 * kJoinParts) k_cache_join(const AttnArgs a) {
-  __shared__ float4 sums[kJoinParts][D / 4];
-  __shared__ float weights[kJoinParts];
+template <int D, int SLICES>  // warps that share a row
+__global__ void __launch_bounds__(32 * kJoinWarps) k_cache_join(const AttnArgs a) {
+  constexpr int E = D / 32, kAhead = 8;  // channels of a lane
+  struct alignas(4 * E) Piece {
+    float x[E];
+  };
+  __shared__ Piece sums[SLICES > 1 ? SLICES : 1][32];
+  __shared__ float weights[SLICES];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the ranges' kernel is complete
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slice = warp % SLICES;
+  const int r = blockIdx.y * (kJoinWarps / SLICES) + warp / SLICES;
   const int4 cut = a.cut[blockIdx.x];
-  const int n = cut.z, r = blockIdx.y, d = threadIdx.x % (D / 4), p = threadIdx.x / (D / 4);
-  const int kvh = cut.y / a.row_groups, h0 = (cut.y - kvh * a.row_groups) * a.pass;
-  if (n == 0 || h0 + r >= a.group) return;
   // part 1 of its own range, part 0 of the following ones
-  auto at = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * a.pass + r; };
-  auto part = [&](int i) { return *reinterpret_cast<const float4*>(a.part + at(i) * D + 4 * d); };
-  constexpr int kAhead = 4;  // fetched before the maximum is known
-  float4 x[kAhead];
+  auto at = [&](int i) {
+    const int range = min((int)blockIdx.x + i, (int)gridDim.x - 1);
+    return ((size_t)range * 2 + (i == 0 ? 1 : 0)) * kRows + r;
+  };
+  auto part = [&](int i) { return *reinterpret_cast<const Piece*>(a.part + at(i) * D + E * lane); };
+  Piece x[kAhead];
   float2 ml[kAhead];
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    const int i = p + k * kJoinParts;
-    x[k] = i < n ? part(i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    ml[k] = i < n ? a.stat[at(i)] : make_float2(-INFINITY, 0.f);
+  for (int k = 0; k < 2; ++k) x[k] = part(slice + k * SLICES), ml[k] = a.stat[at(slice + k * SLICES)];
+  const int n = cut.z, kvh = cut.y / a.row_groups, h0 = (cut.y - kvh * a.row_groups) * kRows;
+  if (n == 0 || h0 + r >= a.group) return;  // with shared rows: the whole thread block
+#pragma unroll
+  for (int k = 2; k < kAhead; ++k) {
+    const int i = slice + k * SLICES;
+    if (i < n) x[k] = part(i), ml[k] = a.stat[at(i)];
   }
   float m = -INFINITY;
-  for (int i = threadIdx.x & 31; i < n; i += 32) m = fmaxf(m, a.stat[at(i)].x);
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.stat[at(i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  Piece sum = {};
   float l = 0.f;
-  auto add = [&](const float4& v, const float2& st) {
-    const float f = st.x == m ? 1.f : exp2_mufu(st.x - m);
-    sum.x = fmaf(v.x, f, sum.x);
-    sum.y = fmaf(v.y, f, sum.y);
-    sum.z = fmaf(v.z, f, sum.z);
-    sum.w = fmaf(v.w, f, sum.w);
-    l = fmaf(st.y, f, l);
-  };
+  for (int i0 = slice; i0 < n; i0 += kAhead * SLICES) {
+    if (i0 > slice) {
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) add(x[k], ml[k]);
-  for (int i = p + kAhead * kJoinParts; i < n; i += kJoinParts) add(part(i), a.stat[at(i)]);
-  sums[p][d] = sum;
-  if (d == 0) weights[p] = l;
-  __syncthreads();
-  if (p > 0) return;
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * SLICES;
+        if (i < n) x[k] = part(i), ml[k] = a.stat[at(i)];
+      }
+    }
 #pragma unroll
-  for (int i = 1; i < kJoinParts; ++i) {
-    const float4 x = sums[i][d];
-    sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
-    l += weights[i];
+    for (int k = 0; k < kAhead; ++k) {
+      if (i0 + k * SLICES >= n) break;
+      const float f = ml[k].x == m ? 1.f : exp2_mufu(ml[k].x - m);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum.x[e] = fmaf(x[k].x[e], f, sum.x[e]);
+      l = fmaf(ml[k].y, f, l);
+    }
+  }
+  if constexpr (SLICES > 1) {
+    sums[slice][lane] = sum;
+    if (lane == 0) weights[slice] = l;
+    __syncthreads();
+    if (slice > 0) return;
+#pragma unroll
+    for (int i = 1; i < SLICES; ++i) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum.x[e] += sums[i][lane].x[e];
+      l += weights[i];
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint2 o;
-  if (a.f16)
-    o = make_uint2(pack_f16x2(sum.x * inv, sum.y * inv), pack_f16x2(sum.z * inv, sum.w * inv));
-  else
-    o = make_uint2(pack_bf16x2(sum.x * inv, sum.y * inv), pack_bf16x2(sum.z * inv, sum.w * inv));
-  *reinterpret_cast<uint2*>(a.o + cut.x * a.o_stride + (kvh * a.group + h0 + r) * D + 4 * d) = o;
+  uint16_t* o = a.o + cut.x * a.o_stride + (kvh * a.group + h0 + r) * D + E * lane;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    reinterpret_cast<uint32_t*>(o)[e / 2] = a.f16
+                                                ? pack_f16x2(sum.x[e] * inv, sum.x[e + 1] * inv)
+                                                : pack_bf16x2(sum.x[e] * inv, sum.x[e + 1] * inv);
 }
 
-// Query heads of a group that share a pass over the cache: 8, or 16 where more.
-inline int pass_of(int group) { return group > 8 ? 8 * kMaxCols : 8; }
-
 // Thread blocks of an attention call: as many as run at once, at most one per
-// kMinUnits units of tables that are full.
-template <int D, int BT, int NC>
+// kMinUnits units of tables that are full, or per pair of a sequence and heads.
+template <int D, int BT>
 int ranges_of(int n_seq, int heads, int width) {
   const long long units = (long long)n_seq * heads * width;
-  const long long most = (long long)num_sms() * Ring<D, BT, NC>::PER_SM;
-  const long long n = (units + kMinUnits - 1) / kMinUnits;
+  const long long most = (long long)num_sms() * Ring<D, BT>::PER_SM;
+  const long long pairs = width > 0 ? (long long)n_seq * heads : 0;
+  const long long n = std::max((units + kMinUnits - 1) / kMinUnits, pairs);
   return (int)(n < most ? n : most);
 }
 
-template <int D, int BT, int NC>
+template <int D, int BT>
 size_t workspace_of(int n_seq, int heads, int width) {
-  return (size_t)ranges_of<D, BT, NC>(n_seq, heads, width) *
-         (2 * 8 * NC * (D * 4 + 8) + sizeof(int4));
+  return (size_t)ranges_of<D, BT>(n_seq, heads, width) *
+         (2 * kRows * (D * 4 + 8) + sizeof(int4));
 }
 
-template <int D, int BT, int NC>
+template <int D, int BT>
 cudaError_t run_attention(AttnArgs& a, void* ws, cudaStream_t st) {
-  using R = Ring<D, BT, NC>;
-  cudaError_t e = cudaFuncSetAttribute(k_cache_attention<D, BT, NC>,
+  using R = Ring<D, BT>;
+  cudaError_t e = cudaFuncSetAttribute(k_cache_attention<D, BT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, R::BYTES);
   if (e != cudaSuccess) return e;
-  const int ranges = ranges_of<D, BT, NC>(a.n_seq, a.kv_heads * a.row_groups, a.width);
+  const int ranges = ranges_of<D, BT>(a.n_seq, a.kv_heads * a.row_groups, a.width);
   a.part = static_cast<float*>(ws);
-  a.stat = reinterpret_cast<float2*>(a.part + (size_t)ranges * 2 * R::ROWS * D);
-  a.cut = reinterpret_cast<int4*>(a.stat + (size_t)ranges * 2 * R::ROWS);
-  k_cache_attention<D, BT, NC><<<(unsigned)ranges, kAttnThreads, R::BYTES, st>>>(a);
+  a.stat = reinterpret_cast<float2*>(a.part + (size_t)ranges * 2 * kRows * D);
+  a.cut = reinterpret_cast<int4*>(a.stat + (size_t)ranges * 2 * kRows);
+  k_cache_attention<D, BT><<<(unsigned)ranges, kAttnThreads, R::BYTES, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // launched while the ranges run, to wait for them on the GPU
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ranges, (unsigned)(a.group < a.pass ? a.group : a.pass));
-  cfg.blockDim = dim3(D / 4 * kJoinParts);
+  const bool many_parts = 8ll * a.n_seq * a.kv_heads * a.row_groups <= ranges;
+  cfg.gridDim = dim3((unsigned)ranges, (unsigned)(!many_parts ? 1 : min(a.group, kRows)));
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_cache_join<D>, a);
+  return many_parts ? cudaLaunchKernelEx(&cfg, k_cache_join<D, kJoinWarps>, a)
+                    : cudaLaunchKernelEx(&cfg, k_cache_join<D, 1>, a);
 }
 
-// F<head_dim, block_tokens, column tiles>(...) for a cache and a group.
-#define H3_BY_CACHE(F, c, pass, ...)                                                       \
-  ((c).head_dim == 128                                                                     \
-       ? (pass) == 8 ? H3_BY_BLOCK(F, 128, 1, c, __VA_ARGS__)                              \
-                     : H3_BY_BLOCK(F, 128, 2, c, __VA_ARGS__)                              \
-       : (pass) == 8 ? H3_BY_BLOCK(F, 64, 1, c, __VA_ARGS__)                               \
-                     : H3_BY_BLOCK(F, 64, 2, c, __VA_ARGS__))
-#define H3_BY_BLOCK(F, D, NC, c, ...)                                                      \
-  ((c).block_tokens == 32   ? F<D, 32, NC>(__VA_ARGS__)                                    \
-   : (c).block_tokens == 64 ? F<D, 64, NC>(__VA_ARGS__)                                    \
-                            : F<D, 128, NC>(__VA_ARGS__))
+// F<head_dim, block_tokens>(...) for a cache.
+#define H3_BY_CACHE(F, c, ...)                                       \
+  ((c).head_dim == 128 ? H3_BY_BLOCK(F, 128, c, __VA_ARGS__)         \
+                       : H3_BY_BLOCK(F, 64, c, __VA_ARGS__))
+#define H3_BY_BLOCK(F, D, c, ...)                                    \
+  ((c).block_tokens == 32   ? F<D, 32>(__VA_ARGS__)                  \
+   : (c).block_tokens == 64 ? F<D, 64>(__VA_ARGS__)                  \
+                            : F<D, 128>(__VA_ARGS__))
 
 template <h3_type T, int D>
 cudaError_t run_store(StoreArgs a, int block_tokens, cudaStream_t st) {
@@ -1153,9 +1134,8 @@ cudaError_t launch_kv_cache_store(const h3_kv_cache& c, int n_seq, int max_new,
 }
 
 size_t cache_attention_workspace(const h3_kv_cache& c, int n_seq, int q_heads, int width) {
-  const int group = q_heads / c.kv_heads, pass = pass_of(group);
-  const int heads = c.kv_heads * ((group + pass - 1) / pass);
-  return H3_BY_CACHE(workspace_of, c, pass, n_seq, heads, width);
+  const int heads = c.kv_heads * ((q_heads / c.kv_heads + kRows - 1) / kRows);
+  return H3_BY_CACHE(workspace_of, c, n_seq, heads, width);
 }
 
 cudaError_t launch_cache_attention(const h3_kv_cache& c, int n_seq, int q_heads,
@@ -1178,13 +1158,12 @@ cudaError_t launch_cache_attention(const h3_kv_cache& c, int n_seq, int q_heads,
   a.n_blocks = c.n_blocks;
   a.kv_heads = c.kv_heads;
   a.group = q_heads / c.kv_heads;
-  a.pass = pass_of(a.group);
-  a.row_groups = (a.group + a.pass - 1) / a.pass;
+  a.row_groups = (a.group + kRows - 1) / kRows;
   a.width = width;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.f16 = f16;
   a.err = err;
-  return H3_BY_CACHE(run_attention, c, a.pass, a, ws, st);
+  return H3_BY_CACHE(run_attention, c, a, ws, st);
 }
 
 }  // namespace h3

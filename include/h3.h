@@ -661,7 +661,9 @@ H3_API h3_status h3_kv_cache_store(const h3_kv_cache* cache, int n_seq, int max_
  * counts as tokens that are not there: both record an error (h3_text_error,
  * H3_ERR_LAYOUT). ws: h3_cache_attention_workspace_size bytes (a few MB at most),
  * used only during the call's work: calls that overlap on the GPU need one each.
- * The result does not depend on the order in which the GPU runs things. Enqueues. */
+ * The result does not depend on the order in which the GPU runs things. Values are
+ * summed relative to the largest V scale of the sequence and kv head, to about
+ * 2^-24 of its largest value. Enqueues. */
 H3_API size_t h3_cache_attention_workspace_size(const h3_kv_cache* cache, int n_seq, int q_heads,
                                                 int table_width);
 H3_API h3_status h3_cache_attention(const h3_kv_cache* cache, int n_seq, int q_heads,

@@ -330,6 +330,29 @@ def test_attention_of_large_queries():
     _check_attention([500, 40], 4, 2, 64, 64, BF, boost=8.0)
 
 
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_attention_over_v_scales_far_apart(dtype, order):
+    """Blocks whose V scales differ by up to all of float32's range, the smallest
+    subnormal or zero, first or last: a token's weight counts whatever its value's
+    size. Values are summed relative to the largest V scale: 2^-24 of that."""
+    BT = 32
+    lengths, QH, KH, D = [9 * BT - 5, 300 * BT], 5, 1, 64
+    cache = Cache(lengths, KH, D, BT)
+    factors = [1.0, 2.0 ** -7, 2.0 ** -9, 2.0 ** -14, 2.0 ** -20, 2.0 ** -31, 2.0 ** -80, 1e-39, 0.0]
+    for s, n in enumerate(lengths):
+        blocks = cache.table[s, :-(-n // BT)].long()
+        f = torch.tensor([factors[::order][i * len(factors) // len(blocks)]
+                          for i in range(len(blocks))], device=DEV)
+        cache.vs[blocks] *= f[:, None]
+    q = torch.randn(2, QH, D, generator=gen(3), device=DEV).to(dtype)
+    o = cache.attend(q, 0.125)
+    ref, a = _attention_formula(cache, q, lengths, 0.125)
+    largest = 127 * float(cache.vs.max())
+    assert_within(o, ref, a * (2.0 ** -11 + 2.4e-4) + ref.abs() * STEP[dtype] * 1.01
+                  + largest * 2.0 ** -24 + 64 * TINY[dtype])
+
+
 def test_attention_is_the_same_every_time():
     cache, q, o = _check_attention([5000, 17, 2222], 8, 2, 128, 64, BF)
     for _ in range(5):

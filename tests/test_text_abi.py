@@ -152,10 +152,10 @@ def test_cache_attention_workspace_size():
     c = _cache()
     size = h3.h3_cache_attention_workspace_size
     assert size(c, 0, 8, 9) == 0 == size(c, 1, 7, 9) == size(c, 1, 8, 0)
-    # two parts of 16 rows of 128 sums and two statistics per range, at most three
+    # two parts of 8 rows of 128 sums and two statistics per range, at most three
     # ranges per SM whatever the number of sequences
     assert 0 < size(c, 1, 8, 1) < size(c, 2, 8, 40) < size(c, 40, 8, 375)
-    assert size(c, 40, 8, 375) == size(c, 4000, 8, 375) <= 3 * 148 * (2 * 16 * (128 * 4 + 8) + 16)
+    assert size(c, 40, 8, 375) == size(c, 4000, 8, 375) <= 3 * 148 * (2 * 8 * (128 * 4 + 8) + 16)
     with pytest.raises(h3.H3Error) as e:
         import torch
         h3.make_kv_cache(torch.zeros(1, 1, 32, 64), torch.zeros(1, 1, 32, 64), None, None)
