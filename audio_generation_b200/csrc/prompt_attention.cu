@@ -53,10 +53,13 @@ struct Bars {
       p_full[2], o_final[2], o_free[2], drain;
 };
 
-// 2^f on the FMA pipe, f in [-1/2, 1/2]: the packed-sequence attention kernel's
-// cubic (relative error at most 7.7e-5), and which of 32 key pairs take it.
-constexpr float kExpC3 = 0.05508868396f, kExpC2 = 0.24260404706f, kExpC1 = 0.69327622652f,
-                kExpC0 = 0.99992895126f;
+// 2^f on the FMA pipe, f in [-1/2, 1/2]: the cubic of least largest relative error
+// (1.02e-4) among those that are 1 at 0, and which of 32 key pairs take it. With
+// arguments limited to -127 and more it then gives 0 there, and so to masked keys
+// (2^-126, say, times the largest v would be more than 1). A NaN gives the largest
+// number, which as a weight becomes infinite and so marks its row.
+constexpr float kExpC3 = 0.05500905961f, kExpC2 = 0.24221096933f, kExpC1 = 0.69328290224f,
+                kExpC0 = 1.f, kExpLowest = -127.f;
 constexpr float kRoundMagic = 12582912.f;  // 1.5 * 2^23
 constexpr uint32_t kCubicPairs = 0x20820820u;  // every sixth
 
@@ -434,7 +437,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint64_t x2 = f2_fma(f2_pack(sc[key], sc[key + 1]), scale2, negm2);
           float p0, p1;
           if ((kCubicPairs >> e) & 1u) {
-            exp2_cubic2(x2, Cubic{kExpC3, kExpC2, kExpC1, kExpC0, kRoundMagic}, p0, p1);
+            f2_unpack(x2, p0, p1);
+            exp2_cubic2_clamped(f2_pack(max_nan(p0, kExpLowest), max_nan(p1, kExpLowest)),
+                                Cubic{kExpC3, kExpC2, kExpC1, kExpC0, kRoundMagic}, p0, p1);
           } else {
             f2_unpack(x2, p0, p1);
             p0 = exp2_mufu(p0);

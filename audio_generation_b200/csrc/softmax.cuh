@@ -40,15 +40,13 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 
 // 2^x for two values on the FMA pipe: x = j + f with j = round(x) (by adding
 // `magic` = 1.5 * 2^23, which leaves the integer in the low mantissa bits) and f
-// in [-1/2, 1/2], 2^f by a cubic, j added to the exponent. Inputs below -126 are
-// clamped.
+// in [-1/2, 1/2], 2^f by a cubic, j added to the exponent. Inputs are at least -126,
+// or -127 where the cubic is 1 at 0 (0 then comes out).
 struct Cubic {
   float c3, c2, c1, c0, magic;
 };
-__device__ __forceinline__ void exp2_cubic2(uint64_t x2, const Cubic& c, float& p0, float& p1) {
-  float x0, x1;
-  f2_unpack(x2, x0, x1);
-  const uint64_t xc = f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+__device__ __forceinline__ void exp2_cubic2_clamped(uint64_t xc, const Cubic& c, float& p0,
+                                                    float& p1) {
   const uint64_t t = f2_add(xc, f2_pack(c.magic, c.magic));
   const uint64_t jf = f2_add(t, f2_pack(-c.magic, -c.magic));  // j, exact
   const uint64_t f = f2_fma(jf, f2_pack(-1.f, -1.f), xc);      // x - j, exact
@@ -60,6 +58,11 @@ __device__ __forceinline__ void exp2_cubic2(uint64_t x2, const Cubic& c, float& 
   f2_unpack(t, t0, t1);
   p0 = __int_as_float(__float_as_int(q0) + (__float_as_int(t0) << 23));
   p1 = __int_as_float(__float_as_int(q1) + (__float_as_int(t1) << 23));
+}
+__device__ __forceinline__ void exp2_cubic2(uint64_t x2, const Cubic& c, float& p0, float& p1) {
+  float x0, x1;
+  f2_unpack(x2, x0, x1);
+  exp2_cubic2_clamped(f2_pack(fmaxf(x0, -126.f), fmaxf(x1, -126.f)), c, p0, p1);
 }
 
 __device__ __forceinline__ float fma_01(float a, float b, float c) {  // limited to [0, 1]

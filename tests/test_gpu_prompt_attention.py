@@ -178,6 +178,37 @@ def test_non_finite_values_stay_with_the_rows_that_attend_them(bad, QH, KH):
             assert torch.equal(o[keep], clean[keep])
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_nan_key_reaches_every_row_behind_it(D, dtype):
+    """At any place among the keys of a tile: the rows from it on are NaN, no other."""
+    lengths = [140] * 66
+
+    def poison(q, k, v):
+        for i in range(66):
+            k[140 * i + 2 * i + 1, 0, 3] = float("nan")
+
+    o = _run(lengths, 2, 1, D, dtype, prepare=poison)[3].view(66, 140, 2, D)
+    rows = torch.arange(140, device=DEV)
+    reached = rows >= 2 * torch.arange(66, device=DEV)[:, None] + 1
+    assert torch.equal(torch.isnan(o).all(-1).all(-1), reached)
+    assert torch.equal(torch.isfinite(o).all(-1).all(-1), ~reached)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_the_largest_values_behind_a_row_do_not_reach_it(dtype):
+    """The type's largest number in v at every later token, at both signs: not a bit
+    of the rows before changes."""
+    lengths, hit = [150, 300, 40], 150 + 101
+    clean = _run(lengths, 5, 1, 128, dtype)[3]
+
+    def largest(q, k, v):
+        v[hit:] = torch.finfo(dtype).max
+        v[hit::2] *= -1
+
+    assert torch.equal(_run(lengths, 5, 1, 128, dtype, prepare=largest)[3][:hit], clean[:hit])
+
+
 def test_garbage_behind_the_last_prompt_is_not_read_into_it():
     def garbage(q, k, v):
         for x in (q, k, v):

@@ -174,13 +174,34 @@ def test_binding_refuses_values_of_the_wrong_device():
     assert h3._dev_ptr(None, 0, "x") is None and h3._dev_ptr(4096, 0, "x") == 4096
 
 
-def test_prompt_attention_has_the_checked_cubic():
-    """The part of the exponentials on the FMA pipe: the same coefficients as in the
-    packed-sequence kernel, whose error bound is checked against float64."""
-    csrc = os.path.join(os.path.dirname(h3.__file__), "csrc")
-    values = []
-    for name in ("attention.cu", "prompt_attention.cu"):
-        src = open(os.path.join(csrc, name)).read()
-        values.append([re.search(r"\b%s\s*=\s*([\d.]+)f" % c, src).group(1)
-                       for c in ("kExpC3", "kExpC2", "kExpC1", "kExpC0", "kRoundMagic")])
-    assert values[0] == values[1]
+def test_exp2_cubic_of_prompt_attention():
+    """The part of its exponentials on the FMA pipe, in the kernel's float32 steps
+    with the coefficients its source has: within the bound stated there, exactly 0
+    for masked keys, and a NaN as the largest number."""
+    np = pytest.importorskip("numpy")
+    src = open(os.path.join(os.path.dirname(h3.__file__), "csrc", "prompt_attention.cu")).read()
+    c3, c2, c1, c0, magic, low = (
+        np.float32(re.search(r"\b%s = (-?[\d.]+)f" % c, src).group(1))
+        for c in ("kExpC3", "kExpC2", "kExpC1", "kExpC0", "kRoundMagic", "kExpLowest"))
+    bound = float(re.search(r"relative error\n// \(([\de.-]+)\)", src).group(1))
+
+    def fma(a, b, c):  # the float64 product of float32 operands is exact
+        return (a.astype(np.float64) * b + np.float64(c)).astype(np.float32)
+
+    def exp2(x):
+        x = np.maximum(x, low)  # a NaN stays
+        x = np.where(np.isnan(x), np.uint32(0x7fffffff).view(np.float32), x)  # as on the GPU
+        t = x + magic
+        f = x - (t - magic)
+        p = fma(fma(fma(np.full_like(f, c3), f, c2), f, c1), f, c0)
+        bits = p.view(np.int32).astype(np.int64) + (t.view(np.int32).astype(np.int64) << 23)
+        return (bits & 0xFFFFFFFF).astype(np.uint32).view(np.float32)
+
+    x = np.concatenate([np.linspace(-125, 15, 1400001),
+                        np.linspace(-0.5, 0.5, 200001)]).astype(np.float32)
+    rel = np.abs(exp2(x).astype(np.float64) / np.exp2(x.astype(np.float64)) - 1).max()
+    assert 0.9 * bound < rel <= bound
+    assert (exp2(np.array([-127, -128, -1e30, -np.inf], np.float32)) == 0).all()
+    below = exp2(np.linspace(-127, -125, 100001).astype(np.float32))
+    assert (below >= 0).all() and below.max() <= 2.0 ** -125 * 1.001
+    assert exp2(np.array([np.nan], np.float32))[0] == np.finfo(np.float32).max
