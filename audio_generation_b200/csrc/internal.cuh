@@ -85,7 +85,9 @@ struct h3_layout {
 struct h3_prompts {
   int device = 0, q_heads = 0, kv_heads = 0, head_dim = 0;
   int rows = 0;     // rows of the packed buffers up to the last prompt's end
-  int n_items = 0;  // two query tiles each
+  int longest = 0;  // tokens of the longest prompt
+  bool brief = false;  // the short prompts' form
+  int n_items = 0;     // two query tiles each, or the short form's rows
   void* items = nullptr;  // device int4 [n_items]
 };
 

@@ -43,8 +43,8 @@ def _reference(q, k, v, offsets, scale):
 def _allowed(o, a, dtype):
     """The weights are rounded to `dtype` (half a step of each), their exponents
     come from float32 scores of D terms (below 1e-4 for the inputs here: 128 x
-    2^-24 x sum |q k| scale, |q k| about 7) and a 2^-22 exponential; the result is
-    rounded once."""
+    2^-24 x sum |q k| scale, |q k| about 7) and an exponential within 1.02e-4: 2^-12
+    together; the result is rounded once."""
     return a * (STEP[dtype] + 2.0 ** -12) + o.abs() * STEP[dtype] * 1.01 + 64 * TINY[dtype]
 
 
@@ -90,6 +90,46 @@ def test_group_sizes(QH, KH, D, dtype):
 def test_lengths(lengths, dtype):
     _check(lengths, 4, 2, 128, dtype)
     _check(lengths, 3, 3, 64, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("QH,KH,lengths", [
+    (1, 1, [1, 17, 2, 60, 77, 5, 128, 33, 0, 64]), (14, 2, [1, 17, 2, 60, 77, 5, 128, 33, 0, 64]),
+    (5, 5, [127, 128, 126]), (24, 1, [3, 31, 32, 33]), (128, 1, [9, 30, 2]), (100, 1, [1]),
+    (40, 8, [8] * 31), (3, 1, [21, 22, 43])])
+def test_short_prompts(QH, KH, lengths, D, dtype):
+    """Batches without a prompt of more than 128 tokens, as few as take their own form."""
+    _check(lengths, QH, KH, D, dtype, first=3, tail=70)
+
+
+def test_many_short_prompts():
+    """So many that the other form is taken again."""
+    _check([100, 37, 128, 5] * 24, 24, 2, 128, BF)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_non_finite_values_in_short_prompts(bad, dtype):
+    lengths, QH, KH, hit = [40, 90, 30], 6, 2, 40 + 17
+
+    def poison(q, k, v):
+        v[hit, 1, 70] = bad
+        v[hit + 1:40 + 90, 0] = torch.finfo(dtype).max
+        q[3, 2, 9] = float("nan")
+        k[40 + 90 + 11, 0, 4] = float("nan")
+
+    clean, o = (_run(lengths, QH, KH, 128, dtype, prepare=f)[3] for f in (None, poison))
+    touched = torch.zeros(sum(lengths), QH, dtype=torch.bool, device=DEV)
+    touched[hit:130, 3:] = True      # rows that attend the bad v
+    touched[hit + 1:130, :3] = True  # and the largest
+    touched[3, 2] = True
+    touched[141:, :3] = True
+    diff = (o.double() - clean.double()).abs()[~touched]
+    assert bool((diff <= 3 * STEP[dtype] * (clean.double().abs()[~touched] + 1)).all())
+    assert not bool(torch.isfinite(o[hit:130, 3:, 70]).any())
+    assert bool(torch.isfinite(o[hit:130, 3:, :70]).all())
+    assert bool(torch.isnan(o[3, 2]).all()) and bool(torch.isnan(o[141:, :3]).all())
 
 
 def test_long_prompt():
