@@ -540,13 +540,13 @@ bool tmap_heads(CUtensorMap* t, const void* p, bool f16, int D, int heads, int r
 }
 
 // ---------------------------------------------------------- short prompts only
-// Where every prompt has at most 128 tokens the time is a chain of latencies, and
+// Where every prompt has at most 256 tokens the time is a chain of latencies, and
 // the form above makes it long: one item at a time per SM, its tiles mostly empty.
 // Here a thread block takes 64 (position, head) rows of a prompt and kv head, many
 // per SM; keys and values up to its last row's position go to shared memory at
 // once, and each of four warps takes 16 rows through warp-level MMAs, 32 keys at a
 // time with a running maximum and sum.
-constexpr int kShortKeys = 128;  // the longest prompt of a batch that comes here
+constexpr int kShortKeys = 256;  // the longest prompt of a batch that comes here
 constexpr int kShortRows = 64;
 
 __device__ __forceinline__ void copy_16(uint32_t dst, const void* src, bool there) {
@@ -755,7 +755,8 @@ cudaError_t run(const h3_prompts* p, const Args& a, cudaStream_t st) {
 // block of the short form costs with its keys and channels, an item of the other 20
 // or 30, and 2.3 us more come before and behind its items. (64 prompts of 3 to 77
 // tokens, 14 heads over 2 x 64: 6.3 us against 10.2; 31 of 8, 40 over 8 x 64: 4.6
-// against 9.2; 32 of 100, 40 over 8 x 128: 48 against 24.)
+// against 9.2; 32 of 100, 40 over 8 x 128: 48 against 24; one of 256, 40 over 8 x 64:
+// 8.3 against 8.7.)
 bool short_is_faster(const h3_prompts* p, long long pairs, long long blocks) {
   return p->kv_heads * blocks * (p->head_dim / 64) * (4.5 + 0.05 * p->longest) <
          p->kv_heads * pairs * (p->head_dim == 128 ? 30. : 20.) + 2300.;

@@ -97,9 +97,9 @@ def test_lengths(lengths, dtype):
 @pytest.mark.parametrize("QH,KH,lengths", [
     (1, 1, [1, 17, 2, 60, 77, 5, 128, 33, 0, 64]), (14, 2, [1, 17, 2, 60, 77, 5, 128, 33, 0, 64]),
     (5, 5, [127, 128, 126]), (24, 1, [3, 31, 32, 33]), (128, 1, [9, 30, 2]), (100, 1, [1]),
-    (40, 8, [8] * 31), (3, 1, [21, 22, 43])])
+    (40, 8, [8] * 31), (3, 1, [21, 22, 43]), (8, 8, [140]), (4, 2, [256, 3, 255])])
 def test_short_prompts(QH, KH, lengths, D, dtype):
-    """Batches without a prompt of more than 128 tokens, as few as take their own form."""
+    """Batches without a prompt of more than 256 tokens, as few as take their own form."""
     _check(lengths, QH, KH, D, dtype, first=3, tail=70)
 
 
