@@ -87,7 +87,8 @@ struct h3_prompts {
   int rows = 0;     // rows of the packed buffers up to the last prompt's end
   int longest = 0;  // tokens of the longest prompt
   bool brief = false;  // the short prompts' form
-  int n_items = 0;     // two query tiles each, or the short form's rows
+  bool single = false; // items of one query tile
+  int n_items = 0;     // two query tiles each, one, or the short form's rows
   void* items = nullptr;  // device int4 [n_items]
 };
 
