@@ -1056,6 +1056,7 @@ cudaError_t run_attention(AttnArgs& a, void* ws, cudaStream_t st) {
   a.cut = reinterpret_cast<int4*>(a.stat + (size_t)ranges * 2 * kRows);
   k_cache_attention<D, BT><<<(unsigned)ranges, kAttnThreads, R::BYTES, st>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (a.width == 1) return cudaSuccess;  // pairs of one block: none is cut
   // launched while the ranges run, to wait for them on the GPU
   cudaLaunchConfig_t cfg = {};
   const bool many_parts = 8ll * a.n_seq * a.kv_heads * a.row_groups <= ranges;

@@ -568,11 +568,14 @@ def _dev_ptr(t, device: int, where: str) -> Optional[int]:
     """Address of a tensor that has to be on the current device (an int or None
     as it is): a host tensor's address, or another device's, is refused here,
     where the kernel would fault on it."""
-    if t is None or isinstance(t, int):
-        return t
-    if t.get_device() != device:
-        raise H3Error(H3_ERR_ARG, f"{where}: tensor on {t.device}, current device {device}")
-    return t.data_ptr()
+    try:
+        if t.get_device() == device:
+            return t.data_ptr()
+    except AttributeError:
+        if t is None or isinstance(t, int):
+            return t
+        raise
+    raise H3Error(H3_ERR_ARG, f"{where}: tensor on {t.device}, current device {device}")
 
 
 def h3_quantize_int8_rows(dtype, rows: int, K: int, x, x_stride: int, codes, scales,
