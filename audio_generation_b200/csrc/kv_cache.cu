@@ -35,10 +35,13 @@ __device__ __forceinline__ int block_of(const int32_t* table, int width, int seq
 // stores run along the tokens. Where most pairs of a sequence and a block up to
 // max_new would be empty, a thread block finds its pair by a scan over the
 // sequences. 18400 tokens of 8 heads x 128 in 16 sequences (113 MB in and out):
-// 31 us (34 without the scan), six waves of one chain each (sequence, values, scale,
+// 30.6 us (34 without the scan), six waves of one chain each (sequence, values, scale,
 // codes); two thread blocks per SM 37 us, four, whose registers spill, 35 us. One
 // token of each of 48 sequences: 4.3 us.
-constexpr int kStoreThreads = 256;
+// As many threads as a block has groups of four slots and eight channels (with 256
+// for all, 36000 tokens of 8 heads x 64, 32 per block: 73 us against 27).
+template <int D, int BT>
+constexpr int kStoreThreads = BT * D / 32 < 256 ? BT * D / 32 : 256;
 
 struct StoreArgs {
   const int32_t *table, *lengths, *offsets;
@@ -74,11 +77,11 @@ __device__ __forceinline__ int blocks_touched(const Arrival& r) {
 
 // The unit-th cache block of all that the sequences touch, in their order: a scan
 // over the sequences by the thread block. False past the last.
-template <int BT>
+template <int BT, int THREADS>
 __device__ __forceinline__ bool find_unit(const StoreArgs& a, int unit, int* sums, int* found,
                                           Arrival* which) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int each = (a.n_seq + kStoreThreads - 1) / kStoreThreads;
+  const int each = (a.n_seq + THREADS - 1) / THREADS;
   const int begin = min(t * each, a.n_seq), end = min(begin + each, a.n_seq);
   int mine = 0;
   for (int s = begin; s < end; ++s) {
@@ -157,11 +160,12 @@ __device__ __forceinline__ uint2 vec_codes(const uint4& u, const BlockScale& b) 
 template <h3_type T, int D, int BT>
 __device__ __forceinline__ void store_block(const StoreArgs& a, int seq, int nth, int head,
                                             const Arrival& r, uint32_t* turned,
-                                            float (*part)[kStoreThreads / 32]) {
+                                            float (*part)[kStoreThreads<D, BT> / 32]) {
+  constexpr int THREADS = kStoreThreads<D, BT>;
   constexpr int RV = D / 8;                 // 16-byte vectors per token
   constexpr int WR = BT / 4;                // words of four slots per channel
   constexpr int GROUPS = WR * RV;           // (word, vector) pairs
-  constexpr int NG = (GROUPS + kStoreThreads - 1) / kStoreThreads;
+  constexpr int NG = (GROUPS + THREADS - 1) / THREADS;
   const int t = threadIdx.x;
   const int before = r.before, first = r.first, count = r.count;
   const int page = before / BT + nth;
@@ -173,7 +177,7 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, int seq, int nth
 
   // the thread's groups: four slots from 4 word on, eight channels from 8 vec on
   const int vec = t % RV, word0 = t / RV;
-  constexpr int WORDS = kStoreThreads / RV;  // word step between a thread's groups
+  constexpr int WORDS = THREADS / RV;  // word step between a thread's groups
   uint4 u[2][NG][4];
   const long long row0 = (long long)first + page * BT - before;  // row of slot 0
 #pragma unroll
@@ -210,7 +214,7 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, int seq, int nth
   BlockScale bs[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const float m = warp_peak(part[w][t % (kStoreThreads / 32)]);
+    const float m = warp_peak(part[w][t % (THREADS / 32)]);
     bs[w] = block_scale<T>(m, old[w], held > 0, a.scales[w] + at, t == 0);
   }
   uint8_t* kc = a.codes[0] + at * (BT * D);
@@ -244,7 +248,7 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, int seq, int nth
     }
   }
   if (bs[0].again)
-    for (int i = t; i < held * D / 4; i += kStoreThreads) {
+    for (int i = t; i < held * D / 4; i += THREADS) {
       uint32_t* p = reinterpret_cast<uint32_t*>(kc) + i;
       *p = word_again(*p, bs[0]);
     }
@@ -252,9 +256,9 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, int seq, int nth
   const bool zero = bs[1].zero;
   if (whole) {
 #pragma unroll
-    for (int i = 0; i < D * WR / 4; i += kStoreThreads) {
+    for (int i = 0; i < D * WR / 4; i += THREADS) {
       const int d = (i + t) / (WR / 4), q = (i + t) % (WR / 4) * 4;
-      if (D * WR / 4 % kStoreThreads != 0 && i + t >= D * WR / 4) break;
+      if (D * WR / 4 % THREADS != 0 && i + t >= D * WR / 4) break;
       const uint32_t* row = turned + d * WR;
       const int f = (d / 8) & (WR - 1);
       uint4 c = make_uint4(row[q ^ f], row[(q + 1) ^ f], row[(q + 2) ^ f], row[(q + 3) ^ f]);
@@ -265,7 +269,7 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, int seq, int nth
   }
   const bool again = bs[1].again;
   const int w0 = (again ? 0 : slot0) / 4, words = (to + 3) / 4 - w0;
-  for (int i = t; i < D * words; i += kStoreThreads) {
+  for (int i = t; i < D * words; i += THREADS) {
     const int d = i % D, word = w0 + i / D;
     uint32_t c = turned[d * WR + (word ^ ((d / 8) & (WR - 1)))];
     if (zero) c = 0;
@@ -287,18 +291,20 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, int seq, int nth
 }
 
 template <h3_type T, int D, int BT>
-__global__ void __launch_bounds__(kStoreThreads, BT * D >= 16384 ? 2 : 3)
+__global__ void __launch_bounds__(kStoreThreads<D, BT>,
+                                  (BT * D >= 16384 ? 512 : 768) / kStoreThreads<D, BT>)
     k_kv_store(const StoreArgs a) {
+  constexpr int THREADS = kStoreThreads<D, BT>;
   __shared__ uint32_t turned[D * BT / 4];
-  __shared__ float part[2][kStoreThreads / 32];
-  __shared__ int sums[kStoreThreads / 32], found[2];
+  __shared__ float part[2][THREADS / 32];
+  __shared__ int sums[THREADS / 32], found[2];
   __shared__ Arrival which;
   const int head = blockIdx.x % a.kv_heads;
   const int unit = blockIdx.x / a.kv_heads;
   int seq, nth;
   Arrival r;
   if (a.search) {
-    if (!find_unit<BT>(a, unit, sums, found, &which)) return;
+    if (!find_unit<BT, THREADS>(a, unit, sums, found, &which)) return;
     seq = found[0];
     nth = found[1];
     r = which;
@@ -1092,9 +1098,9 @@ cudaError_t run_store(StoreArgs a, int block_tokens, cudaStream_t st) {
   a.search = most < units;
   if (a.search) units = most;
   const unsigned grid = (unsigned)(units * a.kv_heads);
-  if (block_tokens == 32) k_kv_store<T, D, 32><<<grid, kStoreThreads, 0, st>>>(a);
-  else if (block_tokens == 64) k_kv_store<T, D, 64><<<grid, kStoreThreads, 0, st>>>(a);
-  else k_kv_store<T, D, 128><<<grid, kStoreThreads, 0, st>>>(a);
+  if (block_tokens == 32) k_kv_store<T, D, 32><<<grid, kStoreThreads<D, 32>, 0, st>>>(a);
+  else if (block_tokens == 64) k_kv_store<T, D, 64><<<grid, kStoreThreads<D, 64>, 0, st>>>(a);
+  else k_kv_store<T, D, 128><<<grid, kStoreThreads<D, 128>, 0, st>>>(a);
   return cudaGetLastError();
 }
 
