@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(kStoreThreads<D, BT>,
 // does not grow with the sequences.
 //
 // A thread block has one producer warp, which streams cache blocks into shared-
-// memory stages with bulk copies, and four consumer warps: two pairs take the
-// stages in turn, the warps of a pair half the tokens each, every warp with its
+// memory stages with bulk copies, and four consumer warps in teams of two (or one)
+// that take the stages in turn, a team's warps half the tokens each, every warp with its
 // own running maximum, sum and accumulator (joined at the end of a segment), so
 // that nothing waits but on its data.
 //
@@ -374,10 +374,13 @@ struct Ring {
   // thread blocks per SM: three where the accumulators leave the registers for it
   static constexpr int PER_SM = BLOCK >= 16384 ? 2 : 3;
   static constexpr int FIT = (PER_SM == 2 ? 98304 : 65536) / (2 * BLOCK);
-  // Even, so that a stage always serves the same pair of warps: a warp that waits
-  // for a stage's next fill has then seen its last one, and cannot take an older
+  // Warps that share a unit (small ones are a warp's alone: 48 sequences of 3000 tokens,
+  // 40 heads over 8 x 64, 34 us against 36), and how many such teams there are.
+  static constexpr int TEAM = BLOCK <= 4096 ? 1 : 2, TEAMS = kConsumers / TEAM;
+  // A multiple of the teams, so that a stage always serves the same one: a warp that
+  // waits for a stage's next fill has then seen its last one, and cannot take an older
   // phase of the same parity for the one it waits for.
-  static constexpr int STAGES = FIT < 16 ? FIT / 2 * 2 : 16;
+  static constexpr int STAGES = FIT < 16 ? FIT / TEAMS * TEAMS : 16;
   static constexpr int PITCH = D + 4;   // floats; the accumulators' stores meet no bank twice
   static constexpr int SUMS = 2 * kRows * PITCH * 4;  // two warps' accumulators
   static constexpr int BYTES = STAGES * 2 * BLOCK + SUMS;
@@ -484,7 +487,7 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
     k_cache_attention(const AttnArgs a) {
   using R = Ring<D, BT>;
   constexpr int PITCH = R::PITCH;
-  constexpr int HT = BT / 2;     // tokens of a warp per cache block
+  constexpr int HT = BT / R::TEAM;  // tokens of a warp per cache block
   constexpr int NB = HT / 8;     // its blocks of eight tokens
   constexpr int NH = D / 64;     // 64-channel halves of a K row
   constexpr int ND = D / 16;     // 16-channel row tiles of the output
@@ -526,7 +529,7 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
   if (warp == kConsumers) {
     if (lane < R::STAGES) {
       mbar_init(&full[lane], 2);   // the copies issued, the list entry written
-      mbar_init(&empty[lane], 2);  // the two warps of a pair
+      mbar_init(&empty[lane], R::TEAM);  // the warps of a team
     }
     if (lane == 0) s_abort = 0;
     fence_mbar_init();
@@ -653,7 +656,7 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, t = lane & 3;
-  const int half = warp & 1;
+  const int team = warp / R::TEAM, half = warp % R::TEAM;
   float* sums = reinterpret_cast<float*>(smem);  // [2][kRows][PITCH]
   int unit = 0;
   bool have_cut = false;
@@ -712,8 +715,8 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
       for (int e = 0; e < 4; ++e) acc[d][e] = 0.f;
     float v_top = 0.f;  // the accumulator holds sums over V scale / v_top
     bool ok = true;
-    // unit i belongs to the pair of warps i % 2
-    for (int i = unit + ((unit ^ (warp >> 1)) & 1); i < unit + n; i += 2) {
+    // unit i belongs to team i % TEAMS
+    for (int i = unit + ((team - unit) & (R::TEAMS - 1)); i < unit + n; i += R::TEAMS) {
       const int s = i % R::STAGES;
       if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (i / R::STAGES) & 1, wc))) {
         ok = false;
