@@ -173,15 +173,17 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // on, `cols` columns each: whole and aligned rows in pieces of 16 bytes, a row's
 // pieces by neighbouring lanes; else neighbouring lanes store neighbouring columns.
 constexpr int kTurn = 36;
+constexpr int kTurnBytes = 4 * 32 * kTurn * 4;  // of four warps
 template <h3_type T>
-__device__ __forceinline__ void store_turned(const Out& o, int64_t off, const float* turn,
-                                             int rows, int cols, bool vec, int lane) {
+__device__ __forceinline__ void store_turned(const Out& o, int64_t off, int64_t stride,
+                                             const float* turn, int rows, int cols, bool vec,
+                                             int lane) {
   if (vec && cols >= 32) {
     constexpr int PER = T == H3_F32 ? 4 : 8;  // values of a piece
     constexpr int LANES = 32 / PER;           // lanes of a row
     const int i0 = lane / LANES, q = lane % LANES * PER;
     const float* src = turn + i0 * kTurn + q;
-    off += i0 * o.stride_m + q;
+    off += i0 * stride + q;
 #pragma unroll
     for (int i = 0; i < 32; i += 32 / LANES) {
       const float4 x = *reinterpret_cast<const float4*>(src + i * kTurn);
@@ -196,7 +198,7 @@ __device__ __forceinline__ void store_turned(const Out& o, int64_t off, const fl
       }
       if (i0 + i < rows)
         *reinterpret_cast<uint4*>(static_cast<uint8_t*>(o.p) +
-                                  (off + i * o.stride_m) * (T == H3_F32 ? 4 : 2)) = w;
+                                  (off + i * stride) * (T == H3_F32 ? 4 : 2)) = w;
     }
     return;
   }
@@ -209,8 +211,22 @@ __device__ __forceinline__ void store_turned(const Out& o, int64_t off, const fl
       if constexpr (T == H3_F32) static_cast<float*>(o.p)[off] = x;
       else static_cast<uint16_t*>(o.p)[off] = (uint16_t)pack16<T>(x, 0.f);
     }
-    off += o.stride_m;
+    off += stride;
   }
+}
+// The same from a row per lane.
+__device__ __forceinline__ void turn_and_store(const Out& o, int64_t off, int64_t stride,
+                                               float* turn, const float* v, int rows, int cols,
+                                               bool vec, int lane) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *reinterpret_cast<float4*>(turn + lane * kTurn + 4 * q) =
+        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  __syncwarp();
+  if (o.type == H3_F32) store_turned<H3_F32>(o, off, stride, turn, rows, cols, vec, lane);
+  else if (o.type == H3_BF16) store_turned<H3_BF16>(o, off, stride, turn, rows, cols, vec, lane);
+  else store_turned<H3_F16>(o, off, stride, turn, rows, cols, vec, lane);
+  __syncwarp();
 }
 
 // Many rows: the persistent CTA-pair form. A pair computes 256 x BN tiles of
@@ -402,17 +418,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
         // (A lane per row would store 16 bytes of 32 rows at a time: 63 us for 2031 x
         // 18992 x 256 to float32, against 43 us; 50 us against 11 for 4517 x 275 x 224.)
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          *reinterpret_cast<float4*>(turn + lane * kTurn + 4 * q) =
-              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        __syncwarp();
-        const int rows = min(32, M - m0), cols = min(32, N - n);
-        const int64_t off = m0 * out.stride_m + n;
-        if (out.type == H3_F32) store_turned<H3_F32>(out, off, turn, rows, cols, vec, lane);
-        else if (out.type == H3_BF16) store_turned<H3_BF16>(out, off, turn, rows, cols, vec, lane);
-        else store_turned<H3_F16>(out, off, turn, rows, cols, vec, lane);
-        __syncwarp();
+        turn_and_store(out, m0 * out.stride_m + n, out.stride_m, turn, v, min(32, M - m0),
+                       min(32, N - n), vec, lane);
       }
       tc_fence_before();
       __syncwarp();
@@ -443,8 +450,10 @@ template <int NT>
 constexpr int s_stage() { return A_STAGE + NT * BKB; }
 template <int NT>
 constexpr int s_stages() { return 200 * 1024 / s_stage<NT>(); }
-template <int NT>
-constexpr int s_smem() { return s_stages<NT>() * s_stage<NT>() + 1024 + 512; }
+template <int NT, bool TURN>
+constexpr int s_smem() {
+  return s_stages<NT>() * s_stage<NT>() + 1024 + 512 + (TURN ? kTurnBytes : 0);
+}
 
 constexpr int kMaxSplit = 8;  // CTAs that share a K axis
 
@@ -457,7 +466,7 @@ __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
   return v;
 }
 
-template <int NT>
+template <int NT, bool TURN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     k_int8_skinny(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA,
                   int M, int N, int kb_n, int split, const Out out, int* err) {
@@ -565,6 +574,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else {
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // weight row of the tile
+    float* turn = reinterpret_cast<float*>(smem + NST * STAGE + 512) + (warp - 2) * 32 * kTurn;
+    const bool vec = out.stride_n % (out.type == H3_F32 ? 4 : 8) == 0;
     uint32_t it = 0;
     for (int t = tile0; t < tiles; t += step, ++it) {
       const uint32_t acc = it & 1, aph = (it >> 1) & 1;
@@ -590,12 +601,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int i = 0; i < 32; ++i)
             if (32 * c + i < rows) part[(32 * c + i) * BM + r] = v[i];
         } else {
+          float y[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float s = __shfl_sync(0xffffffffu, sa, i) * sw;
-            if (32 * c + i < rows && n < N)
-              store_one(out, (m0 + 32 * c + i) * out.stride_m + n * out.stride_n,
-                        (float)(int)v[i] * s);
+          for (int i = 0; i < 32; ++i)
+            y[i] = (float)(int)v[i] * (__shfl_sync(0xffffffffu, sa, i) * sw);
+          if constexpr (TURN) {
+            if (n - lane < N)
+              turn_and_store(out, (n - lane) * out.stride_n + m0 + 32 * c, out.stride_n, turn, y,
+                             min(32, N - (n - lane)), min(32, rows - 32 * c), vec, lane);
+          } else if (n < N) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i < rows)
+                store_one(out, (m0 + 32 * c + i) * out.stride_m + n, y[i]);
           }
         }
       }
@@ -682,7 +700,7 @@ cudaError_t run_pair(int M, int N, int K, const void* a, const void* w, const Ou
 }
 
 // Clusters of `split` CTAs that the current device runs at once (asked once).
-template <int NT>
+template <int NT, bool TURN>
 int clusters_at_once(int split) {
   static int known[64][kMaxSplit + 1] = {};
   int dev = 0;
@@ -691,7 +709,7 @@ int clusters_at_once(int split) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)split);
     cfg.blockDim = dim3(NUM_THREADS);
-    cfg.dynamicSmemBytes = s_smem<NT>();
+    cfg.dynamicSmemBytes = s_smem<NT, TURN>();
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)split;
@@ -699,9 +717,9 @@ int clusters_at_once(int split) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaFuncSetAttribute(k_int8_skinny<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             s_smem<NT>()) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, k_int8_skinny<NT>, &cfg) != cudaSuccess) {
+    if (cudaFuncSetAttribute(k_int8_skinny<NT, TURN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             s_smem<NT, TURN>()) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, k_int8_skinny<NT, TURN>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       return 0;
     }
@@ -719,11 +737,12 @@ struct Plan {
 // Cycles, from measurements at 1.9 GHz: a K step of a CTA costs its MMAs (2 NT) or
 // the fetch of its operands at 44 bytes a cycle, all weights together at least
 // 3440 bytes a cycle (HBM); 6000 go to launch, fill and last tile, and joining a
-// shared K axis costs 1500 and 8 per token. (5120 x 5120, one row: 8 us; 128 rows:
+// shared K axis costs 1500 and 8 per token, with out turned, whose columns are then
+// stored one by one, 350 more for each a CTA stores. (5120 x 5120, one row: 8 us; 128 rows:
 // 12 us; 1024 x 5120, 512 rows: 10 us against 20 us by pairs of CTAs.)
-template <int NT>
+template <int NT, bool TURN>
 Plan plan_skinny(int M, int N, int K) {
-  Plan p;
+  Plan p{};
   const int kb_n = (K + BKB - 1) / BKB, sms = num_sms();
   const long long tiles = (long long)((N + BM - 1) / BM) * ((M + NT - 1) / NT);
   // As many CTAs share a tile's K axis as leave every tile a cluster that runs at
@@ -731,15 +750,21 @@ Plan plan_skinny(int M, int N, int K) {
   int split = tiles < sms ? (int)(sms / tiles) : 1;
   if (split > kb_n / 2) split = kb_n / 2;
   if (split > kMaxSplit) split = kMaxSplit;
-  while (split > 1 && clusters_at_once<NT>(split) < tiles) --split;
+  while (split > 1 && clusters_at_once<NT, TURN>(split) < tiles) --split;
   if (split < 1) split = 1;
-  p.split = split;
-  p.ctas = split > 1 ? (int)tiles * split : (int)(tiles < sms ? tiles : sms);
   const long long step = 2 * NT > (A_STAGE + NT * BKB) / 44 ? 2 * NT : (A_STAGE + NT * BKB) / 44;
-  const long long run = (tiles * split + sms - 1) / sms * ((kb_n + split - 1) / split) * step;
   const long long bytes = (long long)N * K / 3440;
-  p.cycles = (run > bytes ? run : bytes) + 6000 + (split > 1 ? 1500 + 8 * NT : 0);
-  return p;
+  for (;; split = 1) {
+    const long long run = (tiles * split + sms - 1) / sms * ((kb_n + split - 1) / split) * step;
+    const long long join = split > 1 ? 1500 + 8 * NT + (TURN ? 350 * NT / split : 0) : 0;
+    const long long cycles = (run > bytes ? run : bytes) + 6000 + join;
+    if (p.split == 0 || cycles < p.cycles) {
+      p.cycles = cycles;
+      p.split = split;
+      p.ctas = split > 1 ? (int)tiles * split : (int)(tiles < sms ? tiles : sms);
+    }
+    if (split == 1) return p;
+  }
 }
 
 // The same for the pair kernel: 700 cycles a K step and wave, 8000 around.
@@ -751,18 +776,18 @@ long long pair_cycles(int M, int N, int K) {
   return (run > bytes ? run : bytes) + 8000;
 }
 
-template <int NT>
+template <int NT, bool TURN>
 cudaError_t run_skinny(const Plan& p, int M, int N, int K, const void* a, const void* w,
                        const Out& out, int* err, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(k_int8_skinny<NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, s_smem<NT>());
+  cudaError_t e = cudaFuncSetAttribute(k_int8_skinny<NT, TURN>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, s_smem<NT, TURN>());
   if (e != cudaSuccess) return e;
   CUtensorMap ta, tw;
   if (!tmap_codes(&ta, a, M, K, NT) || !tmap_codes(&tw, w, N, K, BM)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.ctas);
   cfg.blockDim = dim3(NUM_THREADS);
-  cfg.dynamicSmemBytes = s_smem<NT>();
+  cfg.dynamicSmemBytes = s_smem<NT, TURN>();
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -770,23 +795,25 @@ cudaError_t run_skinny(const Plan& p, int M, int N, int K, const void* a, const 
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_int8_skinny<NT>, tw, ta, M, N, (K + BKB - 1) / BKB, p.split,
+  return cudaLaunchKernelEx(&cfg, k_int8_skinny<NT, TURN>, tw, ta, M, N, (K + BKB - 1) / BKB, p.split,
                             out, err);
 }
 
 // By the number of tokens.
+template <bool TURN>
 Plan plan_any(int M, int N, int K) {
-  return M <= 16   ? plan_skinny<16>(M, N, K)
-         : M <= 32 ? plan_skinny<32>(M, N, K)
-         : M <= 64 ? plan_skinny<64>(M, N, K)
-                   : plan_skinny<128>(M, N, K);
+  return M <= 16   ? plan_skinny<16, TURN>(M, N, K)
+         : M <= 32 ? plan_skinny<32, TURN>(M, N, K)
+         : M <= 64 ? plan_skinny<64, TURN>(M, N, K)
+                   : plan_skinny<128, TURN>(M, N, K);
 }
+template <bool TURN>
 cudaError_t run_any(const Plan& p, int M, int N, int K, const void* a, const void* w,
                     const Out& out, int* err, cudaStream_t st) {
-  return M <= 16   ? run_skinny<16>(p, M, N, K, a, w, out, err, st)
-         : M <= 32 ? run_skinny<32>(p, M, N, K, a, w, out, err, st)
-         : M <= 64 ? run_skinny<64>(p, M, N, K, a, w, out, err, st)
-                   : run_skinny<128>(p, M, N, K, a, w, out, err, st);
+  return M <= 16   ? run_skinny<16, TURN>(p, M, N, K, a, w, out, err, st)
+         : M <= 32 ? run_skinny<32, TURN>(p, M, N, K, a, w, out, err, st)
+         : M <= 64 ? run_skinny<64, TURN>(p, M, N, K, a, w, out, err, st)
+                   : run_skinny<128, TURN>(p, M, N, K, a, w, out, err, st);
 }
 
 }  // namespace
@@ -809,18 +836,18 @@ cudaError_t launch_matmul_int8(int M, int N, int K, const void* a, const float* 
   // The few-row kernel with a's rows as tokens (up to 2048 of them), or, where out
   // is narrower than long, with w's rows as tokens and out turned; the narrowest
   // token tile that holds all tokens, or tiles of 128 of them. Pairs of CTAs where
-  // they are estimated to be faster. (2290 x 10 x 9040: 7.6 us turned, 30 us by
+  // they are estimated to be faster. (2290 x 10 x 9040: 7.7 us turned, 30 us by
   // pairs, of which there are only nine.)
   const bool few = M <= 2048, turn = N <= 128 && N < M;
   Plan p{}, q{};
-  if (few) p = plan_any(M, N, K);
-  if (turn) q = plan_any(N, M, K);
+  if (few) p = plan_any<false>(M, N, K);
+  if (turn) q = plan_any<true>(N, M, K);
   const long long pairs = M <= 128 ? LLONG_MAX : pair_cycles(M, N, K);
   if (turn && q.cycles < pairs && (!few || q.cycles < p.cycles)) {
     const Out t{out, 1, out_stride, (int)out_type, w_scale, a_scale};
-    return run_any(q, N, M, K, w, a, t, err, st);
+    return run_any<true>(q, N, M, K, w, a, t, err, st);
   }
-  if (few && p.cycles < pairs) return run_any(p, M, N, K, a, w, o, err, st);
+  if (few && p.cycles < pairs) return run_any<false>(p, M, N, K, a, w, o, err, st);
   return run_pair<256>(M, N, K, a, w, o, err, st);
 }
 

@@ -118,7 +118,7 @@ def test_product(M, N, K, dtype):
 @pytest.mark.parametrize("M,N,K", [
     (300, 1, 64), (2290, 10, 9040), (1000, 3, 14320), (4097, 17, 272), (129, 128, 528),
     (5000, 100, 144), (20001, 33, 48), (127, 9, 4096), (4517, 275, 224), (2392, 382, 16),
-    (2051, 3001, 160)])
+    (2051, 3001, 160), (4097, 64, 272), (3001, 128, 1040), (9000, 96, 2064)])
 def test_product_of_many_rows_and_few_or_odd_columns(M, N, K, dtype):
     _product(M, N, K, dtype)
 
