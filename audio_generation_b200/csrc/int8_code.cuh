@@ -201,7 +201,9 @@ struct AbsMax<H3_BF16> {
     asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w));
   }
   __device__ __forceinline__ void add(const uint4& u) { one(u.x), one(u.y), one(u.z), one(u.w); }
-  __device__ __forceinline__ float value() const { return max_nan(fabsf(bf16lo(m)), fabsf(bf16hi(m))); }
+  __device__ __forceinline__ float value() const {
+    return max_nan(fabsf(bf16lo(m)), fabsf(bf16hi(m)));
+  }
 };
 template <>
 struct AbsMax<H3_F16> {

@@ -202,6 +202,22 @@ __device__ __forceinline__ void store_turned(const Out& o, int64_t off, int64_t 
     }
     return;
   }
+  if (stride % 2 == 0 && cols >= 32) {  // rows aligned to two values
+    const int i0 = lane / 16, q = lane % 16 * 2;
+    off += i0 * stride + q;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(turn + (i0 + i) * kTurn + q);
+      if (i0 + i < rows) {
+        if constexpr (T == H3_F32)
+          *reinterpret_cast<float2*>(static_cast<float*>(o.p) + off) = x;
+        else
+          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(o.p) + off) = pack16<T>(x.x, x.y);
+      }
+      off += 2 * stride;
+    }
+    return;
+  }
   if (lane >= cols) return;
   off += lane;
 #pragma unroll
@@ -372,7 +388,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const bool vec = out.stride_m % (out.type == H3_F32 ? 4 : 8) == 0;
     // the tile's column scales, and 32 x 32 values to turn
     float* scales = reinterpret_cast<float*>(smem + PNST * STAGE + 256) + (warp - 2) * BN;
-    float* turn = reinterpret_cast<float*>(smem + PNST * STAGE + 256) + 4 * BN + (warp - 2) * 32 * kTurn;
+    float* turn =
+        reinterpret_cast<float*>(smem + PNST * STAGE + 256) + 4 * BN + (warp - 2) * 32 * kTurn;
     uint32_t it = 0;
     for (int t = pair; t < T; t += n_pairs, ++it) {
       const uint32_t acc = it & 1, aph = (it >> 1) & 1;
@@ -780,7 +797,8 @@ template <int NT, bool TURN>
 cudaError_t run_skinny(const Plan& p, int M, int N, int K, const void* a, const void* w,
                        const Out& out, int* err, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(k_int8_skinny<NT, TURN>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, s_smem<NT, TURN>());
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       s_smem<NT, TURN>());
   if (e != cudaSuccess) return e;
   CUtensorMap ta, tw;
   if (!tmap_codes(&ta, a, M, K, NT) || !tmap_codes(&tw, w, N, K, BM)) return cudaErrorInvalidValue;
@@ -795,8 +813,8 @@ cudaError_t run_skinny(const Plan& p, int M, int N, int K, const void* a, const 
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_int8_skinny<NT, TURN>, tw, ta, M, N, (K + BKB - 1) / BKB, p.split,
-                            out, err);
+  return cudaLaunchKernelEx(&cfg, k_int8_skinny<NT, TURN>, tw, ta, M, N, (K + BKB - 1) / BKB,
+                            p.split, out, err);
 }
 
 // By the number of tokens.

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kStoreThreads<D, BT>,
 constexpr int kAttnThreads = 160, kConsumers = 4;
 constexpr int kRows = 8;        // query heads that share a pass over the cache
 constexpr int kListSize = 64;   // entries of the producer's list, two batches of 32
-constexpr int kMinUnits = 2;    // cache blocks a thread block takes at least, about, but for whole pairs
+constexpr int kMinUnits = 2;    // cache blocks a range has at least, but for whole pairs
 constexpr int kPairUnits = 3;
 
 template <int D, int BT>
@@ -984,7 +984,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_cache_join(const AttnArgs a
   Piece x[kAhead];
   float2 ml[kAhead];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) x[k] = part(slice + k * SLICES), ml[k] = a.stat[at(slice + k * SLICES)];
+  for (int k = 0; k < 2; ++k) {
+    x[k] = part(slice + k * SLICES);
+    ml[k] = a.stat[at(slice + k * SLICES)];
+  }
   const int n = cut.z, kvh = cut.y / a.row_groups, h0 = (cut.y - kvh * a.row_groups) * kRows;
   if (n == 0 || h0 + r >= a.group) return;  // with shared rows: the whole thread block
 #pragma unroll

@@ -339,7 +339,8 @@ def test_attention_over_v_scales_far_apart(dtype, order):
     BT = 32
     lengths, QH, KH, D = [9 * BT - 5, 300 * BT], 5, 1, 64
     cache = Cache(lengths, KH, D, BT)
-    factors = [1.0, 2.0 ** -7, 2.0 ** -9, 2.0 ** -14, 2.0 ** -20, 2.0 ** -31, 2.0 ** -80, 1e-39, 0.0]
+    factors = [1.0, 2.0 ** -7, 2.0 ** -9, 2.0 ** -14, 2.0 ** -20, 2.0 ** -31, 2.0 ** -80, 1e-39,
+               0.0]
     for s, n in enumerate(lengths):
         blocks = cache.table[s, :-(-n // BT)].long()
         f = torch.tensor([factors[::order][i * len(factors) // len(blocks)]
