@@ -251,8 +251,8 @@ __device__ __forceinline__ void turn_and_store(const Out& o, int64_t off, int64_
 // stages; the accumulator is double-buffered in TMEM, so the epilogue of a tile
 // overlaps the next tile's products. Warps: 0 TMA producer, 1 TMEM owner and
 // MMA issuer, 2..5 epilogue (one TMEM lane = one row per thread).
-// 8191 x 14336 x 5376: 380 us alone (3.3 P operations/s, the tensor pipe active in
-// 97 % of the cycles), 440 to 470 us in a loop, where the board's power cap holds
+// 8191 x 14336 x 5376: 368 us alone (3.4 P operations/s, the tensor pipe active in
+// 97 % of the cycles), 436 to 464 us in a loop, where the board's power cap holds
 // the clock down.
 constexpr int PNST = 6;
 template <int BN>
