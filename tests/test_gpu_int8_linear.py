@@ -207,3 +207,18 @@ def test_linear_layer_on_a_stream_and_in_a_graph(M):
         graph.replay()
         torch.cuda.synchronize()
         check()
+
+
+@pytest.mark.parametrize("M,N,stride", [(5, 40, 2 ** 29 + 8), (300, 40, 2 ** 23), (300, 600, 2 ** 23)])
+def test_out_past_two_to_the_31_elements(M, N, stride):
+    """Few rows, turned and by pairs: row offsets that do not fit 32 bits."""
+    g = gen(M + N)
+    a, w = rand_codes(g, M, 272), rand_codes(g, N, 272)
+    sa, sw = torch.ones(M, device=DEV), torch.ones(N, device=DEV)
+    whole = torch.empty(M * stride, dtype=torch.bfloat16, device=DEV)
+    out = whole.view(M, stride)
+    out[:, :N + 8] = -3
+    h3.h3_matmul_int8(M, N, 272, a, sa, w, sw, torch.bfloat16, out, stride)
+    ref = (a.double() @ w.double().T)
+    assert torch.equal(out[:, :N], ref.float().to(torch.bfloat16))
+    assert bool((out[:, N:N + 8] == -3).all())

@@ -337,3 +337,22 @@ def test_refusals_of_the_call():
         assert call(**kw) == h3.H3_ERR_ALIGN, kw
     assert L.h3_prompt_attention(None, 0, ok, 256, ok, 128, ok, 128, 0.1, ok, 256,
                                  None) == h3.H3_ERR_ARG
+
+
+@pytest.mark.parametrize("lengths", [[40], [40, 300]])
+def test_rows_past_two_to_the_31_elements(lengths):
+    """q and o rows so far apart that their offsets do not fit 32 bits: the short
+    form and the other give what they give for dense rows."""
+    QH, KH, D, T = 2, 1, 64, sum(lengths)
+    stride = (2 ** 31 // (T - 8)) // 8 * 8
+    g = gen(T)
+    q = torch.randn(T, QH, D, generator=g, device=DEV).to(BF)
+    k, v = (torch.randn(T, KH, D, generator=g, device=DEV).to(BF) for _ in range(2))
+    far = torch.empty(T * stride, dtype=BF, device=DEV).view(T, stride)
+    far[:, :QH * D] = q.view(T, -1)
+    p = h3.h3_prompts_prepare(_offsets(lengths), QH, KH, D)
+    dense, apart = torch.empty_like(q), torch.empty(T * stride, dtype=BF, device=DEV).view(T, stride)
+    h3.h3_prompt_attention(p, BF, q, QH * D, k, KH * D, v, KH * D, 0.1, dense, QH * D)
+    h3.h3_prompt_attention(p, BF, far, stride, k, KH * D, v, KH * D, 0.1, apart, stride)
+    assert torch.equal(apart[:, :QH * D], dense.view(T, -1))
+    assert h3.h3_text_error() == h3.H3_OK
