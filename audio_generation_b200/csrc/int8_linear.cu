@@ -6,6 +6,8 @@
 #include <cuda_fp16.h>
 #include <limits.h>
 
+#include <type_traits>
+
 #include "host_util.cuh"
 #include "int8_code.cuh"
 #include "internal.cuh"
@@ -650,31 +652,49 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float sw[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) sw[e] = n + e < N ? __ldg(out.w_scale + n + e) : 0.f;
-      uint32_t from[kMaxSplit];
+      const uint32_t mine = smem_u32(smem) + lane * 16;
+      // U tokens of a warp side by side, each from at most Q CTAs: the latency of the
+      // fetches is what the join takes
+      auto join = [&](auto tokens, auto ctas) {
+        constexpr int U = decltype(tokens)::value, Q = decltype(ctas)::value;
+        for (int i0 = first + warp - 2; i0 < last; i0 += 4 * U) {
+          uint4 v[U][Q];
+          float sa[U];
 #pragma unroll
-      for (int q = 0; q < kMaxSplit; ++q)
-        from[q] = mapa_shared(smem_u32(smem) + lane * 16, q < split ? q : 0);
-      for (int i = first + warp - 2; i < last; i += 4) {
-        uint4 v[kMaxSplit];
+          for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + 4 * u, last - 1);
+            sa[u] = __ldg(out.a_scale + m0 + i);
 #pragma unroll
-        for (int q = 0; q < kMaxSplit; ++q)
-          v[q] = q < split ? ld_cluster_v4(from[q] + i * BM * 4) : make_uint4(0, 0, 0, 0);
-        uint4 sum = v[0];
+            for (int q = 0; q < Q; ++q)
+              v[u][q] = q < split ? ld_cluster_v4(mapa_shared(mine, q) + i * BM * 4)
+                                  : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-        for (int q = 1; q < kMaxSplit; ++q)
-          sum.x += v[q].x, sum.y += v[q].y, sum.z += v[q].z, sum.w += v[q].w;
-        const float sa = __ldg(out.a_scale + m0 + i);
-        const float y[4] = {(float)(int)sum.x * (sa * sw[0]), (float)(int)sum.y * (sa * sw[1]),
-                            (float)(int)sum.z * (sa * sw[2]), (float)(int)sum.w * (sa * sw[3])};
-        const size_t at = (m0 + i) * out.stride_m + n * out.stride_n;
-        if (vec) {
-          store_4(out, at, y);
-        } else {
+          for (int u = 0; u < U; ++u) {
+            const int i = i0 + 4 * u;
+            if (i >= last) break;
+            uint4 sum = v[u][0];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < N) store_one(out, at + e * out.stride_n, y[e]);
+            for (int q = 1; q < Q; ++q)
+              sum.x += v[u][q].x, sum.y += v[u][q].y, sum.z += v[u][q].z, sum.w += v[u][q].w;
+            const float y[4] = {
+                (float)(int)sum.x * (sa[u] * sw[0]), (float)(int)sum.y * (sa[u] * sw[1]),
+                (float)(int)sum.z * (sa[u] * sw[2]), (float)(int)sum.w * (sa[u] * sw[3])};
+            const size_t at = (m0 + i) * out.stride_m + n * out.stride_n;
+            if (vec) {
+              store_4(out, at, y);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (n + e < N) store_one(out, at + e * out.stride_n, y[e]);
+            }
+          }
         }
-      }
+      };
+      if (!TURN && split <= 3)
+        join(std::integral_constant<int, 4>(), std::integral_constant<int, 3>());
+      else
+        join(std::integral_constant<int, 1>(), std::integral_constant<int, kMaxSplit>());
     }
     cluster_sync();  // no CTA leaves while another reads its sums
   } else {
@@ -749,17 +769,20 @@ int clusters_at_once(int split) {
 struct Plan {
   long long cycles;
   int split, ctas;
+  int tokens;  // of a tile: NT
 };
 
 // Cycles, from measurements at 1.9 GHz: a K step of a CTA costs its MMAs (2 NT) or
 // the fetch of its operands at 44 bytes a cycle, all weights together at least
 // 3440 bytes a cycle (HBM); 6000 go to launch, fill and last tile, and joining a
-// shared K axis costs 1500 and 8 per token, with out turned, whose columns are then
-// stored one by one, 350 more for each a CTA stores. (5120 x 5120, one row: 8 us; 128 rows:
-// 12 us; 1024 x 5120, 512 rows: 10 us against 20 us by pairs of CTAs.)
+// shared K axis costs 1500 and 90 for each token that a CTA finishes (350 with out
+// turned, whose columns are then stored one by one). (5120 x 5120, one row: 8 us;
+// 128 rows: 11.5 us; 256 rows: 15.6 us in tiles of 256 against 18.3 by pairs of CTAs;
+// 1024 x 5120, 512 rows: 10 us against 20.)
 template <int NT, bool TURN>
 Plan plan_skinny(int M, int N, int K) {
   Plan p{};
+  p.tokens = NT;
   const int kb_n = (K + BKB - 1) / BKB, sms = num_sms();
   const long long tiles = (long long)((N + BM - 1) / BM) * ((M + NT - 1) / NT);
   // As many CTAs share a tile's K axis as leave every tile a cluster that runs at
@@ -773,7 +796,7 @@ Plan plan_skinny(int M, int N, int K) {
   const long long bytes = (long long)N * K / 3440;
   for (;; split = 1) {
     const long long run = (tiles * split + sms - 1) / sms * ((kb_n + split - 1) / split) * step;
-    const long long join = split > 1 ? 1500 + 8 * NT + (TURN ? 350 * NT / split : 0) : 0;
+    const long long join = split > 1 ? 1500 + (TURN ? 350 : 90) * (M < NT ? M : NT) / split : 0;
     const long long cycles = (run > bytes ? run : bytes) + 6000 + join;
     if (p.split == 0 || cycles < p.cycles) {
       p.cycles = cycles;
@@ -817,21 +840,33 @@ cudaError_t run_skinny(const Plan& p, int M, int N, int K, const void* a, const 
                             p.split, out, err);
 }
 
-// By the number of tokens.
+// The narrowest token tile that holds all tokens, or tiles of 128 of them, or of 256
+// where those are so few that their K axis is shared.
 template <bool TURN>
 Plan plan_any(int M, int N, int K) {
-  return M <= 16   ? plan_skinny<16, TURN>(M, N, K)
-         : M <= 32 ? plan_skinny<32, TURN>(M, N, K)
-         : M <= 64 ? plan_skinny<64, TURN>(M, N, K)
-                   : plan_skinny<128, TURN>(M, N, K);
+  if (M <= 16) return plan_skinny<16, TURN>(M, N, K);
+  if (M <= 32) return plan_skinny<32, TURN>(M, N, K);
+  if (M <= 64) return plan_skinny<64, TURN>(M, N, K);
+  const Plan p = plan_skinny<128, TURN>(M, N, K);
+  if constexpr (!TURN) {
+    if (M > 128) {
+      const Plan wide = plan_skinny<256, TURN>(M, N, K);
+      if (wide.split > 1 && wide.cycles < p.cycles) return wide;
+    }
+  }
+  return p;
 }
 template <bool TURN>
 cudaError_t run_any(const Plan& p, int M, int N, int K, const void* a, const void* w,
                     const Out& out, int* err, cudaStream_t st) {
-  return M <= 16   ? run_skinny<16, TURN>(p, M, N, K, a, w, out, err, st)
-         : M <= 32 ? run_skinny<32, TURN>(p, M, N, K, a, w, out, err, st)
-         : M <= 64 ? run_skinny<64, TURN>(p, M, N, K, a, w, out, err, st)
-                   : run_skinny<128, TURN>(p, M, N, K, a, w, out, err, st);
+  switch (p.tokens) {
+    case 16: return run_skinny<16, TURN>(p, M, N, K, a, w, out, err, st);
+    case 32: return run_skinny<32, TURN>(p, M, N, K, a, w, out, err, st);
+    case 64: return run_skinny<64, TURN>(p, M, N, K, a, w, out, err, st);
+    case 128: return run_skinny<128, TURN>(p, M, N, K, a, w, out, err, st);
+  }
+  if constexpr (!TURN) return run_skinny<256, TURN>(p, M, N, K, a, w, out, err, st);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -852,9 +887,8 @@ cudaError_t launch_matmul_int8(int M, int N, int K, const void* a, const float* 
                                int64_t out_stride, int* err, cudaStream_t st) {
   const Out o{out, out_stride, 1, (int)out_type, a_scale, w_scale};
   // The few-row kernel with a's rows as tokens (up to 2048 of them), or, where out
-  // is narrower than long, with w's rows as tokens and out turned; the narrowest
-  // token tile that holds all tokens, or tiles of 128 of them. Pairs of CTAs where
-  // they are estimated to be faster. (2290 x 10 x 9040: 7.7 us turned, 30 us by
+  // is narrower than long, with w's rows as tokens and out turned. Pairs of CTAs
+  // where they are estimated to be faster. (2290 x 10 x 9040: 7.7 us turned, 30 us by
   // pairs, of which there are only nine.)
   const bool few = M <= 2048, turn = N <= 128 && N < M;
   Plan p{}, q{};

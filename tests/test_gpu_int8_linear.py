@@ -109,7 +109,7 @@ def _product(M, N, K, dtype, seed=0, stride=None, a=None, w=None):
     (32, 640, 14336), (33, 32003, 256), (64, 5376, 1024), (65, 100, 4096), (128, 384, 2560),
     (129, 256, 128), (256, 257, 528), (333, 1003, 5376), (700, 1, 64), (1025, 2048, 1040),
     (130, 1500, 5120), (513, 300, 5120), (1030, 129, 2064), (2048, 640, 1296), (2049, 3000, 272),
-    (300, 19000, 512)])
+    (300, 19000, 512), (256, 5120, 2064), (144, 2559, 4112), (400, 2564, 5120), (1500, 1024, 4096)])
 def test_product(M, N, K, dtype):
     _product(M, N, K, dtype)
 
