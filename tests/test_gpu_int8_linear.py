@@ -209,7 +209,8 @@ def test_linear_layer_on_a_stream_and_in_a_graph(M):
         check()
 
 
-@pytest.mark.parametrize("M,N,stride", [(5, 40, 2 ** 29 + 8), (300, 40, 2 ** 23), (300, 600, 2 ** 23)])
+@pytest.mark.parametrize("M,N,stride", [
+    (5, 40, 2 ** 29 + 8), (300, 40, 2 ** 23), (300, 600, 2 ** 23)])
 def test_out_past_two_to_the_31_elements(M, N, stride):
     """Few rows, turned and by pairs: row offsets that do not fit 32 bits."""
     g = gen(M + N)

@@ -351,7 +351,8 @@ def test_rows_past_two_to_the_31_elements(lengths):
     far = torch.empty(T * stride, dtype=BF, device=DEV).view(T, stride)
     far[:, :QH * D] = q.view(T, -1)
     p = h3.h3_prompts_prepare(_offsets(lengths), QH, KH, D)
-    dense, apart = torch.empty_like(q), torch.empty(T * stride, dtype=BF, device=DEV).view(T, stride)
+    dense = torch.empty_like(q)
+    apart = torch.empty(T * stride, dtype=BF, device=DEV).view(T, stride)
     h3.h3_prompt_attention(p, BF, q, QH * D, k, KH * D, v, KH * D, 0.1, dense, QH * D)
     h3.h3_prompt_attention(p, BF, far, stride, k, KH * D, v, KH * D, 0.1, apart, stride)
     assert torch.equal(apart[:, :QH * D], dense.view(T, -1))
