@@ -388,6 +388,12 @@ struct Ring {
   static_assert(SUMS % 128 == 0, "stage alignment");
 };
 
+#ifdef H3_FAULT_INJECTION
+// Test-only build: the unit of every range whose copies are left out, so that the
+// wait of the warps that take it runs out (none where negative).
+static __device__ int g_fault_skip_unit = -1;
+#endif
+
 struct Entry {
   int block, page;
   float ks, vs;
@@ -480,6 +486,20 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+// The same; true for all of them if x is for any.
+__device__ __forceinline__ bool consumers_any(bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(x ? 1u : 0u)
+      : "memory");
+  return any != 0;
 }
 
 template <int D, int BT>
@@ -604,12 +624,16 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
     bool ok = true;
-    int i = 0;  // units listed and issued
+    int i = 0;       // units listed and issued
+    int issued = 0;  // lane 0's count of the latter
     while (i < n_units && ok) {
       const int n = min(min(32, pages - page), n_units - i);
       const int kvh = hg / a.row_groups;
       auto issue = [&](int k, int block) {  // unit k's copies; nothing for no block
         const int s = k % R::STAGES;
+#ifdef H3_FAULT_INJECTION
+        if (k == *(volatile int*)&g_fault_skip_unit) return;
+#endif
         if (block < 0) {
           mbar_arrive(&full[s]);
           return;
@@ -636,14 +660,12 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
           if (k >= i + early) {
             if (!mbar_wait(&empty[s], ((k / R::STAGES) & 1) ^ 1, wc)) {
               ok = false;
-              // let issued copies land before the block retires
-              for (int j = k > R::STAGES ? k - R::STAGES : 0; j < k; ++j)
-                mbar_drain(&full[j % R::STAGES], (j / R::STAGES) & 1);
               break;
             }
             issue(k, list[k % kListSize].block);
           }
           mbar_arrive(&full[s]);  // the entry is written
+          issued = k + 1;
         }
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -651,6 +673,10 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
       page += n;
       if (i < n_units && page == pages) next_pair();
     }
+    // Copies land before the block retires, though the consumers may have given up
+    // (else they have waited for every one, later than this).
+    for (int j = max(0, issued - R::STAGES); lane == 0 && j < issued; ++j)
+      mbar_drain(&full[j % R::STAGES], (j / R::STAGES) & 1);
     return;
   }
 
@@ -864,7 +890,9 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
 #pragma unroll
       for (int k = 0; k < 2; ++k) stat[warp][2 * t + k] = make_float2(m_run[k], l_run[k]);
     }
-    consumers_sync();
+    // A wait that ran out in one warp ends all four after this segment: one that went
+    // on alone would wait at the next one's barriers for good.
+    ok = !consumers_any(!ok);
     float m_all[2], l_all[2], by[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -1180,3 +1208,10 @@ cudaError_t launch_cache_attention(const h3_kv_cache& c, int n_seq, int q_heads,
 }
 
 }  // namespace h3
+
+#ifdef H3_FAULT_INJECTION
+// Test-only build: the unit whose copies cache attention leaves out (-1: none).
+extern "C" __attribute__((visibility("default"))) int h3_test_cache_skip_unit(int unit) {
+  return cudaMemcpyToSymbol(h3::g_fault_skip_unit, &unit, sizeof(int)) == cudaSuccess ? 0 : -1;
+}
+#endif

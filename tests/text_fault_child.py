@@ -1,0 +1,61 @@
+"""Child process of tests/test_gpu_text_timeout.py (not collected by pytest).
+
+Loads the test-only fault-injection build of the library given on the command
+line and runs the named case with it; prints status codes and outputs as JSON.
+"""
+
+import ctypes
+import json
+import sys
+
+import torch
+
+BF = torch.bfloat16
+
+
+def cache_case(h3):
+    """So many short sequences that every range of the attention's work has several
+    segments."""
+    n, QH, KH, D, BT, width = 1500, 8, 2, 128, 64, 5
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    kc, vc = (torch.randint(-127, 128, s, generator=g, device="cuda", dtype=torch.int8)
+              for s in ((40, KH, BT, D), (40, KH, D, BT)))
+    ks, vs = (torch.rand(40, KH, generator=g, device="cuda") * 0.02 + 0.01 for _ in range(2))
+    table = torch.randint(0, 40, (n, width), generator=g, device="cuda", dtype=torch.int32)
+    lengths = torch.randint(1, width * BT + 1, (n,), generator=g, device="cuda", dtype=torch.int32)
+    q = torch.randn(n, QH, D, generator=g, device="cuda").to(BF)
+    cache = h3.make_kv_cache(kc, vc, ks, vs)
+    need = h3.h3_cache_attention_workspace_size(cache, n, QH, width)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+
+    def attend():
+        o = torch.zeros_like(q)
+        h3.h3_cache_attention(cache, n, QH, table, width, lengths, BF, q, QH * D, 0.1, o, QH * D,
+                              ws, need)
+        return h3.h3_text_error(), o.float().cpu().view(-1).view(torch.int32).tolist()[::97]
+
+    return attend
+
+
+def cache(h3, lib):
+    lib.h3_test_cache_skip_unit.restype = ctypes.c_int
+    lib.h3_test_cache_skip_unit.argtypes = [ctypes.c_int]
+    attend, out = cache_case(h3), {}
+    for unit in (0, 1, 2, 7):
+        assert lib.h3_test_cache_skip_unit(unit) == 0
+        out["skipped_%d" % unit] = attend()[0]
+    assert lib.h3_test_cache_skip_unit(-1) == 0
+    out["normal"], out["values"] = attend()
+    return out
+
+
+def main(lib_path: str, case: str) -> None:
+    from audio_generation_b200 import h3
+    h3.LIB_PATH = lib_path
+    h3._lib = None
+    print("RESULT " + json.dumps({"cache": cache}[case](h3, h3.lib())))
+
+
+if __name__ == "__main__":
+    main(*sys.argv[1:])
