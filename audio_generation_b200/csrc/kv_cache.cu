@@ -167,10 +167,10 @@ __device__ __forceinline__ void store_block(const StoreArgs& a, int seq, int nth
   constexpr int GROUPS = WR * RV;           // (word, vector) pairs
   constexpr int NG = (GROUPS + THREADS - 1) / THREADS;
   const int t = threadIdx.x;
+  if (nth >= blocks_touched<BT>(r)) return;
   const int before = r.before, first = r.first, count = r.count;
   const int page = before / BT + nth;
   const int lo = max(before, page * BT), hi = min(before + count, (page + 1) * BT);
-  if (lo >= hi) return;
   const int held = nth == 0 ? before % BT : 0;  // earlier tokens of the block
   const int slot0 = lo - page * BT, to = hi - page * BT;
   const bool whole = slot0 == 0 && to == BT;
@@ -1163,9 +1163,10 @@ cudaError_t launch_kv_cache_store(const h3_kv_cache& c, int n_seq, int max_new,
   a.max_new = max_new;
   a.rows = rows;
   a.n_seq = n_seq;
-  // max_new tokens that begin anywhere inside a block
-  a.pages = (max_new + c.block_tokens - 2) / c.block_tokens + 1;
-  if (a.pages > width) a.pages = width;
+  // max_new tokens that begin anywhere inside a block (max_new may be any number up
+  // to INT_MAX: more than there are rows are none the more)
+  a.pages = (int)std::min(((long long)max_new + c.block_tokens - 2) / c.block_tokens + 1,
+                          (long long)width);
   a.err = err;
   if (c.head_dim == 128)
     return f16 ? run_store<H3_F16, 128>(a, c.block_tokens, st)
