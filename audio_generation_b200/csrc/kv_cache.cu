@@ -1127,10 +1127,10 @@ cudaError_t run_store(StoreArgs a, int block_tokens, cudaStream_t st) {
   // sequence and a block up to max_new would be empty: with as many rows as there
   // are, only rows / block_tokens + 2 n_seq of them can hold one.
   long long units = (long long)a.n_seq * a.pages;
-  if (units * a.kv_heads > 0x7fffffffLL) return cudaErrorInvalidValue;
   const long long most = a.rows / block_tokens + 2LL * a.n_seq;
   a.search = most < units;
   if (a.search) units = most;
+  if (units * a.kv_heads > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)(units * a.kv_heads);
   if (block_tokens == 32) k_kv_store<T, D, 32><<<grid, kStoreThreads<D, 32>, 0, st>>>(a);
   else if (block_tokens == 64) k_kv_store<T, D, 64><<<grid, kStoreThreads<D, 64>, 0, st>>>(a);

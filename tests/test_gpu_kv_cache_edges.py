@@ -4,7 +4,8 @@ import pytest
 import torch
 
 from audio_generation_b200 import h3
-from tests.test_gpu_kv_cache import BF, Cache, _new, _store_formula
+from tests.test_gpu_kv_cache import BF, HF, Cache, _new, _store_formula
+from tests.text_testlib import DEV
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +22,24 @@ def test_store_with_a_loose_bound_on_new_tokens(counts, most):
     assert h3.h3_text_error() == h3.H3_OK
     assert torch.equal(cache.ks, ks) and torch.equal(cache.vs, vs)
     assert torch.equal(cache.kc, kc) and torch.equal(cache.vc, vc)
+
+
+def test_store_into_wide_tables_of_many_sequences():
+    """4000 sequences whose tables have 9000 blocks for 64 heads: more (sequence,
+    block, head) triples than a grid may have, of which 40 rows can touch few."""
+    n, width, KH, D, BT = 4000, 9000, 64, 64, 32
+    cache = Cache([0, 0], KH, D, BT, spare=32)
+    first = cache.table[:, 0].clone()
+    counts = [0] * n
+    counts[17], counts[3990] = 30, 10
+    cache.table = torch.full((n, width), -1, dtype=torch.int32, device=DEV)
+    cache.table[17, 0], cache.table[3990, 0] = first[0], first[1]
+    cache.width, cache.lengths = width, torch.zeros(n, dtype=torch.int32, device=DEV)
+    k, v = _new([30, 10], KH, D, HF)
+    pair = Cache([0, 0], KH, D, BT, spare=32)
+    want = [_store_formula(pair, pair.kc, pair.ks, [30, 10], k, False),
+            _store_formula(pair, pair.vc, pair.vs, [30, 10], v, True)]
+    cache.store(counts, k, v, max_new=width * BT)
+    assert h3.h3_text_error() == h3.H3_OK
+    assert torch.equal(cache.kc, want[0][0]) and torch.equal(cache.ks, want[0][1])
+    assert torch.equal(cache.vc, want[1][0]) and torch.equal(cache.vs, want[1][1])
