@@ -407,7 +407,7 @@ struct AttnArgs {
   uint16_t* o;
   int64_t q_stride, o_stride;
   // workspace, per thread block: two parts (0: a pair begun earlier, 1: a pair
-  // that goes on) of kRows rows of sums and of (maximum, sum of weights), and
+  // that goes on) of kRows rows of averages and of (maximum, sum of weights), and
   // which pair part 1 belongs to, with the number of its parts
   float* part;    // [blocks][2][kRows][D]
   float2* stat;   // [blocks][2][kRows]
@@ -907,12 +907,14 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
       }
       m_all[k] = m;
       l_all[k] = l;
-      by[k] = (m_run[k] == m ? 1.f : exp2_mufu(m_run[k] - m)) * v_top;
+      by[k] = l == 0.f ? 0.f : (m_run[k] == m ? 1.f : exp2_mufu(m_run[k] - m)) / l;
     }
+    // Divided by the weights' sum before the V scale comes in: an average of the
+    // values is in float32's range wherever they are, a sum over the tokens may not be.
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[d][e] *= by[e & 1];
+      for (int e = 0; e < 4; ++e) acc[d][e] = acc[d][e] * by[e & 1] * v_top;
     auto each = [&](auto&& what) {  // (value, its place in a [kRows][PITCH] array)
 #pragma unroll
       for (int d = 0; d < ND; ++d)
@@ -935,17 +937,11 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
     const size_t slot = ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kRows;
     if (warp == 0) {
       const float* from = sums + kRows * PITCH;
-      each([&](float& x, int at) { x += from[at]; });
+      each([&](float& x, int at) { sums[at] = x + from[at]; });
+      if (!whole && g == 0) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        by[k] = !whole ? 1.f : l_all[k] == 0.f ? 0.f : 1.f / l_all[k];
-        if (!whole && g == 0) a.stat[slot + 2 * t + k] = make_float2(m_all[k], l_all[k]);
+        for (int k = 0; k < 2; ++k) a.stat[slot + 2 * t + k] = make_float2(m_all[k], l_all[k]);
       }
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[d][e] *= by[e & 1];
-      each([&](float& x, int at) { sums[at] = x; });
       if (!whole && begins) {
         // the range that holds the pair's end, and so the number of parts
         const long long end = pair_at + pages + kPairUnits;
@@ -998,7 +994,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_cache_join(const AttnArgs a
     float x[E];
   };
   __shared__ Piece sums[SLICES > 1 ? SLICES : 1][32];
-  __shared__ float weights[SLICES];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the ranges' kernel is complete
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slice = warp % SLICES;
   const int r = blockIdx.y * (kJoinWarps / SLICES) + warp / SLICES;
@@ -1023,12 +1018,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_cache_join(const AttnArgs a
     const int i = slice + k * SLICES;
     if (i < n) x[k] = part(i), ml[k] = a.stat[at(i)];
   }
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.stat[at(i)].x);
+  // the maximum and the weights' sum of all parts
+  const float2 own = lane < n ? a.stat[at(lane)] : make_float2(-INFINITY, 0.f);
+  float m = own.x, l = 0.f;
+  for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, a.stat[at(i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  auto weight = [&](const float2& part) {  // of a part's average
+    return part.y * (part.x == m ? 1.f : exp2_mufu(part.x - m));
+  };
+  l = weight(own);
+  for (int i = lane + 32; i < n; i += 32) l += weight(a.stat[at(i)]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   Piece sum = {};
-  float l = 0.f;
   for (int i0 = slice; i0 < n; i0 += kAhead * SLICES) {
     if (i0 > slice) {
 #pragma unroll
@@ -1040,31 +1044,26 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_cache_join(const AttnArgs a
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (i0 + k * SLICES >= n) break;
-      const float f = ml[k].x == m ? 1.f : exp2_mufu(ml[k].x - m);
+      const float f = weight(ml[k]) * inv;
 #pragma unroll
       for (int e = 0; e < E; ++e) sum.x[e] = fmaf(x[k].x[e], f, sum.x[e]);
-      l = fmaf(ml[k].y, f, l);
     }
   }
   if constexpr (SLICES > 1) {
     sums[slice][lane] = sum;
-    if (lane == 0) weights[slice] = l;
     __syncthreads();
     if (slice > 0) return;
 #pragma unroll
-    for (int i = 1; i < SLICES; ++i) {
+    for (int i = 1; i < SLICES; ++i)
 #pragma unroll
       for (int e = 0; e < E; ++e) sum.x[e] += sums[i][lane].x[e];
-      l += weights[i];
-    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t* o = a.o + cut.x * a.o_stride + (kvh * a.group + h0 + r) * D + E * lane;
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     reinterpret_cast<uint32_t*>(o)[e / 2] = a.f16
-                                                ? pack_f16x2(sum.x[e] * inv, sum.x[e + 1] * inv)
-                                                : pack_bf16x2(sum.x[e] * inv, sum.x[e + 1] * inv);
+                                                ? pack_f16x2(sum.x[e], sum.x[e + 1])
+                                                : pack_bf16x2(sum.x[e], sum.x[e + 1]);
 }
 
 // Thread blocks of an attention call: as many as run at once, at most one per
@@ -1163,8 +1162,8 @@ cudaError_t launch_kv_cache_store(const h3_kv_cache& c, int n_seq, int max_new,
   a.max_new = max_new;
   a.rows = rows;
   a.n_seq = n_seq;
-  // max_new tokens that begin anywhere inside a block (max_new may be any number up
-  // to INT_MAX: more than there are rows are none the more)
+  // max_new tokens that begin anywhere inside a block (in 64 bits: INT_MAX
+  // stands for no bound)
   a.pages = (int)std::min(((long long)max_new + c.block_tokens - 2) / c.block_tokens + 1,
                           (long long)width);
   a.err = err;

@@ -1,11 +1,13 @@
 """The 8-bit key / value cache at the ends of its arguments' ranges."""
 
+import math
+
 import pytest
 import torch
 
 from audio_generation_b200 import h3
-from tests.test_gpu_kv_cache import BF, HF, Cache, _new, _store_formula
-from tests.text_testlib import DEV
+from tests.test_gpu_kv_cache import BF, HF, Cache, _attention_formula, _new, _store_formula
+from tests.text_testlib import DEV, STEP, TINY, assert_within, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +45,19 @@ def test_store_into_wide_tables_of_many_sequences():
     assert h3.h3_text_error() == h3.H3_OK
     assert torch.equal(cache.kc, want[0][0]) and torch.equal(cache.ks, want[0][1])
     assert torch.equal(cache.vc, want[1][0]) and torch.equal(cache.vs, want[1][1])
+
+
+@pytest.mark.parametrize("lengths", [[9001], [40, 64, 300], [70] * 500])
+@pytest.mark.parametrize("scale", [1e34, 1e-36])
+def test_attention_over_values_at_the_ends_of_the_range(lengths, scale):
+    """Values up to 4e36, which bfloat16 holds but not their sum over the tokens, and
+    down to 1e-36: averages of them like any others (the bound of values between)."""
+    QH, KH, D = 8, 2, 128
+    cache = Cache(lengths, KH, D, 64)
+    cache.vs.mul_(scale / 0.01)
+    q = torch.randn(len(lengths), QH, D, generator=gen(4), device=DEV).to(BF)
+    o = cache.attend(q, 1 / math.sqrt(D))
+    assert h3.h3_text_error() == h3.H3_OK
+    ref, a = _attention_formula(cache, q, lengths, 1 / math.sqrt(D))
+    assert_within(o, ref, a * (2.0 ** -11 + 2.4e-4) + ref.abs() * STEP[BF] * 1.01
+                  + 127 * float(cache.vs.max()) * 2.0 ** -24 + 64 * TINY[BF])
