@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
     }
     uint32_t again = __ballot_sync(0xffffffffu, row_ok && !(worst <= 3.4028235e38f));
+    if (again) __syncwarp();  // other lanes have stored the row: that comes before
     while (again) {
       const int src = __ffs(again) - 1;
       again &= again - 1;
