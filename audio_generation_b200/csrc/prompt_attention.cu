@@ -84,6 +84,7 @@ struct Args {
   int64_t q_stride, k_stride, v_stride, o_stride;
   const int4* items;  // {first row of the prompt, first position (row), length, 0}
   int n_work;         // items * kv_heads
+  int rows;           // of the packed buffers
   bool single;        // items of one query tile
   int kv_heads, group, tile_pos;  // tile_pos = 128 / group positions per tile
   float scale_log2;
@@ -106,48 +107,122 @@ __device__ __forceinline__ float to_float(uint16_t u) {
 }
 
 // One output row by plain arithmetic, a warp together: for rows whose tiles gave
-// an infinity or a NaN. A key outside the row's range carries the weight 0, but
-// 0 times an infinite or NaN v of a later or a neighbouring prompt's token is
-// NaN in a matrix product; here only the row's own keys are touched, so what
-// they give is the row's true result.
+// an infinity or a NaN that they should not have. A key outside the row's range
+// carries the weight 0, but 0 times an infinite or NaN v of a later or a
+// neighbouring prompt's token is NaN in a matrix product; here only the row's own
+// keys are touched, so what they give is the row's true result. 32 keys at a time, D / 8 lanes to a row of k
+// or v: a lane multiplies its eight channels of as many keys as rows have lanes,
+// the sums are passed on by halves until each lane holds one key's score, and the
+// values' sums meet at the end. The weights stay float32, times 2^-32, so that no
+// sum of finite values leaves the range. A score that is NaN or infinite makes the
+// whole row NaN.
+constexpr float kPlainShift = -32.f;
+
+template <bool F16>
+__device__ __forceinline__ void to_floats(const uint4& u, float* x) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = to_float<F16>((uint16_t)w[k]);
+    x[2 * k + 1] = to_float<F16>((uint16_t)(w[k] >> 16));
+  }
+}
+
 template <int D, bool F16>
 __device__ __noinline__ void plain_row(const Args& a, int start, int pos, int head) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
+  constexpr int LANES = D / 8, ROWS = 32 / LANES;  // lanes of a row, rows of a load
+  const int lane = threadIdx.x & 31, c = lane % LANES, g = lane / LANES;
   const int kvh = head / a.group;
-  const uint16_t* q = a.q + (start + pos) * a.q_stride + head * D + lane * E;
-  float qv[E], acc[E];
+  const uint16_t* k = a.k + kvh * D + 8 * c;
+  const uint16_t* v = a.v + kvh * D + 8 * c;
+  uint4* o = reinterpret_cast<uint4*>(a.o + (start + pos) * a.o_stride + head * D + 8 * c);
+  float q[8], acc[8];
+  to_floats<F16>(*reinterpret_cast<const uint4*>(a.q + (start + pos) * a.q_stride + head * D +
+                                                 8 * c), q);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = to_float<F16>(q[e]);
-    acc[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j <= pos; ++j) {
-    const uint16_t* k = a.k + (start + j) * a.k_stride + kvh * D + lane * E;
-    const uint16_t* v = a.v + (start + j) * a.v_stride + kvh * D + lane * E;
-    float s = 0.f;
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  float m = -INFINITY, l = 0.f;  // l: of this lane's keys
+  for (int j0 = 0; j0 <= pos; j0 += 32) {
+    uint4 x[LANES];
 #pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(qv[e], to_float<F16>(k[e]), s);
+    for (int t = 0; t < LANES; ++t)  // key j0 + t ROWS + g
+      x[t] = *reinterpret_cast<const uint4*>(
+          k + (long long)(start + min(j0 + t * ROWS + g, pos)) * a.k_stride);
+    float part[LANES];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= a.scale_log2;
-    if (s > m) {
-      const float alpha = exp2_mufu(m - s);
+    for (int t = 0; t < LANES; ++t) {
+      float y[8], s0 = 0.f, s1 = 0.f;
+      to_floats<F16>(x[t], y);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) s0 = fmaf(q[e], y[e], s0), s1 = fmaf(q[e + 1], y[e + 1], s1);
+      part[t] = s0 + s1;
+    }
+#pragma unroll
+    for (int t = 0; t < LANES; ++t)  // asked for before the scores are needed
+      x[t] = *reinterpret_cast<const uint4*>(
+          v + (long long)(start + min(j0 + t * ROWS + g, pos)) * a.v_stride);
+#pragma unroll
+    for (int w = LANES / 2; w; w >>= 1)
+#pragma unroll
+      for (int t = 0; t < w; ++t) {
+        const bool high = lane & w;
+        const float give = high ? part[t] : part[t + w], keep = high ? part[t + w] : part[t];
+        part[t] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+      }
+    // the lane's key is j0 + c ROWS + g
+    const float s = j0 + c * ROWS + g <= pos ? part[0] * a.scale_log2 : -INFINITY;
+    if (__any_sync(0xffffffffu, !(s < INFINITY))) {
+      const uint32_t nan = F16 ? 0x7e007e00u : 0x7fc07fc0u;
+      if (g == 0) *o = make_uint4(nan, nan, nan, nan);
+      return;
+    }
+    float to = s;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, d));
+    if (to > m) {
+      const float alpha = exp2_mufu(m - to);
       l *= alpha;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= alpha;
-      m = s;
+      for (int e = 0; e < 8; ++e) acc[e] *= alpha;
+      m = to;
     }
-    const float p = s == -INFINITY ? 0.f : exp2_mufu(s - m);
+    const float p = s == -INFINITY ? 0.f : exp2_mufu(s - m + kPlainShift);
     l += p;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(p, to_float<F16>(v[e]), acc[e]);
-  }
-  uint16_t* o = a.o + (start + pos) * a.o_stride + head * D + lane * E;
+    for (int t = 0; t < LANES; ++t) {
+      const float w = __shfl_sync(0xffffffffu, p, g * LANES + t);
+      float y[8];
+      to_floats<F16>(x[t], y);
+      if (j0 + t * ROWS + g <= pos) {
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(o + e) = pack2<F16>(acc[e] / l, acc[e + 1] / l);
+        for (int e = 0; e < 8; ++e) acc[e] = fmaf(w, y[e], acc[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+#pragma unroll
+  for (int d = LANES; d < 32; d <<= 1)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], d);
+  if (g == 0)
+    *o = make_uint4(pack2<F16>(acc[0] / l, acc[1] / l), pack2<F16>(acc[2] / l, acc[3] / l),
+                    pack2<F16>(acc[4] / l, acc[5] / l), pack2<F16>(acc[6] / l, acc[7] / l));
+}
+
+// Which of eight neighbouring values are infinities or NaN, a bit for each.
+template <bool F16>
+__device__ __forceinline__ uint32_t not_finite_8(const uint16_t* x) {
+  constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+  const uint4 u = *reinterpret_cast<const uint4*>(x);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t bad = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if ((w[k] & kExp) == kExp) bad |= 1u << (2 * k);
+    if ((w[k] >> 16 & kExp) == kExp) bad |= 2u << (2 * k);
+  }
+  return bad;
 }
 
 template <int D, bool F16>
@@ -372,6 +447,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t o_col = lane_base + 256 + i * 128;
     const uint64_t scale2 = f2_pack(a.scale_log2, a.scale_log2);
     bool ok = true;
+    uint32_t marked = 0;  // bit w % 32: piece w has rows with an infinity or a NaN
     int done = 0, rounds = 0;  // score tiles, and items with work, so far
     Item x;
     for (int w = 0; ok && piece(w, x); ++w) {
@@ -434,7 +510,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
       // P = 2^(s * scale - m + shift) in the type of v, over S columns already
       // held in registers, in two halves (one arrival per warp each).
-      const uint64_t negm2 = f2_pack(kShift - m_run, kShift - m_run);
+      // (Scores that are all -inf so far have weight 0.)
+      const float sub = kShift - (m_run == -INFINITY ? 0.f : m_run);
+      const uint64_t negm2 = f2_pack(sub, sub);
       uint64_t sum2[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -474,7 +552,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_fence_after();
     const int head = x.kvh * a.group + r - rp * a.group;
     const bool row_ok = rp < P && pos < x.len;
-    const float inv_l = 1.f / l_run;
+    // A NaN or an infinity among the row's own scores makes its weights NaN, or the
+    // largest number by the cubic: the row is NaN then, and needs no other look.
+    const bool scores_ok = l_run < 1e37f;
+    const float inv_l = scores_ok ? 1.f / l_run : __int_as_float(0x7fc00000);
     // A row's 64 bytes at a time; four lanes turn their pieces of 16 so that a
     // store covers 64 bytes of eight rows instead of 16 of 32.
     const long long mine = row_ok ? (x.start + pos) * a.o_stride + head * D : -1;
@@ -521,14 +602,49 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           *reinterpret_cast<uint4*>(a.o + dst[k] + 32 * c + 8 * (lane & 3)) =
               make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
     }
-    uint32_t again = __ballot_sync(0xffffffffu, row_ok && !(worst <= 3.4028235e38f));
-    if (again) __syncwarp();  // other lanes have stored the row: that comes before
-    while (again) {
-      const int src = __ffs(again) - 1;
-      again &= again - 1;
-      plain_row<D, F16>(a, x.start, __shfl_sync(0xffffffffu, pos, src),
-                        __shfl_sync(0xffffffffu, head, src));
+    if (__any_sync(0xffffffffu, row_ok && scores_ok && !(worst <= 3.4028235e38f)))
+      marked |= 1u << (w & 31);
     }
+    // A row with an infinity or a NaN is computed again if a v outside its range has
+    // one too, in the same channel and in a key tile that the row's tile visits. (Any
+    // other comes from the row's own keys.) That happens when no other warp waits for
+    // this one any more, so that no wait runs out over it, however long the prompts.
+    // 8192 tokens, 56 heads over 8 x 128: 0.82 ms without a bad v, 0.87 with one at
+    // token 3, 8.4 at token 4000, 16 at token 8000 (32 rows of a warp over all keys).
+    __syncwarp();  // rows are stored by other lanes: that comes before
+    for (int w = 0; ok && marked != 0 && piece(w, x); ++w) {
+      const int tiles = i == 0 ? x.n0 : x.n1;
+      if ((marked >> (w & 31) & 1) == 0 || tiles == 0) continue;
+      const int tile0 = x.pos0 + i * P, pos = tile0 + rp;
+      const int head = x.kvh * a.group + r - rp * a.group;
+      const bool row_ok = rp < P && pos < x.len;
+      const int end = min(tiles * 128, a.rows - x.start);
+      bool again = false;
+      for (int c = 0; c < D; c += 8) {
+        const uint32_t mine =
+            row_ok ? not_finite_8<F16>(a.o + (x.start + pos) * a.o_stride + head * D + c) : 0;
+        if (!__any_sync(0xffffffffu, mine != 0)) continue;
+        int last[8];  // the last key with a bad v, of each channel
+#pragma unroll
+        for (int e = 0; e < 8; ++e) last[e] = -1;
+        for (int j0 = tile0; j0 < end; j0 += 32) {
+          const int j = j0 + lane;
+          const uint32_t bad =
+              j < end ? not_finite_8<F16>(a.v + (x.start + j) * a.v_stride + x.kvh * D + c) : 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            last[e] = max(last[e], __reduce_max_sync(0xffffffffu, (bad >> e & 1) ? j : -1));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) again |= (mine >> e & 1) && last[e] > pos;
+      }
+      uint32_t rows = __ballot_sync(0xffffffffu, again);
+      while (rows) {
+        const int src = __ffs(rows) - 1;
+        rows &= rows - 1;
+        plain_row<D, F16>(a, x.start, __shfl_sync(0xffffffffu, pos, src),
+                          __shfl_sync(0xffffffffu, head, src));
+      }
     }
   }
   __syncthreads();
@@ -857,6 +973,7 @@ cudaError_t launch_prompt_attention(const h3_prompts* p, bool f16, const void* q
   a.o_stride = o_stride;
   a.items = static_cast<const int4*>(p->items);
   a.n_work = p->n_items * p->kv_heads;
+  a.rows = p->rows;
   a.kv_heads = p->kv_heads;
   a.group = p->q_heads / p->kv_heads;
   a.tile_pos = 128 / a.group;

@@ -599,8 +599,11 @@ H3_API void h3_prompts_destroy(h3_prompts_t prompts);
  * overlap the inputs. Rows of o outside every prompt are left as they were. Sums
  * and softmax statistics are float32; the softmax weights are rounded to `type`
  * before the product with v. What a row holds does not depend on the values of
- * rows it does not attend, infinities and NaN included. Runs on the device of
- * the prompts object, which must be current (else H3_ERR_ARG). Enqueues. */
+ * rows it does not attend, infinities and NaN included, but for its last bits: rows
+ * up to 128 tokens before an infinite or NaN v, or beside one of a neighbouring
+ * prompt, are computed again with weights that are not rounded (at about 60 ns a
+ * key, up to 32 rows one after another). Runs on the device of the prompts object,
+ * which must be current (else H3_ERR_ARG). Enqueues. */
 H3_API h3_status h3_prompt_attention(h3_prompts_t prompts, h3_type type, const void* q,
                                      int64_t q_stride, const void* k, int64_t k_stride,
                                      const void* v, int64_t v_stride, float scale, void* o,

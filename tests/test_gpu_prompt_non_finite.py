@@ -4,6 +4,7 @@ the formula over its own keys gives, whatever its tiles hold beside them."""
 import pytest
 import torch
 
+from audio_generation_b200 import h3
 from tests.test_gpu_prompt_attention import BF, HF, _allowed, _offsets, _reference, _run
 from tests.text_testlib import DEV, assert_within
 
@@ -34,3 +35,63 @@ def test_bad_values_in_tiles_shared_with_others(QH, KH, D, dtype, bad):
     ref, a = _reference(q, k, v, offsets, scale)
     keep = ~touched
     assert_within(o[keep], ref[keep], _allowed(ref, a, dtype)[keep])
+
+
+@pytest.mark.parametrize("at,most_ms", [(4, 3.0), (3000, 12.0), (5950, 20.0)])
+@pytest.mark.parametrize("which", ["k", "v", "kv"])
+def test_a_bad_token_in_a_long_prompt(which, at, most_ms):
+    """A NaN k reaches every later row of its heads, an infinite v one channel of
+    them. The time is bounded: rows of one tile and the 128 keys around the bad v are
+    computed again, 32 to a warp, at about 50 to 100 cycles a key, at most 10 ms for
+    6000 keys; every later row, key by key at 600 cycles, would be 60 ms."""
+    QH, KH, D, T = 8, 2, 128, 6000
+
+    def poison(q, k, v):
+        if "k" in which:
+            k[at, 0, 7] = float("nan")
+        if "v" in which:
+            v[at, 1, 5] = float("inf")
+
+    q, k, v, o, offsets, scale = _run([T], QH, KH, D, BF, prepare=poison)
+    touched = torch.zeros(T, QH, D, dtype=torch.bool, device=DEV)
+    if "k" in which:
+        touched[at:, :4] = True
+        assert bool(torch.isnan(o[at:, :4]).all())
+    if "v" in which:
+        touched[at:, 4:, 5] = True
+    assert torch.equal(torch.isfinite(o), ~touched)
+    again = torch.empty_like(o)
+    p = h3.h3_prompts_prepare(offsets, QH, KH, D)
+    times = []
+    for _ in range(3):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        h3.h3_prompt_attention(p, BF, q, QH * D, k, KH * D, v, KH * D, scale, again, QH * D)
+        b.record()
+        b.synchronize()
+        times.append(a.elapsed_time(b))
+    assert torch.equal(again.view(torch.int16), o.view(torch.int16))  # NaN too
+    assert min(times) < most_ms, times
+    if "k" in which:
+        k[at, 0, 7] = 0
+    if "v" in which:
+        v[at, 1, 5] = 0
+    ref, w = _reference(q, k, v, offsets, scale)
+    assert_within(o[~touched], ref[~touched], _allowed(ref, w, BF)[~touched])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_keys_of_minus_infinity_weigh_nothing(dtype):
+    """Scores of -inf, for a whole first tile of keys and for some later ones: weight
+    0, and NaN only for rows that have no other score."""
+    def minus(q, k, v):
+        q[:, :, 0] = 1.0
+        k[:, :, 0] = 0.0
+        k[:200, 0, 0] = -float("inf")
+        k[250:300, 1, 0] = -float("inf")
+    q, k, v, o, offsets, scale = _run([700], 4, 2, 64, dtype, prepare=minus)
+    assert bool(torch.isnan(o[:200, :2]).all())
+    assert bool(torch.isfinite(o[200:, :2]).all()) and bool(torch.isfinite(o[:, 2:]).all())
+    ref, a = _reference(q, k, v, offsets, scale)
+    for rows, heads in ((slice(200, None), slice(0, 2)), (slice(None), slice(2, 4))):
+        assert_within(o[rows, heads], ref[rows, heads], _allowed(ref, a, dtype)[rows, heads])

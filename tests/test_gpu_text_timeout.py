@@ -42,3 +42,16 @@ def test_a_cache_block_that_does_not_come(child):
     assert res["normal"] == h3.H3_OK
     status, values = cache_case(h3)()  # the product library on the same inputs: the same bits
     assert status == h3.H3_OK and values == res["values"]
+
+
+def test_rows_computed_again_do_not_let_a_wait_run_out(child):
+    """A bad v near the end of 200000 tokens, so that the rows of its tile before it
+    have to be computed again, under a limit of 50 ms for a wait: at about 50 cycles a
+    key the rows of a warp take longer than that. Rows of eight tokens and more: a
+    product's weights are rounded to 2^-8 of each, |v| is below 6, and both results
+    to 2^-8 of at most 3."""
+    from audio_generation_b200 import h3
+    res = child("prompt")
+    assert res["status"] == h3.H3_OK and res["again"] == h3.H3_OK
+    assert res["as_expected"] and res["diff"] < 6 * 2.0 ** -8 + 2 * 3 * 2.0 ** -8
+    assert res["ms"] > 50

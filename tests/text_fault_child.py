@@ -50,11 +50,38 @@ def cache(h3, lib):
     return out
 
 
+def prompt(h3, lib):
+    """One prompt with an infinite v near its end: the rows computed again by plain
+    arithmetic take far longer than a wait may."""
+    T, D, at = 200000, 64, 199900
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    q, k, v = (torch.randn(T, 1, D, generator=g, device="cuda").to(BF) for _ in range(3))
+    v[at, 0, 5] = float("inf")
+    o = torch.zeros_like(q)
+    p = h3.h3_prompts_prepare([0, T], 1, 1, D)
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    h3.h3_prompt_attention(p, BF, q, D, k, D, v, D, 0.125, o, D)
+    b.record()
+    status = h3.h3_text_error()
+    bad = ~torch.isfinite(o[:, 0])
+    want = torch.zeros_like(bad)
+    want[at:, 5] = True
+    v[at, 0, 5] = 0
+    clean = torch.zeros_like(q)
+    h3.h3_prompt_attention(p, BF, q, D, k, D, v, D, 0.125, clean, D)
+    # the values are means of many: about 0.01, their weights rounded to 2^-8 or not
+    diff = (o - clean).float().abs()[:, 0].masked_fill(want, 0)[8:]
+    return {"status": status, "as_expected": bool(torch.equal(bad, want)),
+            "again": h3.h3_text_error(), "diff": float(diff.max()), "ms": a.elapsed_time(b)}
+
+
 def main(lib_path: str, case: str) -> None:
     from audio_generation_b200 import h3
     h3.LIB_PATH = lib_path
     h3._lib = None
-    print("RESULT " + json.dumps({"cache": cache}[case](h3, h3.lib())))
+    print("RESULT " + json.dumps({"cache": cache, "prompt": prompt}[case](h3, h3.lib())))
 
 
 if __name__ == "__main__":
