@@ -233,8 +233,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   constexpr int TILE = tile_bytes<D>();
   constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE, OFF_BAR = 6 * TILE;
   // fp16 P: weights are stored times 2^7 (at most 2^15 with the lazy maximum),
-  // so that they stay normal numbers down to 2^-21 of the largest.
-  constexpr float kShift = F16 ? 7.f : 0.f;
+  // so that they stay normal numbers down to 2^-21 of the largest. bfloat16 P: times
+  // 2^-24, so that up to 65536 products with the largest v stay within float32.
+  constexpr float kShift = F16 ? 7.f : -24.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));

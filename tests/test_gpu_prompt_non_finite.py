@@ -6,7 +6,7 @@ import torch
 
 from audio_generation_b200 import h3
 from tests.test_gpu_prompt_attention import BF, HF, _allowed, _offsets, _reference, _run
-from tests.text_testlib import DEV, assert_within
+from tests.text_testlib import DEV, STEP, assert_within
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +95,17 @@ def test_keys_of_minus_infinity_weigh_nothing(dtype):
     ref, a = _reference(q, k, v, offsets, scale)
     for rows, heads in ((slice(200, None), slice(0, 2)), (slice(None), slice(2, 4))):
         assert_within(o[rows, heads], ref[rows, heads], _allowed(ref, a, dtype)[rows, heads])
+
+
+@pytest.mark.parametrize("lengths", [[40, 7], [600]])
+def test_the_largest_values_of_the_type_average_to_themselves(lengths):
+    """Sums of bfloat16's largest number leave float32, their average does not."""
+    def largest(q, k, v):
+        v.fill_(torch.finfo(BF).max)
+        v[:, :, 1::2] *= -1
+        v[:, :, 2] = 1.0
+    q, k, v, o, offsets, scale = _run(lengths, 4, 2, 64, BF, prepare=largest)
+    assert bool((o[:, :, 0] >= torch.finfo(BF).max * (1 - 4 * STEP[BF])).all())
+    assert bool(torch.isfinite(o).all())
+    ref, a = _reference(q, k, v, offsets, scale)
+    assert_within(o, ref, _allowed(ref, a, BF))
