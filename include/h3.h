@@ -566,8 +566,10 @@ H3_API h3_status h3_quantize_int8_rows(h3_type type, int rows, int K, const void
 /* out[m, n] = a_scales[m] * w_scales[n] * sum_k a_codes[m, k] * w_codes[n, k]:
  * int8 codes a [M, K], w [N, K] (any value, -128 too), the sum exact in 32-bit
  * integers, scales float32, out of `out_type`, row m out_stride elements after
- * row m - 1 (columns past N are not written). 0 <= M, N <= 2^30; K % 16 == 0 and
- * 0 < K <= 131056 (the sum cannot leave 32 bits); out_stride >= N. Enqueues. */
+ * row m - 1 (columns past N are not written). The sum and both products with it
+ * are rounded to float32 (an infinity only where the value is out of its range,
+ * whatever the scales), the result once more to out_type. 0 <= M, N <= 2^30; K % 16
+ * == 0 and 0 < K <= 131056 (the sum cannot leave 32 bits); out_stride >= N. Enqueues. */
 H3_API h3_status h3_matmul_int8(int M, int N, int K, const void* a_codes, const float* a_scales,
                                 const void* w_codes, const float* w_scales, h3_type out_type,
                                 void* out, int64_t out_stride, h3_stream_t stream);
