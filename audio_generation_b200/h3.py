@@ -559,9 +559,10 @@ def _type(t) -> int:
 
 
 def _current_device() -> int:
-    """The current device's index, -1 before CUDA has been used."""
+    """The current device's index; before CUDA has been used, when no tensor can be
+    on one, a number that is no tensor's (a host tensor's is -1)."""
     import torch
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
 
 def _dev_ptr(t, device: int, where: str) -> Optional[int]:
@@ -575,7 +576,8 @@ def _dev_ptr(t, device: int, where: str) -> Optional[int]:
         if t is None or isinstance(t, int):
             return t
         raise
-    raise H3Error(H3_ERR_ARG, f"{where}: tensor on {t.device}, current device {device}")
+    raise H3Error(H3_ERR_ARG, f"{where}: tensor on {t.device}, current device "
+                  f"{device if device >= 0 else 'none yet'}")
 
 
 def h3_quantize_int8_rows(dtype, rows: int, K: int, x, x_stride: int, codes, scales,
