@@ -195,11 +195,25 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _cuda_functions():
+    """torch's (is_initialized, current device, its current stream), bound at the first
+    use: an import statement in each call costs it 0.2 us."""
+    global _cuda
+    import torch
+    _cuda = (torch.cuda.is_initialized, torch._C._cuda_getDevice,
+             torch._C._cuda_getCurrentRawStream)
+    return _cuda
+
+
+_cuda = None
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        initialized, device, raw_stream = _cuda or _cuda_functions()
+        if initialized():  # the current stream without an object made for it
+            return raw_stream(device())
         import torch
-        if torch.cuda.is_initialized():  # the current stream without an object made for it
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -561,8 +575,8 @@ def _type(t) -> int:
 def _current_device() -> int:
     """The current device's index; before CUDA has been used, when no tensor can be
     on one, a number that is no tensor's (a host tensor's is -1)."""
-    import torch
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    initialized, device, _ = _cuda or _cuda_functions()
+    return device() if initialized() else -2
 
 
 def _dev_ptr(t, device: int, where: str) -> Optional[int]:
@@ -646,11 +660,22 @@ def h3_prompt_attention(prompts: Prompts, dtype, q, q_stride: int, k, k_stride: 
 
 def make_kv_cache(k_codes, v_codes, k_scales, v_scales) -> h3_kv_cache:
     """The cache descriptor of a pool's tensors, sizes from k_codes [n_blocks,
-    kv_heads, block_tokens, head_dim] (the caller keeps the tensors)."""
+    kv_heads, block_tokens, head_dim] (the caller keeps the tensors). The library
+    knows the pool by its sizes alone, so the tensors have to be contiguous: codes of
+    one byte, scales float32 [n_blocks, kv_heads]."""
     n_blocks, kv_heads, block_tokens, head_dim = k_codes.shape
     if v_codes.shape != (n_blocks, kv_heads, head_dim, block_tokens):
         raise H3Error(H3_ERR_SHAPE, "make_kv_cache")
     d, w = _current_device(), "make_kv_cache"
+    try:
+        if not (k_codes.is_contiguous() and v_codes.is_contiguous()
+                and k_codes.element_size() == 1 == v_codes.element_size()
+                and k_scales.is_contiguous() and v_scales.is_contiguous()
+                and k_scales.numel() == n_blocks * kv_heads == v_scales.numel()
+                and k_scales.element_size() == 4 == v_scales.element_size()):
+            raise H3Error(H3_ERR_SHAPE, w)
+    except AttributeError:  # scales given as addresses
+        pass
     return h3_kv_cache(n_blocks, block_tokens, kv_heads, head_dim, _dev_ptr(k_codes, d, w),
                        _dev_ptr(v_codes, d, w), _dev_ptr(k_scales, d, w), _dev_ptr(v_scales, d, w))
 
@@ -660,7 +685,7 @@ def h3_kv_cache_store(cache: h3_kv_cache, n_seq: int, max_new: int, block_table,
                       v_stride: int, rows: Optional[int] = None, stream=None) -> None:
     """rows: the rows of k and v (from k's first dimension by default)."""
     if rows is None:
-        rows = k.shape[0]
+        rows = k.size(0)
     d, w = _current_device(), "h3_kv_cache_store"
     _check(lib().h3_kv_cache_store(ctypes.byref(cache), n_seq, max_new,
                                    _dev_ptr(block_table, d, w), table_width,

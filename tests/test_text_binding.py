@@ -49,3 +49,26 @@ def test_host_tensors_are_refused_before_cuda_is_in_use(call, monkeypatch):
         with pytest.raises(h3.H3Error) as e:
             fn(*given)
         assert e.value.status == h3.H3_ERR_ARG and "cpu" in str(e.value)
+
+
+def _pool(n=3, KH=2, BT=32, D=64):
+    return [torch.zeros(n, KH, BT, D).char(), torch.zeros(n, KH, D, BT).char(),
+            torch.zeros(n, KH), torch.zeros(n, KH)]
+
+
+@pytest.mark.parametrize("which,other", [
+    (0, lambda t: torch.zeros(3, 4, 32, 64).char()[:, ::2]),  # every other head of a larger pool
+    (1, lambda t: torch.zeros(3, 2, 64, 64).char()[..., :32]),
+    (1, lambda t: torch.zeros(3, 2, 32, 64).char().transpose(2, 3)),
+    (0, lambda t: t.half()), (1, lambda t: t.float()),
+    (2, lambda t: torch.ones(1, 2).expand(3, 2)), (3, lambda t: torch.ones(2, 3).t()),
+    (2, lambda t: t.double()), (3, lambda t: t[:2]), (2, lambda t: torch.ones(3))])
+def test_a_pool_that_is_not_what_its_sizes_say_is_refused(which, other, monkeypatch):
+    """Strides that the library cannot know, and tensors that end before it does."""
+    monkeypatch.setattr(h3, "_current_device", lambda: -1)  # let host tensors pass
+    pool = _pool()
+    assert h3.make_kv_cache(*pool).n_blocks == 3
+    pool[which] = other(pool[which])
+    with pytest.raises(h3.H3Error) as e:
+        h3.make_kv_cache(*pool)
+    assert e.value.status == h3.H3_ERR_SHAPE
