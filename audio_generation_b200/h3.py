@@ -640,6 +640,8 @@ def h3_prompts_prepare(offsets: Sequence[int], q_heads: int, kv_heads: int,
     if len(offsets) == 0:
         raise H3Error(H3_ERR_ARG, "h3_prompts_prepare")
     arr = (ctypes.c_int32 * len(offsets))(*offsets)
+    if arr[:] != list(offsets):  # past int32, which ctypes cuts off
+        raise H3Error(H3_ERR_LAYOUT, "h3_prompts_prepare")
     out = ctypes.c_void_p()
     _check(lib().h3_prompts_prepare(arr, len(offsets) - 1, q_heads, kv_heads, head_dim,
                                     ctypes.byref(out)), "h3_prompts_prepare")

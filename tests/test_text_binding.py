@@ -72,3 +72,17 @@ def test_a_pool_that_is_not_what_its_sizes_say_is_refused(which, other, monkeypa
     with pytest.raises(h3.H3Error) as e:
         h3.make_kv_cache(*pool)
     assert e.value.status == h3.H3_ERR_SHAPE
+
+
+@pytest.mark.parametrize("offsets", [[0, 2 ** 32 + 4], [2 ** 32, 2 ** 32 + 4], [0, 5, 2 ** 33 + 9]])
+def test_offsets_past_int32_are_refused(offsets, monkeypatch):
+    class NoLibrary:
+        h3_status_string = h3.lib().h3_status_string
+
+        @staticmethod
+        def h3_prompts_prepare(*args):
+            raise AssertionError("called with other offsets")
+    monkeypatch.setattr(h3, "lib", NoLibrary)
+    with pytest.raises(h3.H3Error) as e:
+        h3.h3_prompts_prepare(offsets, 4, 2, 64)
+    assert e.value.status == h3.H3_ERR_LAYOUT
