@@ -351,8 +351,8 @@ __global__ void __launch_bounds__(kStoreThreads<D, BT>,
 // takes its operands from registers as the codes lie in shared memory; the kernel
 // is bound by bytes and then by the instructions per byte, not by the tensor
 // rate.) Scores: s^T = K q^T on 8-bit integers (m16n8k32), q as two 8-bit limbs of
-// a 16-bit fixed-point row (an error of at most 2^-16 of the row's largest
-// element), the sums exact. Values: o^T += V^T w^T on fp16 (m16n8k16), where the
+// a 16-bit fixed-point row (an error of at most half of its largest element's
+// 32512th, 2^-15.98 of that element), the sums exact. Values: o^T += V^T w^T on fp16 (m16n8k16), where the
 // codes become fp16 exactly and the weights are fp16, times 2^15 so that they
 // stay normal numbers down to 2^-29 of the largest, and times the block's V scale
 // over the largest one met so far, so that the sums of all blocks share one
@@ -867,11 +867,10 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
           if constexpr (NB == 8) {
             const uint4 x = *reinterpret_cast<const uint4*>(v);
             w[r][0] = x.x, w[r][1] = x.y, w[r][2] = x.z, w[r][3] = x.w;
-          } else if constexpr (NB == 4) {
+          } else {
+            static_assert(NB == 4, "a warp takes 32 or 64 tokens of a cache block");
             const uint2 x = *reinterpret_cast<const uint2*>(v);
             w[r][0] = x.x, w[r][1] = x.y;
-          } else {
-            w[r][0] = *reinterpret_cast<const uint32_t*>(v);
           }
         }
 #pragma unroll
