@@ -599,8 +599,9 @@ H3_API void h3_prompts_destroy(h3_prompts_t prompts);
  * elements (>= heads * head_dim, a multiple of 8), so that slices of one
  * projection's output can be given as they are. scale > 0, finite. o may not
  * overlap the inputs. Rows of o outside every prompt are left as they were. Sums
- * and softmax statistics are float32; the softmax weights are rounded to `type`
- * before the product with v. What a row holds does not depend on the values of
+ * and softmax statistics are float32, the exponentials among them within 1.02e-4
+ * (a sixth of them, the others 2^-22); the softmax weights are rounded to `type`
+ * before the product with v, their sum is of the unrounded ones. What a row holds does not depend on the values of
  * rows it does not attend, infinities and NaN included, but for its last bits: rows
  * up to 128 tokens before an infinite or NaN v, or beside one of a neighbouring
  * prompt, are computed again with weights that are not rounded (at about 60 ns a
@@ -666,9 +667,11 @@ H3_API h3_status h3_kv_cache_store(const h3_kv_cache* cache, int n_seq, int max_
  * counts as tokens that are not there: both record an error (h3_text_error,
  * H3_ERR_LAYOUT). ws: h3_cache_attention_workspace_size bytes (a few MB at most),
  * used only during the call's work: calls that overlap on the GPU need one each.
- * The result does not depend on the order in which the GPU runs things. Values are
- * summed relative to the largest V scale of the sequence and kv head, to about
- * 2^-24 of its largest value. Enqueues. */
+ * The result does not depend on the order in which the GPU runs things. What is held
+ * in fewer than float32's bits: a row of q in 16-bit fixed point (each element off by
+ * up to 2^-16 of the row's largest, and a score by that times sum |k|), the weights in
+ * fp16, summed after rounding. Values are summed relative to the largest V scale of
+ * the sequence and kv head, to about 2^-24 of its largest value. Enqueues. */
 H3_API size_t h3_cache_attention_workspace_size(const h3_kv_cache* cache, int n_seq, int q_heads,
                                                 int table_width);
 H3_API h3_status h3_cache_attention(const h3_kv_cache* cache, int n_seq, int q_heads,

@@ -61,3 +61,28 @@ def test_attention_over_values_at_the_ends_of_the_range(lengths, scale):
     ref, a = _attention_formula(cache, q, lengths, 1 / math.sqrt(D))
     assert_within(o, ref, a * (2.0 ** -11 + 2.4e-4) + ref.abs() * STEP[BF] * 1.01
                   + 127 * float(cache.vs.max()) * 2.0 ** -24 + 64 * TINY[BF])
+
+
+@pytest.mark.parametrize("D,BT", [(64, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("factor", [16.0, 256.0])
+def test_attention_of_queries_with_outlier_channels(D, BT, factor):
+    """A few channels far above the rest. An element of q is off by up to half of its
+    row's largest one's 32512th, so a score by that times sum |k| scale; weights are
+    off by twice the largest such error, which is added to the usual bound."""
+    QH, KH, lengths = 8, 2, [700, 33]
+    cache = Cache(lengths, KH, D, BT)
+    q = torch.randn(2, QH, D, generator=gen(11), device=DEV)
+    q[:, :, 3] *= factor
+    q[:, ::2, 40] *= factor / 4
+    q = q.to(BF)
+    scale = 1 / math.sqrt(D) / factor  # weights spread over the tokens
+    o = cache.attend(q, scale)
+    assert h3.h3_text_error() == h3.H3_OK
+    ref, a = _attention_formula(cache, q, lengths, scale)
+    off = torch.zeros(2, QH, 1, dtype=torch.float64, device=DEV)
+    for s, n in enumerate(lengths):
+        k, _ = cache.values(s, n)
+        most = k.abs().sum(-1).amax(-1).repeat_interleave(QH // KH)
+        off[s, :, 0] = q[s].double().abs().amax(-1) / 32512 / 2 * most * scale
+    assert_within(o, ref, a * (2.0 ** -11 + 2.4e-4 + torch.expm1(2 * off))
+                  + ref.abs() * STEP[BF] * 1.01 + 64 * TINY[BF])
