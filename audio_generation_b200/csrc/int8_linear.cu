@@ -96,10 +96,16 @@ __global__ void __launch_bounds__(G == 32 ? 256 : G == 0 ? 1024 : G)
 
 // Short rows take a warp, longer ones a block of as many warps as hold them at
 // eight vectors a thread (four where there are few rows, so that a row's loads
-// are all in flight and little is done in turn), so that few threads idle. The
-// usual lengths have their block size built in: 14336 bf16 elements a row, 8192
-// rows, 57 us against 62 us with the block size read at run time (and with seven
-// warps instead of eight, which leave an SM fewer); now 53.3 us, 6.6 TB/s.
+// are all in flight and little is done in turn), so that few threads idle. 8192 rows
+// of 14336 bf16 elements: 53.3 us, 6.6 TB/s.
+// Block sizes built in, against the one read at run time (us for 8192 rows, bf16 unless
+// said): 64 threads always (K of 2560 10.8 against 11.7, 4096 16.1 : 16.3, float32 1536
+// 10.0 : 11.2, 2048 12.6 : 13.1); 96, 128 and 256 where the last vectors are not all
+// there (5120 19.8 : 21.6, 7168 26.5 : 28.0, 13312 51.6 : 55.0, 14336 54.3 : 57.3; float32
+// 3584 21.5 : 22.2, 7168 44.1 : 45.5, but 2560 17.6 : 16.9), not where they are (6144
+// 25.0 : 24.4, 8192 33.4 : 31.6, 16384 66.8 : 62.7; float32 4096 26.7 : 24.9, 8192 55.8 :
+// 52.9); 160 and 192 never (10240 43.9 : 41.4, 12288 51.5 : 49.0; float32 5120 34.3 :
+// 31.4), and 224 take 256 (14336 with 224 built in 62.7).
 template <h3_type T>
 cudaError_t quantize(int rows, int K, const void* x, int64_t stride_vec, void* codes,
                      float* scales, cudaStream_t st) {
@@ -113,9 +119,9 @@ cudaError_t quantize(int rows, int K, const void* x, int64_t stride_vec, void* c
   else if (nvec <= 256) H3_Q(32, 8, (rows + 7) / 8, 256);
   else if (nvec <= 4096 && rows <= 4 * num_sms()) H3_Q(0, 4, rows, few);
   else if (many == 64) H3_Q(64, 8, rows, 64);
-  else if (many == 96) H3_Q(96, 8, rows, 96);
-  else if (many == 128) H3_Q(128, 8, rows, 128);
-  else if (many == 224 || many == 256) H3_Q(256, 8, rows, 256);
+  else if (many == 96 && nvec < 768) H3_Q(96, 8, rows, 96);
+  else if (many == 128 && nvec < 1024) H3_Q(128, 8, rows, 128);
+  else if (many >= 224 && nvec < 2048) H3_Q(256, 8, rows, 256);
   else if (nvec <= 8192) H3_Q(0, 8, rows, many);
   else H3_Q(0, 0, rows, 1024);
 #undef H3_Q

@@ -1,4 +1,5 @@
-"""The product of int8 codes with scales at the ends of float32's range."""
+"""The int8 linear layer: row lengths on both sides of every choice of a block size,
+and products with scales at the ends of float32's range."""
 
 import pytest
 import torch
@@ -64,3 +65,19 @@ def test_nan_scales_reach_their_row_and_column(M, N, K):
     nan[1] = nan[:, N - 1] = True
     assert torch.equal(torch.isnan(out), nan)
     assert torch.equal(out[~nan], sums[~nan].float())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, F32])
+@pytest.mark.parametrize("vectors", [257, 512, 513, 767, 768, 769, 1023, 1024, 1025, 1536, 1537,
+                                     1792, 2047, 2048, 2049])
+def test_row_lengths_around_the_block_sizes(vectors, dtype):
+    """Bit for bit, at and beside the numbers of 16-byte vectors where a form ends."""
+    per = 16 // dtype.itemsize
+    rows, K = 600, (vectors * per + 15) // 16 * 16
+    x = torch.randn(rows, K, generator=gen(vectors), device=DEV).to(dtype)
+    codes = torch.full((rows, K), 77, dtype=torch.int8, device=DEV)
+    scales = torch.full((rows,), -7.0, device=DEV)
+    h3.h3_quantize_int8_rows(dtype, rows, K, x, K, codes, scales)
+    want = (x.double().abs().amax(1) / 127).float()
+    assert torch.equal(scales, want)
+    assert torch.equal(codes, (x.double() / want.double()[:, None]).round().to(torch.int8))
