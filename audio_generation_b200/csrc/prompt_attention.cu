@@ -544,7 +544,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float a0, a1, b0, b1;
       f2_unpack(f2_add(sum2[0], sum2[1]), a0, a1);
       f2_unpack(f2_add(sum2[2], sum2[3]), b0, b1);
-      l_run += (a0 + a1) + (b0 + b1);
+      // A NaN or an infinity among the tile's own scores makes weights NaN, or the
+      // largest number by the cubic; from here on the row's sum is NaN, whatever the
+      // running maximum does.
+      const float sum = (a0 + a1) + (b0 + b1);
+      l_run += sum < 1e37f ? sum : __int_as_float(0x7fc00000);
     }
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_final[i], rounds & 1, wc));
     if (!ok) break;
@@ -553,10 +557,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_fence_after();
     const int head = x.kvh * a.group + r - rp * a.group;
     const bool row_ok = rp < P && pos < x.len;
-    // A NaN or an infinity among the row's own scores makes its weights NaN, or the
-    // largest number by the cubic: the row is NaN then, and needs no other look.
-    const bool scores_ok = l_run < 1e37f;
-    const float inv_l = scores_ok ? 1.f / l_run : __int_as_float(0x7fc00000);
+    const bool scores_ok = l_run >= 0.f;  // else the row is NaN, and needs no other look
+    const float inv_l = 1.f / l_run;
     // A row's 64 bytes at a time; four lanes turn their pieces of 16 so that a
     // store covers 64 bytes of eight rows instead of 16 of 32.
     const long long mine = row_ok ? (x.start + pos) * a.o_stride + head * D : -1;

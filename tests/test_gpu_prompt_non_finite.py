@@ -81,6 +81,22 @@ def test_a_bad_token_in_a_long_prompt(which, at, most_ms):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("at", [8, 9, 10, 11, 12, 140, 150])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_key_before_scores_that_grow(bad, at, dtype):
+    """The running maximum moves by far more than 2^100 after it: its rows stay NaN,
+    by either form of the exponential."""
+    def grow(q, k, v):
+        q.fill_(1.0)
+        k.copy_((torch.arange(k.shape[0], device=DEV) / 8)[:, None, None].expand_as(k))
+        k[at, 0, 5] = bad
+    q, k, v, o, offsets, scale = _run([700], 4, 2, 64, dtype, prepare=grow)
+    nan = torch.zeros(700, 4, dtype=torch.bool, device=DEV)
+    nan[at:, :2] = True
+    assert torch.equal(torch.isnan(o).all(-1), nan) and torch.equal(torch.isfinite(o).all(-1), ~nan)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
 def test_keys_of_minus_infinity_weigh_nothing(dtype):
     """Scores of -inf, for a whole first tile of keys and for some later ones: weight
     0, and NaN only for rows that have no other score."""
