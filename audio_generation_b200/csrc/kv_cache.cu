@@ -712,8 +712,15 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
       m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const bool fine = m <= kMaxFinite;
-      // (a row below 1e-34 counts as zeros: its fixed-point factor would overflow)
-      const float inv = there && fine && m > 1e-34f ? kFixed / m : 0.f;
+      float up = 1.f;
+      if (m < 1e-30f) {  // so small that the fixed-point factor would overflow
+        up = 0x1p100f;
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[h][e] *= up;
+      }
+      const float inv = there && fine && m > 0.f ? kFixed / (m * up) : 0.f;
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -728,7 +735,7 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
           qh[h][w] = pack4(hi[0], hi[1], hi[2], hi[3]);
           ql[h][w] = pack4(lo[0], lo[1], lo[2], lo[3]);
         }
-      const float f = fine ? m * (a.scale_log2 / kFixed) : __int_as_float(0x7fc00000);
+      const float f = fine ? m * a.scale_log2 * (1.f / kFixed) : __int_as_float(0x7fc00000);
       mul[0] = __shfl_sync(0xffffffffu, f, 8 * t);
       mul[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }

@@ -86,3 +86,16 @@ def test_attention_of_queries_with_outlier_channels(D, BT, factor):
         off[s, :, 0] = q[s].double().abs().amax(-1) / 32512 / 2 * most * scale
     assert_within(o, ref, a * (2.0 ** -11 + 2.4e-4 + torch.expm1(2 * off))
                   + ref.abs() * STEP[BF] * 1.01 + 64 * TINY[BF])
+
+
+@pytest.mark.parametrize("e", [-124, -118, -100, -60, 60, 100, 120])
+def test_attention_of_queries_and_scales_at_the_ends_of_the_range(e):
+    """q times a power of two and the scale divided by it: the same bits, also where
+    one of them is near the end of float32."""
+    cache = Cache([333, 9], 1, 128, 64)
+    q = torch.rand(2, 4, 128, generator=gen(2), device=DEV) + 1  # in [1, 2): no bits are lost
+    q *= torch.randint(0, 2, q.shape, generator=gen(3), device=DEV) * 2 - 1
+    want = cache.attend(q.to(BF), 0.125)
+    got = cache.attend((q.to(BF).double() * 2.0 ** e).to(BF), 0.125 * 2.0 ** -e)
+    assert torch.equal(got, want)
+    assert h3.h3_text_error() == h3.H3_OK
