@@ -484,6 +484,9 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return a / b;
 }
 
+// 1 / l of a weights' sum (0 where there were no tokens), within 2^-22 of it.
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : __fdividef(1.f, l); }
+
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
 }
@@ -913,7 +916,7 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
       }
       m_all[k] = m;
       l_all[k] = l;
-      by[k] = l == 0.f ? 0.f : (m_run[k] == m ? 1.f : exp2_mufu(m_run[k] - m)) / l;
+      by[k] = (m_run[k] == m ? 1.f : exp2_mufu(m_run[k] - m)) * inverse(l);
     }
     // Divided by the weights' sum before the V scale comes in: an average of the
     // values is in float32's range wherever they are, a sum over the tokens may not be.
@@ -1017,6 +1020,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_cache_join(const AttnArgs a
     x[k] = part(slice + k * SLICES);
     ml[k] = a.stat[at(slice + k * SLICES)];
   }
+  float2 own = a.stat[at(lane)];  // a lane's part, for the maximum and the weights' sum
   const int n = cut.z, kvh = cut.y / a.row_groups, h0 = (cut.y - kvh * a.row_groups) * kRows;
   if (n == 0 || h0 + r >= a.group) return;  // with shared rows: the whole thread block
 #pragma unroll
@@ -1024,8 +1028,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_cache_join(const AttnArgs a
     const int i = slice + k * SLICES;
     if (i < n) x[k] = part(i), ml[k] = a.stat[at(i)];
   }
-  // the maximum and the weights' sum of all parts
-  const float2 own = lane < n ? a.stat[at(lane)] : make_float2(-INFINITY, 0.f);
+  if (lane >= n) own = make_float2(-INFINITY, 0.f);
   float m = own.x, l = 0.f;
   for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, a.stat[at(i)].x);
 #pragma unroll
@@ -1037,7 +1040,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_cache_join(const AttnArgs a
   for (int i = lane + 32; i < n; i += 32) l += weight(a.stat[at(i)]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = inverse(l);
   Piece sum = {};
   for (int i0 = slice; i0 < n; i0 += kAhead * SLICES) {
     if (i0 > slice) {
