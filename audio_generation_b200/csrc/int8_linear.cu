@@ -130,6 +130,12 @@ cudaError_t quantize(int rows, int K, const void* x, int64_t stride_vec, void* c
 
 // ------------------------------------------------------------- matrix product
 
+#ifdef H3_FAULT_INJECTION
+// Test-only build: the K step (of a CTA's, in the order of its fetches) whose copies
+// are not counted, so that the wait for it runs out (none where negative).
+static __device__ int g_fault_skip_step = -1;
+#endif
+
 constexpr int BM = 128;        // rows of a CTA's operand tile = TMEM lanes
 constexpr int BKB = 128;       // K bytes per stage: one 128-byte swizzled row
 constexpr int NUM_THREADS = 192;
@@ -348,6 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{err, abort_flag};
   auto at = [&](uint64_t* bar, uint32_t r) { return mapa_shared(smem_u32(bar), r); };
+  uint32_t fills = 0;  // thread 0's stages issued
 
   if (warp == 0) {
     if (lane == 0) {
@@ -363,16 +370,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             break;
           }
           uint8_t* sa = smem + s * STAGE;
+#ifdef H3_FAULT_INJECTION
+          if ((int)n != *(volatile int*)&g_fault_skip_step)
+#endif
           if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE);
           tma_load_2d_pair(sa, &tmA, at(&full[s], 0), kb * BKB, m0 + BM * rank);
           tma_load_2d_pair(sa + A_STAGE, &tmW, at(&full[s], 0), kb * BKB, n0 + (BN / 2) * rank);
           ++n;
         }
       }
-      if (!ok && leader) {  // let issued copies land before the CTA retires
-        const uint32_t first = n > PNST ? n - PNST : 0;
-        for (uint32_t i = first; i < n; ++i) mbar_drain(&full[i % PNST], (i / PNST) & 1);
-      }
+      fills = n;
     }
   } else if (warp == 1) {
     if (leader) {  // the whole warp runs the loop; one elected lane issues
@@ -489,6 +496,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
   }
   __syncthreads();
+  if (threadIdx.x == 0 && leader && *abort_flag) {  // both CTAs' issued copies land first
+    for (uint32_t i = fills > PNST ? fills - PNST : 0; i < fills; ++i)
+      mbar_drain(&full[i % PNST], (i / PNST) & 1);
+  }
   cluster_sync();  // no CTA leaves while the pair's MMAs or signals may still reach it
   if (warp == 1) {
     __syncwarp();
@@ -579,6 +590,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{err, abort_flag};
+  uint32_t fills = 0;  // thread 0's stages issued
 
   if (warp == 0) {
     if (lane == 0) {
@@ -592,15 +604,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             break;
           }
           uint8_t* sw = smem + s * STAGE;
+#ifdef H3_FAULT_INJECTION
+          if ((int)n != *(volatile int*)&g_fault_skip_step)
+#endif
           mbar_arrive_expect_tx(&full[s], STAGE);
           tma_load_2d(sw, &tmW, &full[s], kb * BKB, t / m_tiles * BM);
           tma_load_2d(sw + A_STAGE, &tmA, &full[s], kb * BKB, t % m_tiles * NT);
         }
       }
-      if (!ok) {  // let issued copies land before the CTA retires
-        const uint32_t first = n > NST ? n - NST : 0;
-        for (uint32_t i = first; i < n; ++i) mbar_drain(&full[i % NST], (i / NST) & 1);
-      }
+      fills = n;
     }
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_s8_s32(BM, NT);
@@ -763,6 +775,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     cluster_sync();  // no CTA leaves while another reads its sums
   } else {
     __syncthreads();
+  }
+  if (threadIdx.x == 0 && *abort_flag) {  // issued copies land before the CTA retires
+    for (uint32_t i = fills > NST ? fills - NST : 0; i < fills; ++i)
+      mbar_drain(&full[i % NST], (i / NST) & 1);
   }
   if (warp == 1) {
     __syncwarp();
@@ -968,3 +984,9 @@ cudaError_t launch_matmul_int8(int M, int N, int K, const void* a, const float* 
 }
 
 }  // namespace h3
+
+#ifdef H3_FAULT_INJECTION
+extern "C" __attribute__((visibility("default"))) int h3_test_int8_skip_step(int step) {
+  return cudaMemcpyToSymbol(h3::g_fault_skip_step, &step, sizeof(int)) == cudaSuccess ? 0 : -1;
+}
+#endif

@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kAttnThreads, Ring<D, BT>::PER_SM)
     // Copies land before the block retires, though the consumers may have given up
     // (else they have waited for every one, later than this).
     for (int j = max(0, issued - R::STAGES); lane == 0 && j < issued; ++j)
-      mbar_drain(&full[j % R::STAGES], (j / R::STAGES) & 1);
+      mbar_land(&full[j % R::STAGES], (j / R::STAGES) & 1);
     return;
   }
 

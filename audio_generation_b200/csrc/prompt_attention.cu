@@ -44,6 +44,12 @@
 namespace h3 {
 namespace {
 
+#ifdef H3_FAULT_INJECTION
+// Test-only build: the key tile (of a CTA's, in the order of its fetches) whose copies
+// are not counted, so that the wait for it runs out (none where negative).
+static __device__ int g_fault_skip_keys = -1;
+#endif
+
 constexpr int HALF = 128 * 64 * 2;  // 128 rows x 64 channels: 16 KB
 constexpr int NUM_THREADS = 384;
 // 2 * 128 * kSoftmaxRegs + 128 * kControlRegs must not exceed the 384 * 168
@@ -303,6 +309,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int j = 0; j < n; ++j) {
             int st = nk & 1;
             if (!mbar_wait(&bars->k_empty[st], ((nk >> 1) & 1) ^ 1, wc)) { ok = false; break; }
+#ifdef H3_FAULT_INJECTION
+            if (nk != *(volatile int*)&g_fault_skip_keys)
+#endif
             mbar_arrive_expect_tx(&bars->k_full[st], TILE);
             for (int h = 0; h < D / 64; ++h)
               tma_load_3d(smem + OFF_K + st * TILE + h * HALF, &tk, &bars->k_full[st], 64 * h,
@@ -326,14 +335,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ++nv;
           }
         }
-        if (!ok) {  // let issued copies land before the CTA retires
-          for (int i = 0; i < 2; ++i)
-            if (nq[i] > 0) mbar_drain(&bars->q_full[i], (nq[i] - 1) & 1);
-          for (int j = nk > 2 ? nk - 2 : 0; j < nk; ++j)
-            mbar_drain(&bars->k_full[j & 1], (j >> 1) & 1);
-          for (int j = nv > 2 ? nv - 2 : 0; j < nv; ++j)
-            mbar_drain(&bars->v_full[j & 1], (j >> 1) & 1);
-        }
+        // issued copies land before the CTA retires, whoever has given up
+        for (int i = 0; i < 2; ++i)
+          if (nq[i] > 0) mbar_land(&bars->q_full[i], (nq[i] - 1) & 1);
+        for (int j = nk > 2 ? nk - 2 : 0; j < nk; ++j)
+          mbar_land(&bars->k_full[j & 1], (j >> 1) & 1);
+        for (int j = nv > 2 ? nv - 2 : 0; j < nv; ++j)
+          mbar_land(&bars->v_full[j & 1], (j >> 1) & 1);
       }
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer
@@ -988,3 +996,9 @@ cudaError_t launch_prompt_attention(const h3_prompts* p, bool f16, const void* q
 }
 
 }  // namespace h3
+
+#ifdef H3_FAULT_INJECTION
+extern "C" __attribute__((visibility("default"))) int h3_test_prompt_skip_keys(int tile) {
+  return cudaMemcpyToSymbol(h3::g_fault_skip_keys, &tile, sizeof(int)) == cudaSuccess ? 0 : -1;
+}
+#endif

@@ -103,6 +103,12 @@ __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// The same for a producer's last copies in every launch: most have landed, which is
+// known without a look at the timer.
+__device__ __forceinline__ void mbar_land(uint64_t* bar, uint32_t parity) {
+  if (!mbar_test(bar, parity)) mbar_drain(bar, parity);
+}
+
 // ----------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {

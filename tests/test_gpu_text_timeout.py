@@ -55,3 +55,27 @@ def test_rows_computed_again_do_not_let_a_wait_run_out(child):
     assert res["status"] == h3.H3_OK and res["again"] == h3.H3_OK
     assert res["as_expected"] and res["diff"] < 6 * 2.0 ** -8 + 2 * 3 * 2.0 ** -8
     assert res["ms"] > 50
+
+
+def _check_skipped(res, again):
+    from audio_generation_b200 import h3
+    for n in (0, 1, 5):
+        assert res["skipped_%d" % n] == h3.H3_ERR_TIMEOUT, n
+    assert res["normal"] == h3.H3_OK
+    status, values = again()  # the product library on the same inputs: the same bits
+    assert status == h3.H3_OK and values == res["values"]
+
+
+def test_a_key_tile_that_does_not_come(child):
+    """Prompt attention: other fetches are in flight when the wait runs out."""
+    from audio_generation_b200 import h3
+    from tests.text_fault_child import prompts_case
+    _check_skipped(child("prompts"), prompts_case(h3))
+
+
+def test_a_step_of_a_product_that_does_not_come(child):
+    """Every form of the product of int8 codes, clusters that join their sums included."""
+    from audio_generation_b200 import h3
+    from tests.text_fault_child import SHAPES, products_case
+    for shape, res in zip(SHAPES, child("products")):
+        _check_skipped(res, products_case(h3, *shape))

@@ -77,11 +77,69 @@ def prompt(h3, lib):
             "again": h3.h3_text_error(), "diff": float(diff.max()), "ms": a.elapsed_time(b)}
 
 
+def bits(x):
+    return x.contiguous().view(-1).view(torch.int16).tolist()[::97]
+
+
+def prompts_case(h3):
+    QH, KH, D, lengths = 10, 2, 128, [900, 5, 700, 300]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    T = sum(lengths)
+    q, k, v = (torch.randn(T, n, D, generator=g, device="cuda").to(BF) for n in (QH, KH, KH))
+    offsets = [sum(lengths[:i]) for i in range(5)]
+    p = h3.h3_prompts_prepare(offsets, QH, KH, D)
+
+    def attend():
+        o = torch.zeros_like(q)
+        h3.h3_prompt_attention(p, BF, q, QH * D, k, KH * D, v, KH * D, 0.1, o, QH * D)
+        return h3.h3_text_error(), bits(o)
+    return attend
+
+
+def products_case(h3, M, N, K):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    a, w = (torch.randint(-127, 128, (n, K), generator=g, device="cuda", dtype=torch.int8)
+            for n in (M, N))
+    sa, sw = (torch.rand(n, generator=g, device="cuda") * 0.01 for n in (M, N))
+
+    def product():
+        out = torch.zeros(M, N, dtype=BF, device="cuda")
+        h3.h3_matmul_int8(M, N, K, a, sa, w, sw, BF, out, N)
+        return h3.h3_text_error(), bits(out)
+    return product
+
+
+# by pairs of CTAs; few rows, with and without a shared K axis; turned
+SHAPES = [(4000, 2048, 2048), (40, 40000, 2048), (16, 1024, 8192), (3000, 100, 8192)]
+
+
+def skipping(call, setter):
+    setter.restype, setter.argtypes = ctypes.c_int, [ctypes.c_int]
+    out = {}
+    for n in (0, 1, 5):
+        assert setter(n) == 0
+        out["skipped_%d" % n] = call()[0]
+    assert setter(-1) == 0
+    out["normal"], out["values"] = call()
+    return out
+
+
+def prompts(h3, lib):
+    return skipping(prompts_case(h3), lib.h3_test_prompt_skip_keys)
+
+
+def products(h3, lib):
+    return [skipping(products_case(h3, *s), lib.h3_test_int8_skip_step) for s in SHAPES]
+
+
 def main(lib_path: str, case: str) -> None:
     from audio_generation_b200 import h3
     h3.LIB_PATH = lib_path
     h3._lib = None
-    print("RESULT " + json.dumps({"cache": cache, "prompt": prompt}[case](h3, h3.lib())))
+    cases = {"cache": cache, "prompt": prompt, "prompts": prompts, "products": products}
+    print("RESULT " + json.dumps(cases[case](h3, h3.lib())))
 
 
 if __name__ == "__main__":
