@@ -285,8 +285,8 @@ __device__ __forceinline__ void turn_and_store(const Out& o, int64_t off, int64_
 // stages; the accumulator is double-buffered in TMEM, so the epilogue of a tile
 // overlaps the next tile's products. Warps: 0 TMA producer, 1 TMEM owner and
 // MMA issuer, 2..5 epilogue (one TMEM lane = one row per thread).
-// 8191 x 14336 x 5376: 368 us alone (3.4 P operations/s, the tensor pipe active in
-// 97 % of the cycles), 436 to 464 us in a loop, where the board's power cap holds
+// 8191 x 14336 x 5376: 372 us alone (3.4 P operations/s, the tensor pipe active in
+// 97 % of the cycles), 430 to 470 us in a loop, where the board's power cap holds
 // the clock down.
 constexpr int PNST = 6;
 template <int BN>
@@ -517,8 +517,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 // axis of one and add their integer sums through distributed shared memory,
 // each finishing a share of the tokens. Neighbouring lanes store neighbouring
 // columns of out. Warps as above; the accumulator is double-buffered.
-// 1 x 14336 x 5120: 14.8 us (73 MB: 5.0 TB/s, 3 to 4 us of it launch, fill and
-// tail); 48 x 32003 x 5120 with float32 out: 31.2 us (170 MB: 5.5 TB/s).
+// 1 x 14336 x 5120: 13.6 to 15 us (73 MB: 5 TB/s, 3 to 4 us of it launch, fill and
+// tail); 48 x 32003 x 5120 with float32 out: 32.0 us (170 MB: 5.3 TB/s).
 template <int NT>
 constexpr int s_stage() { return A_STAGE + NT * BKB; }
 template <int NT>

@@ -35,9 +35,9 @@ __device__ __forceinline__ int block_of(const int32_t* table, int width, int seq
 // stores run along the tokens. Where most pairs of a sequence and a block up to
 // max_new would be empty, a thread block finds its pair by a scan over the
 // sequences. 18400 tokens of 8 heads x 128 in 16 sequences (113 MB in and out):
-// 30.6 us (34 without the scan), six waves of one chain each (sequence, values, scale,
+// 29.0 us (34 without the scan), six waves of one chain each (sequence, values, scale,
 // codes); two thread blocks per SM 37 us, four, whose registers spill, 35 us. One
-// token of each of 48 sequences: 4.3 us.
+// token of each of 48 sequences: 4.5 us.
 // As many threads as a block has groups of four slots and eight channels (with 256
 // for all, 36000 tokens of 8 heads x 64, 32 per block: 73 us against 27).
 template <int D, int BT>
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kStoreThreads<D, BT>,
 // product is free, and the tokens are assigned to rows so that its V operand is
 // one contiguous piece of a transposed V row; the weights turn between the two
 // layouts by 8 x 8 transposes across the warp. 40 sequences of 500 to 24000 tokens,
-// 40 heads over 8 x 128 (423 MB): 75 us, 5.6 TB/s; one of 4001 tokens: 10.6 us.
+// 40 heads over 8 x 128 (423 MB): 75 us, 5.6 TB/s; one of 4001 tokens: 10.9 us.
 constexpr int kAttnThreads = 160, kConsumers = 4;
 constexpr int kRows = 8;        // query heads that share a pass over the cache
 constexpr int kListSize = 64;   // entries of the producer's list, two batches of 32

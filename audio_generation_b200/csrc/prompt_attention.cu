@@ -19,17 +19,18 @@
 // Where G does not divide 128 the last rows of a tile are idle.
 //
 // Work items (two tiles each, or one where that leaves no SM idle) come from the
-// prompts object, longest key range first. One CTA per SM takes them in turn (there and back over the list's
-// rounds, so that no CTA always gets the longer one), every role running on into
-// the next item: its first keys and its q are fetched and a query tile's first
+// prompts object, longest key range first. One CTA per SM takes them in turn (there
+// and back over the list's rounds, so that no CTA always gets the longer one), every
+// role running on into the next item: its first keys and its q are fetched and a query tile's first
 // scores computed right after the tile's last product of the item before, while
 // that is still being divided and stored. A q tile is given back after the item's
 // last score product with it, an O accumulator when its rows have been read.
 //
 // Bound by the softmax's chain: 1650 cycles per 128 x 128 tile against 1024 of tensor
-// work at D = 128. One prompt of 8192 tokens, 56 heads over 8 x 128: 900 us, 1070
-// TFLOP/s; 12 prompts of 120 to 2500 tokens, 40 over 8: 128 us. An item costs about
-// 4 us beyond its key tiles, from its first fetch to its last store.
+// work at D = 128. One prompt of 8192 tokens, 56 heads over 8 x 128: 810 us at full
+// clock (1190 TFLOP/s), 925 us in a loop of seconds, whose power cap brings the clock
+// to 1.63 GHz; 12 prompts of 120 to 2500 tokens, 40 over 8: 131 and 148 us. An item
+// costs about 4 us beyond its key tiles, from its first fetch to its last store.
 #include <cuda_fp16.h>
 
 #include <algorithm>

@@ -603,7 +603,7 @@ H3_API void h3_prompts_destroy(h3_prompts_t prompts);
  * (a sixth of them, the others 2^-22); the softmax weights are rounded to `type`
  * before the product with v, their sum is of the unrounded ones. What a row holds does not depend on the values of
  * rows it does not attend, infinities and NaN included, but for its last bits: rows
- * up to 128 tokens before an infinite or NaN v, or beside one of a neighbouring
+ * up to 255 tokens before an infinite or NaN v, or beside one of the following
  * prompt, are computed again with weights that are not rounded (at about 60 ns a
  * key, up to 32 rows one after another). Runs on the device of the prompts object,
  * which must be current (else H3_ERR_ARG). Enqueues. */
