@@ -643,8 +643,8 @@ typedef struct {
  * with earlier tokens grows, their codes are rounded again to the same values
  * under the new scale. A block of zeros has scale 0. An infinity or a NaN marks
  * its block and kv head: scale NaN, codes 0 (attention over it gives NaN).
- * max_new: the largest number of new tokens of one sequence; `rows`: the rows of
- * k and v. A sequence whose lengths or offsets are negative, whose new tokens are
+ * max_new: the largest number of new tokens of one sequence, or any larger number;
+ * `rows`: the rows of k and v. A sequence whose lengths or offsets are negative, whose new tokens are
  * more than max_new, leave `rows` or do not fit table_width blocks is not stored,
  * nor is a token whose table entry names no block: both record an error
  * (h3_text_error, H3_ERR_LAYOUT; where offsets decrease, parts of other sequences
@@ -668,10 +668,10 @@ H3_API h3_status h3_kv_cache_store(const h3_kv_cache* cache, int n_seq, int max_
  * H3_ERR_LAYOUT). ws: h3_cache_attention_workspace_size bytes (a few MB at most),
  * used only during the call's work: calls that overlap on the GPU need one each.
  * The result does not depend on the order in which the GPU runs things. What is held
- * in fewer than float32's bits: a row of q in 16-bit fixed point (each element off by
- * up to 2^-16 of the row's largest, and a score by that times sum |k|), the weights in
- * fp16, summed after rounding. Values are summed relative to the largest V scale of
- * the sequence and kv head, to about 2^-24 of its largest value. Enqueues. */
+ * in fewer than float32's bits: a row of q in 16-bit fixed point (an element is off
+ * by up to about 2^-16 of the row's largest, a score by that times sum |k|), the
+ * weights in fp16, summed after rounding. Values are summed relative to the largest
+ * V scale of the sequence and kv head, to about 2^-24 of its largest value. Enqueues. */
 H3_API size_t h3_cache_attention_workspace_size(const h3_kv_cache* cache, int n_seq, int q_heads,
                                                 int table_width);
 H3_API h3_status h3_cache_attention(const h3_kv_cache* cache, int n_seq, int q_heads,
